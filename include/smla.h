@@ -11,6 +11,15 @@
  *   smla_decode        the four steps above in one call (decode steps with
  *                      MTP draft tokens, and chunked prefill)
  *
+ * and the operators around it:
+ *
+ *   kvpack_append      new tokens' raw projections -> norm, position rotation,
+ *                      quantisation -> the pool (kvpack_store takes finished ones)
+ *   smla_query_prep    q_pe rotation; indexer queries -> norm, rotation, E4M3
+ *                      codes and head weights, as smla_index_scores takes them
+ *   smla_attend_dense  latent attention over the whole visible context (no
+ *                      selection), decode tokens and prefill chunks
+ *
  * Sources (cited by page title and section):
  *   [AgentX]  "vLLM、エージェント型ワークロード向け最適化技術「AgentX」を公開"
  *             (news.ainew.jp rendering of the vLLM AgentX post), sections
@@ -388,6 +397,121 @@ smla_status_t smla_dcp_topk_merge(const float* shard_scores, int64_t shard_strid
  */
 smla_status_t smla_lse_merge(const void* parts_out, const float* parts_lse, int n_shards, int n_tokens,
                              int n_heads, int d, void* out, float* lse, void* stream);
+
+/*
+ * Position rotation shared by kvpack_append and smla_query_prep.  The rotated
+ * vector x of d_rope dims is cut into d_rope / 2 pairs; pair i of a token at
+ * position p turns by the angle whose cosine and sine are cos_sin[p][i] and
+ * cos_sin[p][d_rope / 2 + i]:
+ *   (x_a, x_b) -> (x_a cos - x_b sin, x_a sin + x_b cos)
+ * in fp32.  Pair i is (2i, 2i + 1) when interleaved, else (i, i + d_rope / 2).
+ */
+typedef struct smla_rope {
+  const float* cos_sin;    /* device, fp32 [n_positions, d_rope], 4-byte aligned             */
+  int64_t n_positions;     /* rows of the table                                              */
+  int32_t interleaved;     /* pairs of the attention's rope dims (q_pe, rope key)            */
+  int32_t idx_interleaved; /* pairs of the indexer's rotated dims                            */
+  int32_t idx_rope;        /* 1: the first d_rope dims of indexer queries and keys rotate, 0: none */
+} smla_rope_t;
+
+/*
+ * kvpack_append -- kvpack_store for tokens straight from the projections: the
+ * latent's RMS norm, the rope key's rotation, and the indexer key's norm,
+ * rotation and quantisation happen on the way into the pool.
+ * [GLM-5.3 "How to try"]: the KV cache is FP8; the formulas are those of the
+ * store (per-tile amax / 448) after
+ *   y = latent * rsqrt(mean(latent^2) + eps) * latent_norm       (NULL: y = latent)
+ *   r = rotation of rope_key at positions[t]                      (rounded to bf16)
+ *   z = idx_k * rsqrt(mean(idx_k^2) + eps) * idx_norm             (idx_bias NULL)
+ *   z = (idx_k - mean) * rsqrt(var + eps) * idx_norm + idx_bias   (a layer norm)
+ *       (idx_norm NULL: z = idx_k), then its first d_rope dims rotated if rope->idx_rope
+ * all in fp32, y and z not rounded before they are quantised: scale = amax / F,
+ * code = round-to-nearest-even, saturating, of y * (F / amax), F = 448 (E4M3) or
+ * 6 (E2M1); amax below 2^-100 takes scale 1 and codes 0.
+ *   latent       bf16 [n_tokens, d_latent], rows latent_stride elements apart
+ *   rope_key     bf16 [n_tokens, d_rope], rows rope_stride elements apart
+ *   idx_k        bf16 [n_tokens, d_index], rows idx_k_stride elements apart; NULL
+ *                (a layer without an indexer): the key and its scale stay as they are
+ *   latent_norm  fp32 [d_latent] or NULL; idx_norm fp32 [d_index] or NULL;
+ *                idx_bias fp32 [d_index] or NULL (not without idx_norm)
+ *   rope         NULL: nothing rotates (positions may be NULL)
+ *   positions    int64 [n_tokens]
+ *   slot_mapping int64 [n_tokens], as kvpack_store: -1 = skip, a slot beyond the pool is
+ *                skipped and latched; a token whose position is outside the table is too
+ * Two tokens of one call must not share a slot.  Inputs must be finite.  The
+ * pool is 16-byte aligned, the inputs aligned to their element.  Built for the
+ * latents that kvpack_store takes (64, 128, 256 or 512), d_rope <= 64 and d_index
+ * of 32, 64, 128 or 256.
+ */
+smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, int layer, const void* latent,
+                            int64_t latent_stride, const void* rope_key, int64_t rope_stride, const void* idx_k,
+                            int64_t idx_k_stride, const float* latent_norm, const float* idx_norm,
+                            const float* idx_bias, float eps, const smla_rope_t* rope, const int64_t* positions,
+                            const int64_t* slot_mapping, int n_tokens, void* stream);
+
+/*
+ * smla_query_prep -- the queries of a step from their projections, in one pass:
+ *   q_pe_out[t, h]  = rotation of q_pe[t, h] at positions[t], rounded to bf16
+ *   z = q_idx[t, h] * rsqrt(mean(q_idx[t, h]^2) + eps) * idx_norm   (NULL: z = q_idx),
+ *       then its first d_rope dims rotated if rope->idx_rope, in fp32
+ *   s = amax(z) / 448 (1 when amax < 2^-100)
+ *   q_idx_out[t, h] = E4M3 round-to-nearest-even, saturating, of z * (448 / amax)
+ *   w_out[t, h]     = w[t, h] * w_scale * s
+ * [AgentX "DeepSeek V4"]: 64 indexer heads a token.  s > 0, so the scale moves
+ * out of the ReLU into the head weight: smla_index_scores of q_idx_out and w_out
+ * is the score of the unquantised queries up to the rounding of their codes.
+ *   q_pe      bf16 [n_tokens, n_heads, d_rope]: element strides of a token and a head are
+ *             given, so that it may be a slice of a wider projection; NULL: only the indexer's
+ *   q_pe_out  bf16 [n_tokens, n_heads, d_rope] contiguous (the q_pe of the attention calls);
+ *             it does not overlap q_pe
+ *   q_idx     bf16 [n_tokens, n_idx_heads, d_index] with strides; NULL: only q_pe
+ *   idx_norm  fp32 [d_index] or NULL;  w fp32 [n_tokens, n_idx_heads]
+ *   q_idx_out uint8 [n_tokens, n_idx_heads, d_index], w_out fp32 [n_tokens, n_idx_heads]
+ *   rope      NULL: nothing rotates (q_pe is copied)
+ * A token whose position is outside the table latches SMLA_ERR_BAD_INDEX and its outputs
+ * are left as they were.  Built for d_rope <= 64 and d_index of 32, 64, 128 or 256.
+ */
+smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* params, const smla_rope_t* rope,
+                              const int64_t* positions, const void* q_pe, int64_t q_pe_token_stride,
+                              int64_t q_pe_head_stride, void* q_pe_out, const void* q_idx,
+                              int64_t q_idx_token_stride, int64_t q_idx_head_stride, const float* idx_norm, float eps,
+                              const float* w, float w_scale, uint8_t* q_idx_out, float* w_out, int n_tokens,
+                              void* stream);
+
+/*
+ * smla_attend_dense -- latent MQA attention of every query token over its whole
+ * visible context 0..p(t), without a selection: dense layers, contexts shorter
+ * than a selection is worth, the yardstick of a selection.  [GLM-5.3 "How to try"]:
+ * a prompt inside the top-k takes the sparse kernel with every position
+ * selected; this call gives the same result for any length.
+ *   out[t, h] = sum_{j <= p(t)} softmax_j(softmax_scale * (q[t, h] . K[j] + q_pe[t, h] . kpe[j])) K[j]
+ *   lse[t, h] = ln sum_{j <= p(t)} exp(softmax_scale * (...))
+ * for decode steps (with MTP drafts) and prefill chunks alike; a token that sees
+ * nothing (seq_lens[b] below its query tokens, e.g. a context shard that holds
+ * none of its positions) gets out = 0 and lse = -inf.
+ *   params     n_heads (<= 128) and softmax_scale are used
+ *   q          bf16 [n_tokens, n_heads, d_latent], q_pe bf16 [n_tokens, n_heads, d_rope]
+ *   out        bf16 [n_tokens, n_heads, d_latent], 16-byte aligned; rows from
+ *              query_start_loc[batch] on are left as they were
+ *   lse        fp32 [n_tokens, n_heads] or NULL
+ *   workspace  optional (NULL and 0): with smla_attend_dense_workspace_size() bytes,
+ *              16-byte aligned, long contexts are split evenly over the SMs and the parts
+ *              merged by their lse, without it each group of query tokens stays on one pair
+ *              of SMs.  Its contents need not be kept; calls that may overlap need one each.
+ * seq_lens, query_start_loc and block_table are read on the device: block ids outside the
+ * pool read as zeros and positions past the block-table row are not visited (both latch
+ * SMLA_ERR_BAD_INDEX).  query_start_loc is trusted to increase from 0 to at most n_tokens.
+ * Memory past a sequence's length is never used, whatever it holds.
+ * The pool is 16-byte aligned.
+ */
+smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t* params, const void* pool, int layer,
+                                const void* q, const void* q_pe, const int32_t* block_table, int bt_stride,
+                                const int32_t* seq_lens, const int32_t* query_start_loc, int batch, int n_tokens,
+                                void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch bytes with which smla_attend_dense splits contexts over the SMs (partial outputs of two
+ * ranges per pair of SMs); 0 for shapes and sizes that do not split. */
+size_t smla_attend_dense_workspace_size(const smla_layout_t* layout, const smla_params_t* params, int n_tokens);
 
 /* Self-check of the on-device wait bound and of the pipelined kernels' exit
  * protocol.  One CTA of four warps: warp 0 waits on an mbarrier that no thread

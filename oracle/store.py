@@ -71,7 +71,7 @@ def kvpack_store(layout: PoolLayout, pool: np.ndarray, layer: int, latent_bits, 
     rec = _offsets(layout, slots, layer, "record")[:, None]
     pool[rec + np.arange(d_l)] = codes
     pool[rec + d_l + np.arange(4 * n_s)] = np.ascontiguousarray(scales).view(np.uint8).reshape(-1, 4 * n_s)
-    pool[rec + d_l + 4 * n_s + np.arange(2 * d_r)] = rope.view(np.uint8).reshape(-1, 2 * d_r)
+    pool[rec + d_l + 4 * n_s + np.arange(2 * d_r)] = rope.view(np.uint8).reshape(slots.size, 2 * d_r)
     key = _offsets(layout, slots, layer, "key")[:, None]
     pool[key + np.arange(d_i)] = idx_k
     sc = _offsets(layout, slots, layer, "scale")[:, None]
@@ -86,8 +86,8 @@ def read_record(layout: PoolLayout, pool: np.ndarray, layer: int, slots):
     scales = np.ascontiguousarray(pool[rec + d_l + np.arange(4 * n_s)]).view(np.float32)
     vals = e4m3_decode(codes).reshape(-1, n_s, layout.quant_tile) * scales.astype(np.float64)[:, :, None]
     lat = vals.reshape(-1, d_l).astype(np.float32).astype(np.float64)   # fp32(decode(code) * scale)
-    rope_bits = np.ascontiguousarray(pool[rec + d_l + 4 * n_s + np.arange(2 * d_r)]).view(np.uint16)
-    return lat, bf16_bits_to_f64(rope_bits)
+    rope_bits = np.ascontiguousarray(pool[rec + d_l + 4 * n_s + np.arange(2 * d_r)]).reshape(-1).view(np.uint16)
+    return lat, bf16_bits_to_f64(rope_bits.reshape(-1, d_r) if d_r else np.zeros((lat.shape[0], 0), np.uint16))
 
 
 def read_index_key(layout: PoolLayout, pool: np.ndarray, layer: int, slots):

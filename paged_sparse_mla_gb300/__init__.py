@@ -21,7 +21,8 @@ __all__ = [
     "smla_index_scores", "smla_topk", "smla_attend", "smla_decode", "smla_get_last_error",
     "status_string", "version", "EXPORTED_SYMBOLS", "smla_decode_static", "smla_prefill_chunk",
     "smla_dcp_topk_merge", "smla_lse_merge", "smla_attend_hisparse", "smla_selftest_wait",
-    "attend_workspace_size", "topk_workspace_size",
+    "attend_workspace_size", "topk_workspace_size", "Rope", "make_rope", "kvpack_append", "smla_query_prep",
+    "smla_attend_dense", "attend_dense_workspace_size",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -29,6 +30,7 @@ EXPORTED_SYMBOLS = (
     "smla_attend", "smla_decode", "smla_get_last_error", "smla_status_string", "smla_version",
     "smla_decode_static", "smla_prefill_chunk", "smla_dcp_topk_merge", "smla_lse_merge", "smla_attend_hisparse",
     "smla_selftest_wait", "smla_attend_workspace_size", "smla_topk_workspace_size", "smla_layout_init_keys",
+    "kvpack_append", "smla_query_prep", "smla_attend_dense", "smla_attend_dense_workspace_size",
 )
 
 KEY_FORMATS = {"e4m3": 0, "e2m1": 1}  # smla_key_format_t
@@ -70,6 +72,12 @@ class Params(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float)]
 
 
+class Rope(ctypes.Structure):
+    """Mirror of smla_rope_t (made by make_rope, which keeps the table alive in ``table``)."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_int64), ("interleaved", ctypes.c_int32),
+                ("idx_interleaved", ctypes.c_int32), ("idx_rope", ctypes.c_int32)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -83,7 +91,8 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(build_lib.LIB):
             raise RuntimeError(f"libsmla.so not built ({build_lib.LIB}); run paged_sparse_mla_gb300.build_lib.build()")
         L = ctypes.CDLL(build_lib.LIB)
-        LP, PP = ctypes.POINTER(Layout), ctypes.POINTER(Params)
+        LP, PP, RP = ctypes.POINTER(Layout), ctypes.POINTER(Params), ctypes.POINTER(Rope)
+        _F = ctypes.c_float
         sig = {
             "smla_layout_init": (_I, [LP, _I, _I, _I, _I, _I, _I, _I64]),
             "smla_layout_init_keys": (_I, [LP, _I, _I, _I, _I, _I, _I, _I, _I64]),
@@ -103,6 +112,12 @@ def lib() -> ctypes.CDLL:
             "smla_dcp_topk_merge": (_I, [_P, _I64, _I64, _P, _I, _I, _I, _P, _P, _P]),
             "smla_attend_hisparse": (_I, [LP, PP, _P, _I, _P, _P, _I64, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P]),
             "smla_lse_merge": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P]),
+            "kvpack_append": (_I, [LP, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _F, RP, _P, _P, _I, _P]),
+            "smla_query_prep": (_I, [LP, PP, RP, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _F, _P, _F, _P, _P, _I,
+                                     _P]),
+            "smla_attend_dense": (_I, [LP, PP, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, ctypes.c_size_t,
+                                       _P]),
+            "smla_attend_dense_workspace_size": (ctypes.c_size_t, [LP, PP, _I]),
             "smla_selftest_wait": (_I, [_I64, _P]),
             "smla_get_last_error": (_I, [_P]),
             "smla_status_string": (ctypes.c_char_p, [_I]),
@@ -400,6 +415,117 @@ def smla_lse_merge(parts_out, parts_lse, out, lse, stream=None):
     _need(lse, torch.float32, "lse", t * h)
     _check(lib().smla_lse_merge(_ptr(parts_out), _ptr(parts_lse), n, t, h, d, _ptr(out), _ptr(lse), _stream(stream)),
            "smla_lse_merge")
+
+
+def make_rope(cos_sin, interleaved, idx_interleaved=False, idx_rope=True) -> Rope:
+    """Rotation table of kvpack_append and smla_query_prep: cos_sin fp32 [n_positions, d_rope], cosines
+    of a position's d_rope / 2 angles, then their sines."""
+    _need(cos_sin, torch.float32, "cos_sin", dims=2)
+    if not cos_sin.is_contiguous():
+        raise ValueError("cos_sin: a contiguous table expected")
+    rope = Rope(cos_sin.data_ptr(), cos_sin.shape[0], int(interleaved), int(idx_interleaved), int(idx_rope))
+    rope.table = cos_sin
+    return rope
+
+
+def _need_rope(layout, rope, positions, n):
+    """The rotation's table fits the layout and lies with the other tensors; a position per token."""
+    if rope is None:
+        return
+    if rope.table.shape[1] != layout.d_rope:
+        raise ValueError(f"cos_sin: rows of d_rope = {layout.d_rope} expected, got shape {tuple(rope.table.shape)}")
+    if positions is None:
+        raise ValueError("positions: needed with a rotation")
+    _need(positions, torch.int64, "positions", n)
+    _ptr(rope.table)
+
+
+def _rows(t, dtype, name, shape):
+    """(pointer, element strides of the leading axes) of a tensor whose last axis is contiguous and whose
+    shape is exactly `shape`; its leading axes may have any stride.  None passes as (None, zeros)."""
+    if t is None:
+        return None, (0,) * (len(shape) - 1)
+    _expect(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: its last axis has to be contiguous, got strides {t.stride()}")
+    if not t.is_cuda:
+        raise ValueError("libsmla takes CUDA tensors only")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), t.stride()[:-1]
+
+
+def kvpack_append(layout, pool, layer, latent, rope_key, idx_k, rope, positions, slot_mapping, latent_norm=None,
+                  idx_norm=None, idx_bias=None, eps=1e-6, stream=None):
+    """Norm, rotate, quantise and store new tokens.  latent [n, d_latent], rope_key [n, d_rope] and idx_k
+    [n, d_index] (or None) are bf16 with contiguous rows any distance apart; rope is a Rope or None."""
+    _expect(slot_mapping, torch.int64, "slot_mapping")
+    n = slot_mapping.numel()
+    _need(pool, torch.uint8, "pool", layout.pool_bytes)
+    _need(latent_norm, torch.float32, "latent_norm", layout.d_latent)
+    _need(idx_norm, torch.float32, "idx_norm", layout.d_index)
+    _need(idx_bias, torch.float32, "idx_bias", layout.d_index)
+    _need_rope(layout, rope, positions, n)
+    lat, (lat_s,) = _rows(latent, torch.bfloat16, "latent", (n, layout.d_latent))
+    rk, (rk_s,) = _rows(rope_key if layout.d_rope else None, torch.bfloat16, "rope_key", (n, layout.d_rope))
+    ik, (ik_s,) = _rows(idx_k, torch.bfloat16, "idx_k", (n, layout.d_index))
+    _check(lib().kvpack_append(ctypes.byref(layout), _ptr(pool), layer, lat, lat_s, rk, rk_s, ik, ik_s,
+                               _ptr(latent_norm), _ptr(idx_norm), _ptr(idx_bias), eps,
+                               None if rope is None else ctypes.byref(rope), _ptr(positions), _ptr(slot_mapping), n,
+                               _stream(stream)), "kvpack_append")
+
+
+def smla_query_prep(layout, params, rope, positions, q_pe=None, q_pe_out=None, q_idx=None, w=None, w_scale=1.0,
+                    q_idx_out=None, w_out=None, idx_norm=None, eps=1e-6, stream=None):
+    """Rotate q_pe [T, n_heads, d_rope]; norm, rotate and quantise q_idx [T, n_idx_heads, d_index] and fold
+    each head's scale into w [T, n_idx_heads].  Either may be None; both may be slices of wider tensors."""
+    if q_pe is None and q_idx is None:
+        raise ValueError("smla_query_prep: needs q_pe or q_idx")
+    n = (q_idx if q_pe is None else q_pe).shape[0]
+    H, HI = params.n_heads, params.n_idx_heads
+    _need_rope(layout, rope, positions, n)
+    pe, (pe_t, pe_h) = _rows(q_pe, torch.bfloat16, "q_pe", (n, H, layout.d_rope))
+    ix, (ix_t, ix_h) = _rows(q_idx, torch.bfloat16, "q_idx", (n, HI, layout.d_index))
+    if q_pe is not None:
+        if q_pe_out is None:
+            raise ValueError("q_pe_out: needed with q_pe")
+        _need(q_pe_out, torch.bfloat16, "q_pe_out", n * H * layout.d_rope)
+    if q_idx is not None:
+        if w is None or q_idx_out is None or w_out is None:
+            raise ValueError("w, q_idx_out and w_out: needed with q_idx")
+        _need(w, torch.float32, "w", n * HI)
+        _need(q_idx_out, torch.uint8, "q_idx_out", n * HI * layout.d_index)
+        _need(w_out, torch.float32, "w_out", n * HI)
+    _need(idx_norm, torch.float32, "idx_norm", layout.d_index)
+    _check(lib().smla_query_prep(ctypes.byref(layout), ctypes.byref(params),
+                                 None if rope is None else ctypes.byref(rope), _ptr(positions), pe, pe_t, pe_h,
+                                 _ptr(q_pe_out), ix, ix_t, ix_h, _ptr(idx_norm), eps, _ptr(w), w_scale,
+                                 _ptr(q_idx_out), _ptr(w_out), n, _stream(stream)), "smla_query_prep")
+
+
+def attend_dense_workspace_size(layout, params, n_tokens) -> int:
+    return int(lib().smla_attend_dense_workspace_size(ctypes.byref(layout), ctypes.byref(params), n_tokens))
+
+
+def smla_attend_dense(layout, params, pool, layer, q, q_pe, block_table, seq_lens, query_start_loc, out, lse=None,
+                      workspace=None, stream=None):
+    """Latent attention over the whole visible context.  `lse` is optional; `workspace` (uint8 device tensor
+    of at least attend_dense_workspace_size(...) bytes, optional) lets long contexts split over the SMs."""
+    T, H = q.shape[0], params.n_heads
+    _need(pool, torch.uint8, "pool", layout.pool_bytes)
+    _need(q, torch.bfloat16, "q", T * H * layout.d_latent)
+    _need(q_pe, torch.bfloat16, "q_pe", T * H * layout.d_rope)
+    _need_geometry(block_table, seq_lens, query_start_loc, seq_lens.numel())
+    _need(out, torch.bfloat16, "out", T * H * layout.d_latent)
+    _need(lse, torch.float32, "lse", T * H)
+    _need(workspace, torch.uint8, "workspace")
+    _check(lib().smla_attend_dense(ctypes.byref(layout), ctypes.byref(params), _ptr(pool), layer, _ptr(q), _ptr(q_pe),
+                                   _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
+                                   seq_lens.numel(), T, _ptr(out), _ptr(lse), _ptr(workspace),
+                                   0 if workspace is None else workspace.numel(), _stream(stream)),
+           "smla_attend_dense")
 
 
 def smla_selftest_wait(limit_ns, stream=None):

@@ -1,0 +1,469 @@
+// kvpack_append and smla_query_prep: from a layer's projections to the cache and to the queries.
+//
+// [GLM-5.3 "How to try", "Config and numbers"]: the KV cache is FP8.  [AgentX "Hybrid KV cache
+// management"]: one packed allocation per block holds every cache group.  [AgentX "DeepSeek V4"]: 64
+// indexer heads a token.
+//
+// Norm, position rotation, quantisation and the scatter (or the head weight) are one pass: a row is
+// read once as bf16, kept in fp32 registers (in shared memory only where a rotation pairs elements of
+// different lanes) and leaves as codes.  The normalised values are not rounded to bf16 before they are
+// quantised: that rounding (2^-9) would only add to the code's (2^-4).
+#include <cuda_fp4.h>
+
+#include "smla_internal.h"
+
+namespace smla {
+namespace {
+
+constexpr int kWarps = 8;             // warps per CTA
+constexpr int kMaxIndex = 256;        // largest d_index
+constexpr float kTinyAmax = 7.888609052210118e-31f;  // 2^-100: below it 448 / amax would near fp32's end
+
+struct RopeArgs {
+  const float* cos_sin;  // nullptr: nothing rotates
+  int64_t n_positions;
+  const int64_t* positions;
+  int d_rope, interleaved, idx_interleaved, idx_rope;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// N consecutive bf16 values; `vec`: the address is a multiple of min(16, 2 N) bytes.
+template <int N>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, bool vec, float (&x)[N]) {
+  if constexpr (N % 8 == 0) {
+    if (vec) {
+#pragma unroll
+      for (int v = 0; v < N / 8; ++v) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + v);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          x[8 * v + 2 * q] = __uint_as_float(ws[q] << 16);
+          x[8 * v + 2 * q + 1] = __uint_as_float(ws[q] & 0xFFFF0000u);
+        }
+      }
+      return;
+    }
+  } else if constexpr (N == 4) {
+    if (vec) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+      x[0] = __uint_as_float(w.x << 16);
+      x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      x[2] = __uint_as_float(w.y << 16);
+      x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __bfloat162float(p[i]);
+}
+
+// amax -> (scale, its reciprocal) for codes of largest magnitude `top`.
+__device__ __forceinline__ void quant_scale(float amax, float top, float& scale, float& inv) {
+  const bool tiny = amax < kTinyAmax;
+  scale = tiny ? 1.0f : amax / top;
+  inv = tiny ? 1.0f : top / amax;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Element pairs of a rotation: the pair of element i, and whether i is its first one.
+__device__ __forceinline__ void rope_pair(int i, int half, int interleaved, int& pair, int& other, bool& first) {
+  if (interleaved) {
+    pair = i >> 1;
+    other = i ^ 1;
+    first = (i & 1) == 0;
+  } else {
+    first = i < half;
+    pair = first ? i : i - half;
+    other = first ? i + half : i - half;
+  }
+}
+
+// Rotates the first d_rope of the row's 32 * EK values (lane l holds elements EK l .. EK l + EK - 1)
+// through `stage`, a row of floats of this warp.
+template <int EK>
+__device__ __forceinline__ void rotate_row(float (&z)[EK], const float* cs, int d_rope, int interleaved, float* stage,
+                                           int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < EK; ++i) stage[lane * EK + i] = z[i];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < EK; ++i) {
+    const int e = lane * EK + i;
+    if (e < d_rope) {
+      int pair, other;
+      bool first;
+      rope_pair(e, d_rope / 2, interleaved, pair, other, first);
+      const float c = __ldg(cs + pair), s = __ldg(cs + d_rope / 2 + pair), o = stage[other];
+      z[i] = first ? z[i] * c - o * s : o * s + z[i] * c;
+    }
+  }
+}
+
+struct AppendArgs {
+  KernelLayout L;
+  uint8_t* pool;
+  int layer;
+  const __nv_bfloat16 *latent, *rope_key, *idx_k;
+  int64_t latent_stride, rope_stride, idx_stride;
+  const float *latent_norm, *idx_norm, *idx_bias;
+  float eps;
+  RopeArgs rope;
+  const int64_t* slots;
+  int n_tokens;
+  bool vec_latent, vec_idx;
+  unsigned* err;
+};
+
+// One warp per token: lane l owns latent elements [E l, E l + E) and key elements [EK l, EK l + EK).
+template <int E, int EK>
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A) {
+  __shared__ float stage[kWarps][32 * EK];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + warp;
+  if (t >= A.n_tokens) return;
+  const KernelLayout& L = A.L;
+  const int64_t slot = __ldg(A.slots + t);
+  const int64_t pos = A.rope.cos_sin ? __ldg(A.rope.positions + t) : 0;
+  float x[E];
+  load_bf16<E>(A.latent + t * A.latent_stride + lane * E, A.vec_latent, x);
+  float z[EK];
+  if (A.idx_k) load_bf16<EK>(A.idx_k + t * A.idx_stride + lane * EK, A.vec_idx, z);
+  const int half = L.d_rope / 2;
+  int ra = lane, rb = lane + half;
+  if (A.rope.interleaved) {
+    ra = 2 * lane;
+    rb = 2 * lane + 1;
+  }
+  float r0 = 0.f, r1 = 0.f;
+  if (lane < half) {
+    r0 = __bfloat162float(A.rope_key[t * A.rope_stride + ra]);
+    r1 = __bfloat162float(A.rope_key[t * A.rope_stride + rb]);
+  }
+  if (slot < 0) return;
+  if (slot >= L.num_blocks * L.block_size || (A.rope.cos_sin && (pos < 0 || pos >= A.rope.n_positions))) {
+    if (lane == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
+    return;
+  }
+  const int64_t blk = slot / L.block_size;
+  const int off = static_cast<int>(slot - blk * L.block_size);
+  uint8_t* base = A.pool + blk * L.block_stride + static_cast<int64_t>(A.layer) * L.layer_stride;
+  uint8_t* rec = base + L.rec_off + static_cast<int64_t>(off) * L.rec_stride;
+  const float* cs = A.rope.cos_sin ? A.rope.cos_sin + pos * L.d_rope : nullptr;
+
+  // ---- rope key ----
+  if (lane < half) {
+    if (cs) {
+      const float c = __ldg(cs + lane), s = __ldg(cs + half + lane);
+      const float y0 = r0 * c - r1 * s;
+      r1 = r0 * s + r1 * c;
+      r0 = y0;
+    }
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(rec + L.d_latent + 4 * L.n_scales);
+    dst[ra] = __float2bfloat16_rn(r0);
+    dst[rb] = __float2bfloat16_rn(r1);
+  }
+
+  // ---- latent: norm, per-tile scale, codes ----
+  if (A.latent_norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss += x[i] * x[i];
+    const float rstd = rsqrtf(warp_sum(ss) / static_cast<float>(32 * E) + A.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = x[i] * rstd * __ldg(A.latent_norm + lane * E + i);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  const int lanes_per_tile = L.quant_tile / E;
+  for (int m = 1; m < lanes_per_tile; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  float scale, inv;
+  quant_scale(amax, 448.0f, scale, inv);
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    const uint32_t w = e4m3x2(x[i] * inv, x[i + 1] * inv);
+    reinterpret_cast<uint16_t*>(rec + lane * E)[i / 2] = static_cast<uint16_t>(w);
+  }
+  if ((lane * E) % L.quant_tile == 0) reinterpret_cast<float*>(rec + L.d_latent)[(lane * E) / L.quant_tile] = scale;
+
+  // ---- indexer key ----
+  if (A.idx_k == nullptr) return;
+  constexpr float kN = 32 * EK;
+  if (A.idx_norm) {
+    float mean = 0.f;
+    if (A.idx_bias) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < EK; ++i) sum += z[i];
+      mean = warp_sum(sum) / kN;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < EK; ++i) {
+      z[i] -= mean;
+      ss += z[i] * z[i];
+    }
+    const float rstd = rsqrtf(warp_sum(ss) / kN + A.eps);
+#pragma unroll
+    for (int i = 0; i < EK; ++i) {
+      z[i] = z[i] * rstd * __ldg(A.idx_norm + lane * EK + i);
+      if (A.idx_bias) z[i] += __ldg(A.idx_bias + lane * EK + i);
+    }
+  }
+  if (cs && A.rope.idx_rope) rotate_row<EK>(z, cs, L.d_rope, A.rope.idx_interleaved, stage[warp], lane);
+  float kmax = 0.f;
+#pragma unroll
+  for (int i = 0; i < EK; ++i) kmax = fmaxf(kmax, fabsf(z[i]));
+  float kscale, kinv;
+  const bool fp4 = L.key_format == SMLA_KEY_E2M1;
+  quant_scale(warp_max(kmax), fp4 ? 6.0f : 448.0f, kscale, kinv);
+  uint8_t* kdst = base + L.idx_key_off + static_cast<int64_t>(off) * L.key_bytes;
+  if (fp4) {
+    if constexpr (EK == 1) {
+      const float hi = __shfl_down_sync(0xffffffffu, z[0], 1);
+      if ((lane & 1) == 0)
+        kdst[lane / 2] = __nv_cvt_float2_to_fp4x2(make_float2(z[0] * kinv, hi * kinv), __NV_E2M1, cudaRoundNearest);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EK; i += 2)
+        kdst[(lane * EK + i) / 2] =
+            __nv_cvt_float2_to_fp4x2(make_float2(z[i] * kinv, z[i + 1] * kinv), __NV_E2M1, cudaRoundNearest);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EK; ++i)
+      kdst[lane * EK + i] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(z[i] * kinv, __NV_SATFINITE, __NV_E4M3));
+  }
+  if (lane == 0) reinterpret_cast<float*>(base + L.idx_scale_off)[off] = kscale;
+}
+
+struct QueryArgs {
+  const __nv_bfloat16 *q_pe, *q_idx;
+  int64_t pe_token, pe_head, idx_token, idx_head;
+  __nv_bfloat16* q_pe_out;
+  const float *idx_norm, *w;
+  float eps, w_scale;
+  uint8_t* codes;
+  float* w_out;
+  int n_tokens, n_heads, n_idx_heads, d_rope, d_index;
+  RopeArgs rope;
+  bool vec_idx;
+  unsigned* err;
+};
+
+// One warp per row: rows [0, n_idx_heads) of a token are its indexer heads, the next n_heads its q_pe.
+template <int EK>
+__global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryArgs A) {
+  __shared__ float stage[kWarps][32 * EK];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hi = A.q_idx ? A.n_idx_heads : 0, rows = hi + (A.q_pe ? A.n_heads : 0);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  const int64_t t = row / rows;
+  const int h = static_cast<int>(row - t * rows);
+  if (t >= A.n_tokens) return;
+  const float* cs = nullptr;
+  if (A.rope.cos_sin) {
+    const int64_t pos = __ldg(A.rope.positions + t);
+    if (pos < 0 || pos >= A.rope.n_positions) {
+      if (lane == 0 && h == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
+      return;
+    }
+    cs = A.rope.cos_sin + pos * A.d_rope;
+  }
+  const int half = A.d_rope / 2;
+  if (h >= hi) {
+    if (lane >= half) return;
+    const int head = h - hi;
+    const int a = A.rope.interleaved ? 2 * lane : lane, b = A.rope.interleaved ? 2 * lane + 1 : lane + half;
+    const __nv_bfloat16* src = A.q_pe + t * A.pe_token + head * A.pe_head;
+    float x0 = __bfloat162float(src[a]), x1 = __bfloat162float(src[b]);
+    if (cs) {
+      const float c = __ldg(cs + lane), s = __ldg(cs + half + lane);
+      const float y0 = x0 * c - x1 * s;
+      x1 = x0 * s + x1 * c;
+      x0 = y0;
+    }
+    __nv_bfloat16* dst = A.q_pe_out + (t * A.n_heads + head) * A.d_rope;
+    dst[a] = __float2bfloat16_rn(x0);
+    dst[b] = __float2bfloat16_rn(x1);
+    return;
+  }
+  float z[EK];
+  load_bf16<EK>(A.q_idx + t * A.idx_token + h * A.idx_head + lane * EK, A.vec_idx, z);
+  if (A.idx_norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < EK; ++i) ss += z[i] * z[i];
+    const float rstd = rsqrtf(warp_sum(ss) / static_cast<float>(32 * EK) + A.eps);
+#pragma unroll
+    for (int i = 0; i < EK; ++i) z[i] = z[i] * rstd * __ldg(A.idx_norm + lane * EK + i);
+  }
+  if (cs && A.rope.idx_rope) rotate_row<EK>(z, cs, A.d_rope, A.rope.idx_interleaved, stage[warp], lane);
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < EK; ++i) amax = fmaxf(amax, fabsf(z[i]));
+  float scale, inv;
+  quant_scale(warp_max(amax), 448.0f, scale, inv);
+  uint8_t* dst = A.codes + (t * A.n_idx_heads + h) * A.d_index + lane * EK;
+#pragma unroll
+  for (int i = 0; i < EK; ++i) dst[i] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(z[i] * inv, __NV_SATFINITE, __NV_E4M3));
+  if (lane == 0) A.w_out[t * A.n_idx_heads + h] = __ldg(A.w + t * A.n_idx_heads + h) * A.w_scale * scale;
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// SMLA_ERR_INVALID_ARG for a rotation that cannot be applied to these dims.
+smla_status_t check_rope(const smla_rope_t* rope, const int64_t* positions, int d_rope, int d_index, bool indexer) {
+  if (rope == nullptr) return SMLA_OK;
+  if (!rope->cos_sin || !aligned(rope->cos_sin, 4) || rope->n_positions <= 0 || !positions) return SMLA_ERR_INVALID_ARG;
+  if (indexer && rope->idx_rope && d_rope > d_index) return SMLA_ERR_INVALID_ARG;
+  return SMLA_OK;
+}
+
+RopeArgs rope_args(const smla_rope_t* rope, const int64_t* positions, int d_rope) {
+  RopeArgs r{};
+  r.d_rope = d_rope;
+  if (rope != nullptr && d_rope > 0) {
+    r.cos_sin = rope->cos_sin;
+    r.n_positions = rope->n_positions;
+    r.positions = positions;
+    r.interleaved = rope->interleaved != 0;
+    r.idx_interleaved = rope->idx_interleaved != 0;
+    r.idx_rope = rope->idx_rope != 0;
+  }
+  return r;
+}
+
+bool index_dims_supported(int d_index) { return d_index == 32 || d_index == 64 || d_index == 128 || d_index == kMaxIndex; }
+
+template <int E>
+void launch_append(const AppendArgs& A, int d_index, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(A.n_tokens) + kWarps - 1) / kWarps);
+  switch (d_index) {
+    case 32: append_kernel<E, 1><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    case 64: append_kernel<E, 2><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    case 128: append_kernel<E, 4><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    default: append_kernel<E, 8><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+  }
+}
+
+}  // namespace
+}  // namespace smla
+
+using namespace smla;
+
+extern "C" smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, int layer, const void* latent,
+                                       int64_t latent_stride, const void* rope_key, int64_t rope_stride,
+                                       const void* idx_k, int64_t idx_k_stride, const float* latent_norm,
+                                       const float* idx_norm, const float* idx_bias, float eps,
+                                       const smla_rope_t* rope, const int64_t* positions, const int64_t* slot_mapping,
+                                       int n_tokens, void* stream) {
+  if (!layout_ok(layout) || n_tokens < 0 || layer < 0 || layer >= layout->n_layers) return SMLA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return SMLA_OK;
+  const bool idx = idx_k != nullptr;
+  if (!pool || !aligned(pool, 16) || !latent || !slot_mapping || (layout->d_rope > 0 && !rope_key) ||
+      latent_stride < 0 || rope_stride < 0 || idx_k_stride < 0 || (idx_bias && !idx_norm) || !(eps >= 0.f))
+    return SMLA_ERR_INVALID_ARG;
+  smla_status_t st = check_rope(rope, positions, layout->d_rope, layout->d_index, idx);
+  if (st != SMLA_OK) return st;
+  const KernelLayout L = kernel_layout(*layout);
+  if (!store_shape_supported(L) || L.d_rope > 64 || !index_dims_supported(L.d_index)) return SMLA_ERR_UNSUPPORTED;
+  AppendArgs A{};
+  st = checked_device(&A.err);
+  if (st != SMLA_OK) return st;
+  A.L = L;
+  A.pool = static_cast<uint8_t*>(pool);
+  A.layer = layer;
+  A.latent = static_cast<const __nv_bfloat16*>(latent);
+  A.rope_key = static_cast<const __nv_bfloat16*>(rope_key);
+  A.idx_k = static_cast<const __nv_bfloat16*>(idx_k);
+  A.latent_stride = latent_stride;
+  A.rope_stride = rope_stride;
+  A.idx_stride = idx_k_stride;
+  A.latent_norm = latent_norm;
+  A.idx_norm = idx_norm;
+  A.idx_bias = idx_bias;
+  A.eps = eps;
+  A.rope = rope_args(rope, positions, L.d_rope);
+  A.slots = slot_mapping;
+  A.n_tokens = n_tokens;
+  A.vec_latent = aligned(latent, 16) && latent_stride % 8 == 0;
+  A.vec_idx = aligned(idx_k, 16) && idx_k_stride % 8 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (L.d_latent / 32) {
+    case 2: launch_append<2>(A, L.d_index, s); break;
+    case 4: launch_append<4>(A, L.d_index, s); break;
+    case 8: launch_append<8>(A, L.d_index, s); break;
+    default: launch_append<16>(A, L.d_index, s); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+extern "C" smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* params,
+                                         const smla_rope_t* rope, const int64_t* positions, const void* q_pe,
+                                         int64_t q_pe_token_stride, int64_t q_pe_head_stride, void* q_pe_out,
+                                         const void* q_idx, int64_t q_idx_token_stride, int64_t q_idx_head_stride,
+                                         const float* idx_norm, float eps, const float* w, float w_scale,
+                                         uint8_t* q_idx_out, float* w_out, int n_tokens, void* stream) {
+  if (!layout_ok(layout) || !params || n_tokens < 0) return SMLA_ERR_INVALID_ARG;
+  if (n_tokens == 0) return SMLA_OK;
+  const bool pe = q_pe != nullptr, idx = q_idx != nullptr;
+  if ((pe && (!q_pe_out || params->n_heads <= 0 || layout->d_rope <= 0 || q_pe_token_stride < 0 || q_pe_head_stride < 0)) ||
+      (idx && (!w || !q_idx_out || !w_out || params->n_idx_heads <= 0 || q_idx_token_stride < 0 ||
+               q_idx_head_stride < 0)) ||
+      !(eps >= 0.f))
+    return SMLA_ERR_INVALID_ARG;
+  if (!pe && !idx) return SMLA_OK;
+  smla_status_t st = check_rope(rope, positions, layout->d_rope, layout->d_index, idx);
+  if (st != SMLA_OK) return st;
+  if (layout->d_rope > 64 || (idx && !index_dims_supported(layout->d_index))) return SMLA_ERR_UNSUPPORTED;
+  QueryArgs A{};
+  st = checked_device(&A.err);
+  if (st != SMLA_OK) return st;
+  A.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  A.q_idx = static_cast<const __nv_bfloat16*>(q_idx);
+  A.pe_token = q_pe_token_stride;
+  A.pe_head = q_pe_head_stride;
+  A.idx_token = q_idx_token_stride;
+  A.idx_head = q_idx_head_stride;
+  A.q_pe_out = static_cast<__nv_bfloat16*>(q_pe_out);
+  A.idx_norm = idx_norm;
+  A.w = w;
+  A.eps = eps;
+  A.w_scale = w_scale;
+  A.codes = q_idx_out;
+  A.w_out = w_out;
+  A.n_tokens = n_tokens;
+  A.n_heads = params->n_heads;
+  A.n_idx_heads = params->n_idx_heads;
+  A.d_rope = layout->d_rope;
+  A.d_index = layout->d_index;
+  A.rope = rope_args(rope, positions, layout->d_rope);
+  A.vec_idx = aligned(q_idx, 16) && q_idx_token_stride % 8 == 0 && q_idx_head_stride % 8 == 0;
+  const int64_t rows = static_cast<int64_t>(n_tokens) * ((pe ? A.n_heads : 0) + (idx ? A.n_idx_heads : 0));
+  if ((rows + kWarps - 1) / kWarps > 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
+  const unsigned blocks = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (idx ? layout->d_index : 32) {
+    case 32: query_kernel<1><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    case 64: query_kernel<2><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    case 128: query_kernel<4><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+    default: query_kernel<8><<<blocks, 32 * kWarps, 0, s>>>(A); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
