@@ -80,7 +80,8 @@ typedef enum smla_status {
   SMLA_ERR_CUDA = 3,         /* a CUDA runtime call or launch failed       */
   SMLA_ERR_BAD_INDEX = 4,    /* device saw a block id / slot outside the pool (read clamped) */
   SMLA_ERR_TIMEOUT = 5,      /* a bounded on-device wait gave up            */
-  SMLA_ERR_SCRATCH_LIMIT = 6 /* smla_decode_static: one query token's scratch exceeds the static array */
+  SMLA_ERR_SCRATCH_LIMIT = 6,/* smla_decode_static: one query token's scratch exceeds the static array */
+  SMLA_ERR_RANGE = 7         /* smla_attend_dense saw a cached value beyond fp16's range */
 } smla_status_t;
 
 /*
@@ -502,6 +503,10 @@ smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* 
  * pool read as zeros and positions past the block-table row are not visited (both latch
  * SMLA_ERR_BAD_INDEX).  query_start_loc is trusted to increase from 0 to at most n_tokens.
  * Memory past a sequence's length is never used, whatever it holds.
+ * Latents of 512 dims in tiles of 128 with 64 rope dims run on the tensor cores with
+ * fp16 operands (fp32 accumulation): a latent scale above 65504 / 448 or a rope value
+ * beyond fp16's range latches SMLA_ERR_RANGE, and the outputs that read it are not
+ * valid; cached values below 2^-14 are held to 2^-25 absolutely.  Other shapes kvpack_store takes (d_rope <= 64) run in fp32 on the CUDA cores.
  * The pool is 16-byte aligned.
  */
 smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t* params, const void* pool, int layer,

@@ -36,7 +36,8 @@ EXPORTED_SYMBOLS = (
 KEY_FORMATS = {"e4m3": 0, "e2m1": 1}  # smla_key_format_t
 
 STATUS = {0: "SMLA_OK", 1: "SMLA_ERR_INVALID_ARG", 2: "SMLA_ERR_UNSUPPORTED", 3: "SMLA_ERR_CUDA",
-          4: "SMLA_ERR_BAD_INDEX", 5: "SMLA_ERR_TIMEOUT", 6: "SMLA_ERR_SCRATCH_LIMIT"}
+          4: "SMLA_ERR_BAD_INDEX", 5: "SMLA_ERR_TIMEOUT", 6: "SMLA_ERR_SCRATCH_LIMIT",
+          7: "SMLA_ERR_RANGE"}
 
 
 class SmlaError(RuntimeError):

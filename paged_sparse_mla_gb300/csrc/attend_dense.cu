@@ -4,6 +4,7 @@
 // attention is MQA over the latent; V is the latent.  [GLM-5.3 "How to try"]: a prompt that fits the
 // top-k attends over all of its positions; here that holds at any length.
 #include <atomic>
+#include <cmath>
 
 #include "smla_internal.h"
 
@@ -161,6 +162,961 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
+
+// ---------------------------------------------------------------------------
+// The full latent shape (512 latent dims in tiles of 128, 64 rope dims) on the tensor cores.
+//
+// A cluster of two CTAs (a pair) works on 128 rows, a row being one (query token, head) of one
+// sequence, and on tiles of 128 keys; each CTA owns 64 of the rows and 64 of the keys:
+//   S[128 x 128] = Q[128 x 576] . K^T      two-SM MMAs, M = 128, N = 128: each CTA brings its 64 query
+//                                          rows and its 64 keys
+//   P = 2^(S f - m), row sums in registers  each CTA for its 64 rows and all 128 keys
+//   O[128 x 512] += P[128 x 128] . V        two-SM MMAs, M = 128, N = 256, twice: each CTA brings its 64
+//                                          rows of P and all 128 keys of its 256 latent dims
+// An M = 128 two-SM accumulator keeps a CTA's 64 rows in 128 lanes: lanes 0-63 hold the first half of
+// the columns, lanes 64-127 the second.  So O (64 rows x 512 dims in fp32) takes 256 tensor-memory
+// columns of each CTA, which leaves room for two score buffers; with one SM per 128 rows it would
+// fill all 512.
+// ---------------------------------------------------------------------------
+constexpr int kRows = 128, kKeys = 128;      // of a pair
+constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
+constexpr int kDL = 512, kDR = 64, kChunks = 9;  // 64-dim chunks: 8 latent, 1 rope
+constexpr int kSoftmaxWarps = 8, kKWarps = 4, kVWarps = 4;
+constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
+constexpr int kThreads = 32 * (kIssuer + 4);  // the issuer's warpgroup: one warp issues, three only lend registers
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 96, kProducerRegs = 120, kIssuerRegs = 40;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + (kKWarps + kVWarps) * kProducerRegs + 4 * kIssuerRegs) <=
+                  kThreads * kLaunchRegs,
+              "register split exceeds the launch");
+constexpr float kRescale = 8.0f;       // the running maximum moves when a score passes it by 2^8
+constexpr float kMaxScale = 65504.0f / 448.0f, kMaxHalf = 65504.0f;
+constexpr float kSmallScale = 1.220703125e-4f;  // 2^-13: below it a scale loses bits in fp16
+constexpr int kMaxPairs = 128;
+constexpr int kMinTiles = 2;           // key tiles a pair takes at least
+constexpr int kPrefetchAhead = 4;      // tiles requested into L2 ahead of the loads
+
+struct __align__(1024) PairSmem {
+  uint8_t k[kChunks][kCtaKeys * 128];  // chunk c: [own 64 keys][64 dims] fp16, 128-byte swizzle
+  uint8_t v[4][kKeys * 128];           // chunk c: [128 keys][64 of the CTA's 256 latent dims]
+  uint8_t q[kChunks][kCtaRows * 128];
+  uint8_t p[2][kCtaRows * 128];        // chunk c: [64 rows][keys 64 c .. 64 c + 63]
+  float red[4][kCtaRows];
+  float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
+  uint64_t k_full, v_full, p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
+  uint64_t k_free, v_free, s_full[2];                  // completed by the MMAs in both CTAs
+  uint64_t final_bar;
+  int64_t x0, x1, us;                  // the pair's range of tiles and the first tile of its first unit
+  int b, g;                            // that unit
+  int64_t total;                       // work in all, over `pairs` pairs
+  int pairs;
+  int abort;
+  uint32_t tmem_slot;
+};
+constexpr size_t kPairSmemBytes = sizeof(PairSmem) + 1024;
+static_assert(kPairSmemBytes <= 232448, "shared memory");
+
+// The unit that begins in a pair's range and goes on in the next pairs' (ntok = 0: none): its parts are
+// slot 2 p + 1 of this pair and slot 2 r of every pair r > p whose range begins before `end`.
+struct PairMeta {
+  int64_t end, total;  // one past the unit's last tile; all work, divided evenly over `pairs`
+  int pairs, tok0, ntok;
+};
+
+struct PairArgs {
+  DenseArgs D;
+  int group;        // query tokens of a unit: as many as fit 128 rows
+  float abs_scale;  // |softmax_scale| log2(e)
+  float sign;       // of softmax_scale, applied to the queries
+  bool q_vec;       // q is 16-byte and q_pe 4-byte aligned
+  float *part_out, *part_lse;  // partial results, slots [2 pairs][128 rows]; nullptr: units are not split
+  PairMeta* meta;   // [pairs]
+};
+
+// sum_{g < n} floor((a g + b) / m), all non-negative (Euclid's algorithm on the lattice points).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// A unit is `group` query tokens of a sequence (fewer at its end) with the key tiles its last token sees
+// (at least one, so that tokens which see nothing are written too).
+__device__ __forceinline__ int unit_tiles(const PairArgs& A, int b, int g, int n_q) {
+  const int last = min((g + 1) * A.group, n_q) - 1;
+  return max(1, static_cast<int>((visible(A.D, b, last, n_q) + kKeys - 1) / kKeys));
+}
+
+// Work of the first g units of sequence b: their tiles, or their number where units are not split.
+__device__ int64_t work_before(const PairArgs& A, int b, int g, int n_q) {
+  if (A.part_out == nullptr) return g;
+  const int64_t len = __ldg(A.D.seq_lens + b), most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
+  const int units = (n_q + A.group - 1) / A.group;
+  if (len >= n_q && len <= most) {
+    const int whole = min(g, units - 1);
+    int64_t s = floor_sum(whole, kKeys, A.group, len - n_q + A.group + kKeys - 1);
+    if (g == units) s += (len + kKeys - 1) / kKeys;
+    return s;
+  }
+  int64_t s = 0;
+  for (int i = 0; i < g; ++i) s += unit_tiles(A, b, i, n_q);
+  return s;
+}
+
+// The units of this pair in turn, with the pair's tiles [ta, tb) of each.
+struct Walk {
+  int64_t x0, x1, us;
+  int b, g, q0, n_q;
+  int tok0, ntok, nvis, tiles, ta, tb;
+  bool on;
+  __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
+    x0 = sm.x0;
+    x1 = sm.x1;
+    us = sm.us;
+    b = sm.b;
+    g = sm.g;
+    on = x0 < x1;
+    if (on) unit(A);
+  }
+  __device__ __forceinline__ void unit(const PairArgs& A) {
+    q0 = __ldg(A.D.qsl + b);
+    n_q = __ldg(A.D.qsl + b + 1) - q0;
+    tok0 = q0 + g * A.group;
+    ntok = min(A.group, n_q - g * A.group);
+    nvis = static_cast<int>(visible(A.D, b, g * A.group + ntok - 1, n_q));
+    tiles = max(1, (nvis + kKeys - 1) / kKeys);
+    if (A.part_out != nullptr) {
+      ta = static_cast<int>(max(x0 - us, static_cast<int64_t>(0)));
+      tb = static_cast<int>(min(x1 - us, static_cast<int64_t>(tiles)));
+    } else {
+      ta = 0;
+      tb = tiles;
+    }
+  }
+  __device__ __forceinline__ void next(const PairArgs& A) {
+    us += A.part_out != nullptr ? tiles : 1;
+    on = us < x1;
+    if (!on) return;
+    if (++g * A.group >= n_q) {
+      g = 0;
+      do ++b;
+      while (__ldg(A.D.qsl + b + 1) == __ldg(A.D.qsl + b));
+    }
+    unit(A);
+  }
+};
+
+// A walk tile by tile.
+struct TileWalk {
+  Walk w;
+  int tile;
+  __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
+    w.start(A, sm);
+    tile = w.on ? w.ta : 0;
+  }
+  __device__ __forceinline__ void next(const PairArgs& A) {
+    if (!w.on) return;
+    if (++tile >= w.tb) {
+      w.next(A);
+      tile = w.on ? w.ta : 0;
+    }
+  }
+};
+
+// ---- cluster and two-SM instructions ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Arrive on a barrier of another (or this) CTA of the pair; the address comes from map_cta.
+__device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "n"(kSuspendHintNs)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait as mbar_wait, with cluster scope; a wait that gives up raises the abort flag of both CTAs.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsigned* err, int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  volatile int* flag = abort;
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (try_wait_cluster(addr, parity)) return true;
+    if ((i & 15u) == 15u) {
+      if (*flag) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > kWaitLimitNs) {
+        latch_error(err, SMLA_ERR_TIMEOUT);
+        for (uint32_t r = 0; r < 2; ++r)
+          asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_cta(smem_u32(abort), r)) : "memory");
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void pair_drain(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait_cluster(addr, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {
+  }
+}
+__device__ __forceinline__ void mma2_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs when every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 16 E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale rounds to 11 bits and
+// the product once more (2 x 2^-11 in all).  `slow`: some scale of the warp's batch is so small that
+// fp16 would hold it with fewer bits; the products are then formed in fp32.
+__device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, bool slow, uint4& o0, uint4& o1) {
+  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t ow[8];
+  const __half2 s2 = __float2half2_rn(sc);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(cw[x >> 1] >> (16 * (x & 1))), __NV_E4M3);
+    const __half2 c = *reinterpret_cast<const __half2*>(&h);
+    if (!slow) {
+      const __half2 y = __hmul2(c, s2);
+      ow[x] = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+      const float2 f = __half22float2(c);
+      ow[x] = pack_half2(f.x * sc, f.y * sc);
+    }
+  }
+  o0 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+  o1 = make_uint4(ow[4], ow[5], ow[6], ow[7]);
+}
+
+// Address of the record of position j of sequence b (nullptr at or past nvis, or for a bad block id).
+__device__ __forceinline__ const uint8_t* record_of(const DenseArgs& D, int b, int j, int nvis) {
+  if (j >= nvis) return nullptr;
+  const KernelLayout& L = D.L;
+  const int blk = __ldg(D.block_table + static_cast<int64_t>(b) * D.bt_stride + j / L.block_size);
+  if (blk < 0 || blk >= L.num_blocks) {
+    latch_error(D.err, SMLA_ERR_BAD_INDEX);
+    return nullptr;
+  }
+  return D.pool + static_cast<int64_t>(blk) * L.block_stride + static_cast<int64_t>(D.layer) * L.layer_stride +
+         L.rec_off + static_cast<int64_t>(j % L.block_size) * L.rec_stride;
+}
+__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int lane) {
+  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), lane));
+}
+
+// The pair's range of work: every thread takes sequences, a scan over the CTA finds the total and the
+// unit in which the range begins.
+__device__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
+  int64_t* warp_sum = reinterpret_cast<int64_t*>(sm.red);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int batch = A.D.batch;
+  const int64_t most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
+  int64_t total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t carry = 0;
+    const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / kMinTiles : total));
+    const int64_t x0 = pair < P ? pair * total / P : total, x1 = pair < P ? (pair + 1) * total / P : total;
+    if (pass == 1 && threadIdx.x == 0) {
+      sm.x0 = x0;
+      sm.x1 = x1;
+      sm.pairs = static_cast<int>(P);
+      sm.total = total;
+    }
+    for (int c0 = 0; c0 < batch; c0 += kThreads) {
+      const int b = c0 + threadIdx.x;
+      int64_t mine = 0;
+      int n_q = 0, units = 0;
+      if (b < batch) {
+        n_q = __ldg(A.D.qsl + b + 1) - __ldg(A.D.qsl + b);
+        units = (n_q + A.group - 1) / A.group;
+        if (n_q > 0) mine = work_before(A, b, units, n_q);
+        if (pass == 0 && blockIdx.x == 0 && n_q > 0 && __ldg(A.D.seq_lens + b) > most)
+          latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
+      }
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      __syncthreads();
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      int64_t before = carry, all = carry;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+      }
+      const int64_t lo = before + incl - mine;
+      if (pass == 1 && mine > 0 && x0 < x1 && lo <= x0 && x0 < lo + mine) {
+        int ga = 0, gb = units - 1;  // the last unit that begins at or before x0
+        while (ga < gb) {
+          const int gm = (ga + gb + 1) / 2;
+          if (lo + work_before(A, b, gm, n_q) <= x0) ga = gm;
+          else gb = gm - 1;
+        }
+        sm.b = b;
+        sm.g = ga;
+        sm.us = lo + work_before(A, b, ga, n_q);
+      }
+      carry = all;
+    }
+    total = carry;
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_pair_kernel(const PairArgs A) {
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem& sm = *reinterpret_cast<PairSmem*>(
+      smem_raw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_rank();
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  unsigned* err = A.D.err;
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.k_full, 2 * kKWarps);
+    mbar_init(&sm.v_full, 2 * kVWarps);
+    mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
+    mbar_init(&sm.q_full, 2 * kSoftmaxWarps);
+    mbar_init(&sm.k_free, 1);
+    mbar_init(&sm.v_free, 1);
+    mbar_init(&sm.final_bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
+      mbar_init(&sm.s_full[i], 1);
+    }
+    sm.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  plan(A, sm, pair, n_pairs);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either arrives on the other's
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_slot;
+  const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
+
+  if (warp >= kIssuer) {
+    // ------------------------------ MMA issuer (one thread of the first CTA) ------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+    if (warp == kIssuer && lane == 0 && cta == 0) {
+      const uint32_t idesc1 = make_idesc(128, kKeys, 0, 0, 0, 0);  // fp16, both K-major
+      const uint32_t idesc2 = make_idesc(128, 256, 0, 0, 0, 1);    // fp16, P K-major, V MN-major
+      const uint64_t dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024), dk = sw128_desc(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t dp = sw128_desc(smem_u32(sm.p[0]), 16, 1024), dv = sw128_desc(smem_u32(sm.v[0]), kKeys * 128, 1024);
+      uint32_t k1 = 0, k2 = 0, n = 0;  // MMA1s and MMA2s issued, units begun
+      // S = Q . K^T of tile k1 into score buffer k1 % 2
+      const auto mma1 = [&]() -> bool {
+        if (!pair_wait(&sm.k_full, k1 & 1, err, &sm.abort)) return false;
+        if (!pair_wait(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1, err, &sm.abort)) return false;
+        tc_fence_after();
+        const uint32_t ts = tmem_s + (k1 & 1) * 64;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mma2_f16(ts, dq + ((c * kCtaRows * 128 + x * 32) >> 4), dk + ((c * kCtaKeys * 128 + x * 32) >> 4), idesc1,
+                     (c | x) != 0);
+        commit2(&sm.s_full[k1 & 1]);
+        commit2(&sm.k_free);
+        ++k1;
+        return true;
+      };
+      // O (+)= P . V of tile k2
+      const auto mma2 = [&](bool first) -> bool {
+        if (!pair_wait(&sm.v_full, k2 & 1, err, &sm.abort)) return false;
+        if (!pair_wait(&sm.p_full, k2 & 1, err, &sm.abort)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mma2_f16(tmem_o + j * 128, dp + (((x >> 2) * kCtaRows * 128 + (x & 3) * 32) >> 4),
+                     dv + ((2 * j * kKeys * 128 + x * 2048) >> 4), idesc2, !(first && x == 0));
+        commit2(&sm.v_free);
+        ++k2;
+        return true;
+      };
+      Walk w;
+      bool ok = true;
+      for (w.start(A, sm); w.on && ok; w.next(A), ++n) {
+        ok = pair_wait(&sm.q_full, n & 1, err, &sm.abort) && mma1();
+        for (int t = w.ta; t < w.tb && ok; ++t) {
+          if (t + 1 < w.tb) ok = mma1();  // the next tile's scores while this one's softmax works
+          ok = ok && mma2(t == w.ta);
+        }
+      }
+      if (k1 > 0) {  // nothing may still read or write the pair's memory when it leaves
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&sm.final_bar))
+                     : "memory");
+        pair_drain(&sm.final_bar, 0);
+      }
+    }
+  } else if (warp >= kFirstV) {
+    // ------------------------------ V: 128 keys x this CTA's 256 latent dims ------------------------------
+    // Warp vw takes keys 32 vw .. + 31 of a tile, two at a time (16 lanes of 16 codes each).
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    const int vw = warp - kFirstV;
+    const int sub = lane & 15, hi = lane >> 4;
+    const int c = sub >> 2, odd = c & 1, s0 = 2 * (sub & 3);
+    const int code_off = 256 * static_cast<int>(cta) + 16 * sub, scale_off = kDL + 4 * (2 * static_cast<int>(cta) + (sub >> 3));
+    const uint32_t full = map_cta(smem_u32(&sm.v_full), 0);
+    uint4 codes[16];
+    float sc[16];
+    const auto lookup = [&](const TileWalk& tw) -> const uint8_t* {
+      return tw.w.on ? record_of(A.D, tw.w.b, tw.tile * kKeys + 32 * vw + lane, tw.w.nvis) : nullptr;
+    };
+    const auto load = [&](const uint8_t* ptr) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint8_t* r = shfl_ptr(ptr, 2 * i + hi);
+        codes[i] = make_uint4(0, 0, 0, 0);
+        sc[i] = 0.f;
+        if (r != nullptr) {
+          codes[i] = __ldg(reinterpret_cast<const uint4*>(r + code_off));
+          sc[i] = __ldg(reinterpret_cast<const float*>(r + scale_off));
+        }
+      }
+    };
+    TileWalk tw;
+    tw.start(A, sm);
+    bool on = tw.w.on;
+    load(lookup(tw));
+    tw.next(A);
+    bool on_next = tw.w.on;
+    const uint8_t* ptr = lookup(tw);
+    for (uint32_t kk = 0; on; ++kk) {
+      bool small = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) small |= sc[i] < kSmallScale && sc[i] != 0.f;
+      const bool slow = __any_sync(0xffffffffu, small);
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free, (kk & 1) ^ 1, err, &sm.abort))) break;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint4 o0, o1;
+        dequant16_half(codes[i], sc[i], slow, o0, o1);
+        const int key = 32 * vw + 2 * i + hi;
+        *reinterpret_cast<uint4*>(&sm.v[c][sw128_off(key, s0 + odd)]) = odd ? o1 : o0;
+        *reinterpret_cast<uint4*>(&sm.v[c][sw128_off(key, s0 + 1 - odd)]) = odd ? o0 : o1;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(full);
+      load(ptr);
+      on = on_next;
+      tw.next(A);
+      on_next = tw.w.on;
+      ptr = lookup(tw);
+    }
+  } else if (warp >= kFirstK) {
+    // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
+    // Warp kw takes keys 16 kw .. + 15: a key's 512 codes in one load (a lane per 16), the rope of four
+    // keys in another (eight lanes each).
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    const int kw = warp - kFirstK;
+    const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
+    const int scale_off = kDL + 4 * (lane >> 3), rope_off = kDL + 16 + 16 * (lane & 7);
+    const uint32_t full = map_cta(smem_u32(&sm.k_full), 0);
+    uint4 codes[16], rope[4];
+    float sc[16];
+    const auto lookup = [&](const TileWalk& tw) -> const uint8_t* {
+      return tw.w.on ? record_of(A.D, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 16 * kw + (lane & 15), tw.w.nvis)
+                     : nullptr;
+    };
+    const auto load = [&](const uint8_t* ptr) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint8_t* r = shfl_ptr(ptr, i);
+        codes[i] = make_uint4(0, 0, 0, 0);
+        sc[i] = 0.f;
+        if (r != nullptr) {
+          codes[i] = __ldg(reinterpret_cast<const uint4*>(r) + lane);
+          sc[i] = __ldg(reinterpret_cast<const float*>(r + scale_off));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* r = shfl_ptr(ptr, 4 * i + (lane >> 3));
+        rope[i] = r != nullptr ? __ldg(reinterpret_cast<const uint4*>(r + rope_off)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    TileWalk tw, ahead;  // the tile whose records are looked up next, and the one requested into L2
+    tw.start(A, sm);
+    ahead = tw;
+    for (int i = 0; i < kPrefetchAhead; ++i) ahead.next(A);
+    bool on = tw.w.on, bad = false;
+    load(lookup(tw));
+    tw.next(A);
+    bool on_next = tw.w.on;
+    const uint8_t* ptr = lookup(tw);
+    for (uint32_t kk = 0; on; ++kk) {
+      bool small = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        small |= sc[i] < kSmallScale && sc[i] != 0.f;
+        bad |= !(sc[i] <= kMaxScale);
+      }
+      const bool slow = __any_sync(0xffffffffu, small);
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint4 o0, o1;
+        dequant16_half(codes[i], sc[i], slow, o0, o1);
+        const int key = 16 * kw + i;
+        *reinterpret_cast<uint4*>(&sm.k[c][sw128_off(key, s0 + odd)]) = odd ? o1 : o0;
+        *reinterpret_cast<uint4*>(&sm.k[c][sw128_off(key, s0 + 1 - odd)]) = odd ? o0 : o1;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float lo = __uint_as_float(w[x] << 16), h = __uint_as_float(w[x] & 0xFFFF0000u);
+          bad |= fmaxf(fabsf(lo), fabsf(h)) > kMaxHalf;
+          o[x] = pack_half2(lo, h);
+        }
+        *reinterpret_cast<uint4*>(&sm.k[8][sw128_off(16 * kw + 4 * i + (lane >> 3), lane & 7)]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(full);
+      load(ptr);
+      on = on_next;
+      tw.next(A);
+      on_next = tw.w.on;
+      ptr = lookup(tw);
+      if (lane < 16) {
+        const uint8_t* r = lookup(ahead);
+        if (r != nullptr) prefetch_l2_bulk(r, 656);
+      }
+      ahead.next(A);
+    }
+    if (bad) latch_error(err, SMLA_ERR_RANGE);
+  } else {
+    // ------------------------------ queries, softmax, epilogue ------------------------------
+    // Thread: TMEM lane L = 32 (warp % 4) + lane, which is row L % 64 and half kh = L / 64 of a tile's
+    // keys (of O's dims); warps 0-3 take the first 32 columns of the half (the first 128 of O's), warps
+    // 4-7 the others.  The four threads of a row agree on its running maximum.
+    const int sp = warp & 3, wg = warp >> 2;
+    const int L = 32 * sp + lane, row = L & 63, kh = L >> 6;
+    const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+    const uint32_t p_full = map_cta(smem_u32(&sm.p_full), 0), q_full = map_cta(smem_u32(&sm.q_full), 0);
+    const uint32_t s_free[2] = {map_cta(smem_u32(&sm.s_free[0]), 0), map_cta(smem_u32(&sm.s_free[1]), 0)};
+    const int H = A.D.n_heads;
+    // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is
+    // scaled by a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's
+    // eight bits exactly down to 2^-23 of that element.
+    const auto load_q = [&](const Walk& w, int slot) {
+      const int rows = w.ntok * H - kCtaRows * static_cast<int>(cta);
+      const int64_t first = static_cast<int64_t>(w.tok0) * H + kCtaRows * cta;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint4 a[4], b[4];
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * warp + 4 * half + i;
+          a[i] = b[i] = make_uint4(0, 0, 0, 0);
+          e[i] = 0;
+          if (r < rows) {
+            const __nv_bfloat16* src = A.D.q + (first + r) * kDL + 16 * lane;
+            const __nv_bfloat16* pe = A.D.q_pe + (first + r) * kDR + 2 * lane;
+            if (A.q_vec) {
+              a[i] = __ldg(reinterpret_cast<const uint4*>(src));
+              b[i] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+              e[i] = __ldg(reinterpret_cast<const uint32_t*>(pe));
+            } else {
+              const uint16_t* u = reinterpret_cast<const uint16_t*>(src);
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(pe);
+              uint32_t t[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) t[x] = u[2 * x] | (static_cast<uint32_t>(u[2 * x + 1]) << 16);
+              a[i] = make_uint4(t[0], t[1], t[2], t[3]);
+              b[i] = make_uint4(t[4], t[5], t[6], t[7]);
+              e[i] = v[0] | (static_cast<uint32_t>(v[1]) << 16);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * warp + 4 * half + i;
+          const uint32_t w9[9] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w, e[i]};
+          uint32_t top = 0;  // the largest magnitude's bits (fp32 bits of non-negative values order as integers)
+#pragma unroll
+          for (int x = 0; x < 9; ++x) top = max(top, max((w9[x] << 16) & 0x7FFFFFFFu, w9[x] & 0x7FFF0000u));
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int ex = static_cast<int>(top >> 23);  // biased exponent
+          const int up = (ex == 0 || ex == 255) ? 0 : min(126, 127 + 8 - ex);  // zeros, infinities and NaN as they are
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23) * A.sign;
+          uint32_t o[9];
+#pragma unroll
+          for (int x = 0; x < 9; ++x)
+            o[x] = pack_half2(__uint_as_float(w9[x] << 16) * f, __uint_as_float(w9[x] & 0xFFFF0000u) * f);
+          const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
+          const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]) = odd ? o1 : o0;
+          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + 1 - odd)]) = odd ? o0 : o1;
+          *reinterpret_cast<uint32_t*>(&sm.q[8][sw128_off(r, lane >> 2) + 4 * (lane & 3)]) = o[8];
+          if (lane == 0) sm.row_f[slot][r] = A.abs_scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(q_full);
+    };
+
+    Walk w;
+    w.start(A, sm);
+    if (A.meta != nullptr && cta == 0 && threadIdx.x == 0) A.meta[pair].ntok = 0;
+    if (w.on) load_q(w, 0);
+    named_bar_sync(1, 32 * kSoftmaxWarps);  // row_f
+    uint32_t kk = 0, n = 0;
+    bool failed = false;
+    while (w.on && !failed) {
+      const int grow = kCtaRows * static_cast<int>(cta) + row;  // row of the unit
+      const bool real = grow < w.ntok * H;
+      const int vis = real ? static_cast<int>(visible(A.D, w.b, w.tok0 - w.q0 + grow / H, w.n_q)) : 0;
+      // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
+      const float f = fmaxf(sm.row_f[n & 1][row], 1.2e-38f);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int tile = w.ta; tile < w.tb; ++tile, ++kk) {
+        const int buf = kk & 1;
+        ok = ok && pair_wait(&sm.s_full[buf], (kk >> 1) & 1, err, &sm.abort);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t r[32];
+        tmem_ld32(tmem_s + lane_base + buf * 64 + 32 * wg, r);
+        tmem_ld_wait(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(s_free[buf]);
+        // visible keys among this thread's 32
+        const int vr = vis - (tile * kKeys + 64 * kh + 32 * wg);
+        float mx = -INFINITY;
+        if (__all_sync(0xffffffffu, vr >= 32)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (i >= vr) r[i] = 0xFF800000u;  // -inf
+            mx = fmaxf(mx, __uint_as_float(r[i]));
+          }
+        }
+        mx = mx == -INFINITY ? -INFINITY : mx * f;
+        // The maximum of a row moves only when a score passes it by 2^8; only then (and on the first
+        // tile) the four threads of every row compare notes.
+        const bool first = tile == w.ta;
+        if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || mx > m + kRescale)) {
+          sm.red[2 * wg + kh][row] = mx;
+          if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) {
+            failed = true;
+            break;
+          }
+          const float mt = fmaxf(fmaxf(sm.red[0][row], sm.red[1][row]), fmaxf(sm.red[2][row], sm.red[3][row]));
+          const bool move = first || mt > m + kRescale;
+          const float mn = move ? fmaxf(m, mt) : m;
+          const float alpha = move && m != -INFINITY ? exp2f(m - mn) : 1.f;
+          l *= alpha;
+          m = mn;
+          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // O holds the tiles before this one once their last MMA is done; this tile's waits for p_full
+            ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              uint32_t o[32];
+              tmem_ld32(tmem_o + lane_base + 128 * wg + 32 * x, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tmem_o + lane_base + 128 * wg + 32 * x, o);
+            }
+            tmem_st_wait();
+          }
+          named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint32_t pw[16];
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float p0 = fast_exp2(fmaf(__uint_as_float(r[i]), f, -mu)), p1 = fast_exp2(fmaf(__uint_as_float(r[i + 1]), f, -mu));
+          l0 += p0;
+          l1 += p1;
+          pw[i / 2] = pack_half2(p0, p1);
+        }
+        l += l0 + l1;
+        if (kk > 0) ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;  // P is read
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          *reinterpret_cast<uint4*>(&sm.p[kh][sw128_off(row, 4 * wg + v)]) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(p_full);
+      }
+      if (failed) break;
+      // the next unit's queries while the last MMAs run (the last scores are read: Q is free)
+      Walk nx = w;
+      nx.next(A);
+      if (nx.on) load_q(nx, (n + 1) & 1);
+      // ---- end of unit ----
+      ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;
+      __syncwarp();
+      tc_fence_after();
+      sm.red[2 * wg + kh][row] = l;
+      if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) break;
+      const float lt = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
+      const float inv = lt == 0.f ? 0.f : 1.f / lt;  // no visible key: zeros
+      const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
+      const bool partial = w.ta > 0 || w.tb < w.tiles;
+      const int64_t slot = 2 * pair + (w.ta > 0 ? 0 : 1);
+      const int64_t orow = static_cast<int64_t>(w.tok0) * H + grow;
+      const int d0 = 256 * kh + 128 * wg;
+      if (kh == 0 && wg == 0 && real) {
+        if (partial) A.part_lse[slot * kRows + grow] = lse;
+        else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
+      }
+#pragma unroll 1
+      for (int x = 0; x < 4; ++x) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(tmem_o + lane_base + 128 * wg + 32 * x, o);
+        tmem_ld_wait(o);
+        if (real && partial) {
+          float4* dst = reinterpret_cast<float4*>(A.part_out + (slot * kRows + grow) * kDL + d0 + 32 * x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+        } else if (real) {
+          uint4* dst = reinterpret_cast<uint4*>(A.D.out + orow * kDL + d0 + 32 * x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              h[y] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read, row_f of the next unit is written
+      // the unit that goes on in the next pair: what the merge has to join
+      if (cta == 0 && threadIdx.x == 0 && w.ta == 0 && w.tb < w.tiles) A.meta[pair] = {w.us + w.tiles, sm.total, sm.pairs, w.tok0, w.ntok};
+      w = nx;
+      ++n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's arrivals and MMAs no longer touch this one
+  if (warp == kIssuer) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Joins the parts of units that ran on several pairs: lse = ln sum e^lse_i, out = sum e^(lse_i - lse) out_i
+// in fp32.  One block per row at a time, a thread per four dims; the parts' loads go out eight at a time.
+constexpr int kMergeThreads = 128;
+__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMeta* __restrict__ meta,
+                                                                    const float* __restrict__ part_lse,
+                                                                    const float* __restrict__ part_out, int n_pairs,
+                                                                    int n_heads, __nv_bfloat16* __restrict__ out,
+                                                                    float* __restrict__ lse) {
+  __shared__ int cum[kMaxPairs + 1];  // rows to join of the pairs before p
+  __shared__ float weight[kMaxPairs];
+  static_assert(kMergeThreads == kMaxPairs, "a thread per pair");
+  const int tid = threadIdx.x, lane = tid & 31;
+  cum[tid + 1] = tid < n_pairs ? meta[tid].ntok * n_heads : 0;
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+  for (int o = 1; o < kMaxPairs; o <<= 1) {
+    const int v = tid + 1 > o ? cum[tid + 1 - o] : 0;
+    __syncthreads();
+    cum[tid + 1] += v;
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < cum[kMaxPairs]; item += gridDim.x) {
+    int p = 0, hi = n_pairs - 1;
+    while (p < hi) {
+      const int mid = (p + hi + 1) / 2;
+      if (cum[mid] <= item) p = mid;
+      else hi = mid - 1;
+    }
+    const int row = item - cum[p];
+    const PairMeta M = meta[p];
+    // pairs p + 1 .. p + more carry the rest
+    int more = 0;
+    while (p + more + 1 < M.pairs && (p + more + 1) * M.total / M.pairs < M.end) ++more;
+    const int parts = more + 1;
+    const auto slot = [&](int i) -> int64_t { return i == 0 ? 2 * p + 1 : 2 * (p + i); };
+    float z = 0.f, mx = -INFINITY;
+    if (tid < 32) {
+      float v[kMaxPairs / 32];
+#pragma unroll
+      for (int i = 0; i < kMaxPairs / 32; ++i) {
+        v[i] = 32 * i + lane < parts ? __ldg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
+        mx = fmaxf(mx, v[i]);
+        if (v[i] != v[i]) mx = v[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int i = 0; i < kMaxPairs / 32; ++i) {
+        v[i] = expf(v[i] - base);
+        z += v[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+      for (int i = 0; i < kMaxPairs / 32; ++i)
+        if (32 * i + lane < parts) weight[32 * i + lane] = v[i] * inv;
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < parts) v[i] = __ldg(reinterpret_cast<const float4*>(part_out + (slot(i0 + i) * kRows + row) * kDL) + tid);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i < parts) {
+          const float f = weight[i0 + i];
+          acc.x += f * v[i].x;
+          acc.y += f * v[i].y;
+          acc.z += f * v[i].z;
+          acc.w += f * v[i].w;
+        }
+      }
+    }
+    const int64_t orow = static_cast<int64_t>(M.tok0) * n_heads + row;
+    reinterpret_cast<uint2*>(out + orow * kDL)[tid] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    if (tid == 0 && lse != nullptr) lse[orow] = z == 0.f ? -INFINITY : mx + logf(z);
+    __syncthreads();  // weight is read
+  }
+}
+
+// Layouts of the full latent shape.
+bool pair_shape(const KernelLayout& L) { return L.d_latent == kDL && L.quant_tile == 128 && L.d_rope == kDR; }
+
+constexpr size_t kMetaBytes = (kMaxPairs * sizeof(PairMeta) + 255) / 256 * 256;
+constexpr size_t kPartLseBytes = 2 * kMaxPairs * kRows * sizeof(float);
+constexpr size_t kPartOutBytes = size_t(2) * kMaxPairs * kRows * kDL * sizeof(float);
+
+smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                cudaStream_t s) {
+  static std::atomic<int> pairs_of[kMaxDeviceSlots] = {};  // pairs resident at once
+  const int dev = current_device_index();
+  if (dev < 0) return SMLA_ERR_CUDA;
+  int pairs = pairs_of[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
+    if (cudaFuncSetAttribute(dense_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPairSmemBytes)) != cudaSuccess)
+      return SMLA_ERR_CUDA;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, dense_pair_kernel) != cudaSuccess) return SMLA_ERR_CUDA;
+    if (fa.numRegs < kLaunchRegs) return SMLA_ERR_UNSUPPORTED;  // setmaxnreg.inc draws on the launch's registers
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * kMaxPairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&pairs, dense_pair_kernel, &cfg) != cudaSuccess || pairs <= 0) return SMLA_ERR_CUDA;
+    if (pairs > kMaxPairs) pairs = kMaxPairs;
+    pairs_of[dev].store(pairs, std::memory_order_release);
+  }
+  PairArgs A{};
+  A.D = D;
+  A.group = kRows / D.n_heads;
+  A.abs_scale = fabsf(softmax_scale) * kLog2e;
+  A.sign = softmax_scale < 0.f ? -1.f : 1.f;
+  A.q_vec = (reinterpret_cast<uintptr_t>(D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(D.q_pe) & 3) == 0;
+  const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
+  if (split) {
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    A.meta = reinterpret_cast<PairMeta*>(w);
+    A.part_lse = reinterpret_cast<float*>(w + kMetaBytes);
+    A.part_out = reinterpret_cast<float*>(w + kMetaBytes + kPartLseBytes);
+  }
+  dense_pair_kernel<<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  if (split) {
+    dense_merge_kernel<<<8 * device_sm_count(), kMergeThreads, 0, s>>>(A.meta, A.part_lse, A.part_out, pairs, D.n_heads, D.out, D.lse);
+    if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  }
+  return SMLA_OK;
+}
+
 }  // namespace
 }  // namespace smla
 
@@ -169,7 +1125,7 @@ using namespace smla;
 extern "C" size_t smla_attend_dense_workspace_size(const smla_layout_t* layout, const smla_params_t* params,
                                                    int n_tokens) {
   if (!layout_ok(layout) || params == nullptr || n_tokens <= 0 || params->n_heads <= 0) return 0;
-  return 0;
+  return pair_shape(kernel_layout(*layout)) ? kMetaBytes + kPartLseBytes + kPartOutBytes : 0;
 }
 
 extern "C" smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t* params, const void* pool,
@@ -205,5 +1161,7 @@ extern "C" smla_status_t smla_attend_dense(const smla_layout_t* layout, const sm
   A.n_tokens = n_tokens;
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;
-  return launch_dense_fp32(A, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pair_shape(L)) return launch_dense_pair(A, params->softmax_scale, workspace, workspace_bytes, s);
+  return launch_dense_fp32(A, s);
 }

@@ -1,12 +1,13 @@
 """smla_attend_dense on the GPU against attention in float64 over the same cache.
 
 Tolerance, per output element, from the roundings that the call documents.  The tensor-core path holds
-the dequantised keys (scale and product: 2 x 2^-11 relative) and the probabilities (2^-11) in fp16; a
-score is off by at most dS = sigma sum_d |q_d K_jd| 2^-10, which moves its probability by the factor
-e^dS on either side of the normalisation.  So
-    |out - ref| <= 2^-8 |ref| + sum_j p_j |K_j| (2^-10 + 2^-11 + 2 dS_max) + 1e-5 max_j |K_j|
-with 2^-8 for the bf16 result and the last term for fp32 sums and the fp16 steps near zero (2^-25 of
-keys or probabilities below 2^-14).  lse moves by at most dS_max, plus 1e-5 (1 + |lse|) for its logarithm
+the dequantised keys (scale and product: 2 x 2^-11 relative) and the probabilities (2^-11) in fp16.  Below
+2^-14 fp16's step stays 2^-24: there a key is off by up to 2^-25, half a step, whatever its size.  So a
+score is off by at most dS = sigma sum_d |q_d| (|K_jd| 2^-10 + 2^-25), which moves its probability by the
+factor e^dS on either side of the normalisation, and
+    |out - ref| <= 2^-8 |ref| + sum_j p_j |K_j| (2^-10 + 2^-11 + 2 dS_max) + 2^-25 + 1e-5 max_j |K_j|
+with 2^-8 for the bf16 result, 2^-25 = sum_j p_j 2^-25 for the keys' steps near zero, and the last term
+for the fp32 sums and the probabilities below 2^-14 (2^-25 each, of at most a few thousand).  lse moves by at most dS_max, plus 1e-5 (1 + |lse|) for its logarithm
 and the fp32 sums.  The fp32 path of other shapes stays inside the same bounds.
 """
 import numpy as np
@@ -98,8 +99,8 @@ class Case:
                 p = torch.softmax(s, -1)
                 outs.append(p @ lat[:v])
                 lses.append(torch.logsumexp(s, -1))
-                ds = abs(self.sigma) * 2.0 ** -10 * (q.abs() @ lat[:v].abs().T).amax(-1)
-                bo.append(2.0 ** -8 * outs[-1].abs() + (p @ lat[:v].abs()) * (2.0 ** -10 + 2.0 ** -11 + 2 * ds[:, None]) + 1e-5 * lat[:v].abs().max())
+                ds = abs(self.sigma) * (2.0 ** -10 * (q.abs() @ lat[:v].abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))
+                bo.append(2.0 ** -8 * outs[-1].abs() + (p @ lat[:v].abs()) * (2.0 ** -10 + 2.0 ** -11 + 2 * ds[:, None]) + 2.0 ** -25 + 1e-5 * lat[:v].abs().max())
                 bl.append(ds + 1e-5 * (1 + lses[-1].abs()))
             at += c
         return [torch.stack(x) for x in (outs, lses, bo, bl)]
@@ -247,6 +248,21 @@ def test_lengths_past_the_block_table_are_cut_and_latch():
     got = c.run()
     assert smla.smla_get_last_error() == 4
     c.check(got)
+
+
+def test_values_beyond_fp16_latch_range():
+    c = Case([100], [1], 64, seed=14)
+    c.run()
+    ok()
+    rec = c.pool.view(-1, c.lay.block_stride)[int(c.table[0, 0]), :64 * 656].view(64, 656)
+    rec[5, 512:516] = torch.tensor([200.0], device="cuda").view(torch.uint8)
+    c.run()
+    assert smla.smla_get_last_error() == 7
+    c = Case([100], [1], 64, seed=14)
+    rec = c.pool.view(-1, c.lay.block_stride)[int(c.table[0, 1]), :64 * 656].view(64, 656)
+    rec[30, 528:530] = torch.tensor([70000.0], device="cuda").bfloat16().view(torch.uint8)
+    c.run()
+    assert smla.smla_get_last_error() == 7
 
 
 def test_nan_query_stays_in_its_row():
