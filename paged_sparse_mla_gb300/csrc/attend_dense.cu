@@ -5,6 +5,7 @@
 // top-k attends over all of its positions; here that holds at any length.
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "smla_internal.h"
 
@@ -181,15 +182,17 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 constexpr int kRows = 128, kKeys = 128;      // of a pair
 constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
 constexpr int kDL = 512, kDR = 64, kChunks = 9;  // 64-dim chunks: 8 latent, 1 rope
-constexpr int kSoftmaxWarps = 8, kKWarps = 4, kVWarps = 4;
+constexpr int kSoftmaxWarps = 8, kKWarps = 8, kVWarps = 8;
+constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kKeys / kVWarps;  // of a warp, in a tile
 constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
 constexpr int kThreads = 32 * (kIssuer + 4);  // the issuer's warpgroup: one warp issues, three only lend registers
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 96, kProducerRegs = 120, kIssuerRegs = 40;
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 96, kProducerRegs = 64, kIssuerRegs = 56;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + (kKWarps + kVWarps) * kProducerRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
 constexpr float kRescale = 8.0f;       // the running maximum moves when a score passes it by 2^8
-constexpr float kMaxScale = 65504.0f / 448.0f, kMaxHalf = 65504.0f;
+constexpr float kMaxScale = 65504.0f / 448.0f;
+constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
 constexpr float kSmallScale = 1.220703125e-4f;  // 2^-13: below it a scale loses bits in fp16
 constexpr int kMaxPairs = 128;
 constexpr int kMinTiles = 2;           // key tiles a pair takes at least
@@ -205,12 +208,11 @@ struct __align__(1024) PairSmem {
   uint64_t k_full, v_full, p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
   uint64_t k_free, v_free, s_full[2];                  // completed by the MMAs in both CTAs
   uint64_t final_bar;
-  int64_t x0, x1, us;                  // the pair's range of tiles and the first tile of its first unit
-  int b, g;                            // that unit
-  int64_t total;                       // work in all, over `pairs` pairs
-  int pairs;
+  int64_t x0, total;                   // start of the pair's range of work; all work, over `pairs` pairs
+  int pairs, b, g, rel, len;           // the range's first unit and its position (see Walk)
   int abort;
   uint32_t tmem_slot;
+  uint32_t k_loaded;                   // tiles whose keys the first K warp has asked for
 };
 constexpr size_t kPairSmemBytes = sizeof(PairSmem) + 1024;
 static_assert(kPairSmemBytes <= 232448, "shared memory");
@@ -230,6 +232,8 @@ struct PairArgs {
   bool q_vec;       // q is 16-byte and q_pe 4-byte aligned
   float *part_out, *part_lse;  // partial results, slots [2 pairs][128 rows]; nullptr: units are not split
   PairMeta* meta;   // [pairs]
+  const uint8_t* records;               // the layer's records in block 0
+  uint32_t bs_mul, bs_shift1, bs_shift2;  // division by block_size
 };
 
 // sum_{g < n} floor((a g + b) / m), all non-negative (Euclid's algorithm on the lattice points).
@@ -273,40 +277,34 @@ __device__ int64_t work_before(const PairArgs& A, int b, int g, int n_q) {
   return s;
 }
 
-// The units of this pair in turn, with the pair's tiles [ta, tb) of each.
+// The units of this pair in turn.  Positions count tiles from the start of the pair's range: the unit
+// begins at `rel` (below zero if an earlier pair began it) and the range ends at `len`.
 struct Walk {
-  int64_t x0, x1, us;
-  int b, g, q0, n_q;
-  int tok0, ntok, nvis, tiles, ta, tb;
-  bool on;
+  int b, g, q0, n_q, nvis, rel, len;
   __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
-    x0 = sm.x0;
-    x1 = sm.x1;
-    us = sm.us;
     b = sm.b;
     g = sm.g;
-    on = x0 < x1;
-    if (on) unit(A);
+    rel = sm.rel;
+    len = sm.len;
+    if (on()) unit(A);
+  }
+  __device__ __forceinline__ bool on() const { return rel < len; }
+  __device__ __forceinline__ int tok0(const PairArgs& A) const { return q0 + g * A.group; }
+  __device__ __forceinline__ int ntok(const PairArgs& A) const { return min(A.group, n_q - g * A.group); }
+  __device__ __forceinline__ int tiles() const { return max(1, (nvis + kKeys - 1) / kKeys); }
+  // the pair's tiles [ta, tb) of the unit
+  __device__ __forceinline__ int ta(const PairArgs& A) const { return A.part_out != nullptr ? max(-rel, 0) : 0; }
+  __device__ __forceinline__ int tb(const PairArgs& A) const {
+    return A.part_out != nullptr ? min(tiles(), len - rel) : tiles();
   }
   __device__ __forceinline__ void unit(const PairArgs& A) {
     q0 = __ldg(A.D.qsl + b);
     n_q = __ldg(A.D.qsl + b + 1) - q0;
-    tok0 = q0 + g * A.group;
-    ntok = min(A.group, n_q - g * A.group);
-    nvis = static_cast<int>(visible(A.D, b, g * A.group + ntok - 1, n_q));
-    tiles = max(1, (nvis + kKeys - 1) / kKeys);
-    if (A.part_out != nullptr) {
-      ta = static_cast<int>(max(x0 - us, static_cast<int64_t>(0)));
-      tb = static_cast<int>(min(x1 - us, static_cast<int64_t>(tiles)));
-    } else {
-      ta = 0;
-      tb = tiles;
-    }
+    nvis = static_cast<int>(visible(A.D, b, g * A.group + ntok(A) - 1, n_q));
   }
   __device__ __forceinline__ void next(const PairArgs& A) {
-    us += A.part_out != nullptr ? tiles : 1;
-    on = us < x1;
-    if (!on) return;
+    rel += A.part_out != nullptr ? tiles() : 1;
+    if (!on()) return;
     if (++g * A.group >= n_q) {
       g = 0;
       do ++b;
@@ -319,16 +317,21 @@ struct Walk {
 // A walk tile by tile.
 struct TileWalk {
   Walk w;
-  int tile;
+  int tile, tb;
+  __device__ __forceinline__ bool on() const { return w.on(); }
+  __device__ __forceinline__ void enter(const PairArgs& A) {
+    tile = w.on() ? w.ta(A) : 0;
+    tb = w.on() ? w.tb(A) : 0;
+  }
   __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
     w.start(A, sm);
-    tile = w.on ? w.ta : 0;
+    enter(A);
   }
   __device__ __forceinline__ void next(const PairArgs& A) {
-    if (!w.on) return;
-    if (++tile >= w.tb) {
+    if (!w.on()) return;
+    if (++tile >= tb) {
       w.next(A);
-      tile = w.on ? w.ta : 0;
+      enter(A);
     }
   }
 };
@@ -347,28 +350,21 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// Arrive on a barrier of another (or this) CTA of the pair; the address comes from map_cta.
+// Arrive on a barrier of another (or this) CTA of the pair; the address comes from map_cta.  What the
+// arrival hands over is this CTA's own shared memory, already made visible to the MMAs by the proxy
+// fence before it, or tensor memory that has been read: no thread of the other CTA reads it, so the
+// release need not reach past this CTA.  (A release at cluster scope waits for every outstanding load
+// of the thread: it took 1,500 to 2,000 cycles of each hand-off.)
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t addr, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity), "n"(kSuspendHintNs)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait as mbar_wait, with cluster scope; a wait that gives up raises the abort flag of both CTAs.
+// Bounded wait as mbar_wait; a wait that gives up raises the abort flag of both CTAs.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsigned* err, int* abort) {
   const uint32_t addr = smem_u32(bar);
   volatile int* flag = abort;
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
-    if (try_wait_cluster(addr, parity)) return true;
+    if (mbar_try_wait(addr, parity)) return true;
     if ((i & 15u) == 15u) {
       if (*flag) return false;
       const uint64_t t = globaltimer_ns();
@@ -386,15 +382,30 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsign
 __device__ __forceinline__ void pair_drain(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
   const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_cluster(addr, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {
+  while (!mbar_try_wait(addr, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {
   }
 }
-__device__ __forceinline__ void mma2_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D (+)= A . B over both CTAs.  The operands move by constant byte offsets from a descriptor's low word
+// (its address field counts 16 bytes); the sums stand inside the statement, so that the compiler does not
+// keep dozens of 64-bit descriptors.
+template <int kAOff, int kBOff>
+__device__ __forceinline__ void mma2_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+      "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(kAOff >> 4), "n"(kBOff >> 4)
       : "memory");
+}
+// f(integral_constant 0) .. f(integral_constant N - 1)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
 }
 // Arrive on `bar` of both CTAs when every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void commit2(uint64_t* bar) {
@@ -415,9 +426,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // 16 E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale rounds to 11 bits and
-// the product once more (2 x 2^-11 in all).  `slow`: some scale of the warp's batch is so small that
-// fp16 would hold it with fewer bits; the products are then formed in fp32.
-__device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, bool slow, uint4& o0, uint4& o1) {
+// the product once more (2 x 2^-11 in all).  kSlow: the scale may be so small that fp16 would hold it with
+// fewer bits, so the products are formed in fp32.
+template <bool kSlow>
+__device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, uint4& o0, uint4& o1) {
   const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t ow[8];
   const __half2 s2 = __float2half2_rn(sc);
@@ -425,7 +437,7 @@ __device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, boo
   for (int x = 0; x < 8; ++x) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(cw[x >> 1] >> (16 * (x & 1))), __NV_E4M3);
     const __half2 c = *reinterpret_cast<const __half2*>(&h);
-    if (!slow) {
+    if constexpr (!kSlow) {
       const __half2 y = __hmul2(c, s2);
       ow[x] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
@@ -436,21 +448,25 @@ __device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, boo
   o0 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
   o1 = make_uint4(ow[4], ow[5], ow[6], ow[7]);
 }
+__device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale && s != 0.f; }
 
-// Address of the record of position j of sequence b (nullptr at or past nvis, or for a bad block id).
-__device__ __forceinline__ const uint8_t* record_of(const DenseArgs& D, int b, int j, int nvis) {
-  if (j >= nvis) return nullptr;
-  const KernelLayout& L = D.L;
-  const int blk = __ldg(D.block_table + static_cast<int64_t>(b) * D.bt_stride + j / L.block_size);
-  if (blk < 0 || blk >= L.num_blocks) {
+// What masked and unreadable positions read as: scales and rope of zero.
+__device__ uint4 g_zero_record[41];
+
+// Address of the record of position j of sequence b: zeros at or past nvis, or for a bad block id.
+__device__ __forceinline__ const uint8_t* record_of(const PairArgs& A, int b, int j, int nvis) {
+  const DenseArgs& D = A.D;
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_record);
+  if (j >= nvis) return zero;
+  // j / block_size by multiplication (Granlund and Montgomery's round-up method)
+  const uint32_t t = __umulhi(static_cast<uint32_t>(j), A.bs_mul);
+  const int pg = static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
+  const int blk = __ldg(D.block_table + static_cast<int64_t>(b) * D.bt_stride + pg);
+  if (blk < 0 || blk >= D.L.num_blocks) {
     latch_error(D.err, SMLA_ERR_BAD_INDEX);
-    return nullptr;
+    return zero;
   }
-  return D.pool + static_cast<int64_t>(blk) * L.block_stride + static_cast<int64_t>(D.layer) * L.layer_stride +
-         L.rec_off + static_cast<int64_t>(j % L.block_size) * L.rec_stride;
-}
-__device__ __forceinline__ const uint8_t* shfl_ptr(const uint8_t* p, int lane) {
-  return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), lane));
+  return A.records + static_cast<int64_t>(blk) * D.L.block_stride + (j - pg * D.L.block_size) * 656;
 }
 
 // The pair's range of work: every thread takes sequences, a scan over the CTA finds the total and the
@@ -467,7 +483,8 @@ __device__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
     const int64_t x0 = pair < P ? pair * total / P : total, x1 = pair < P ? (pair + 1) * total / P : total;
     if (pass == 1 && threadIdx.x == 0) {
       sm.x0 = x0;
-      sm.x1 = x1;
+      sm.len = static_cast<int>(x1 - x0);
+      if (x0 >= x1) sm.rel = 0;
       sm.pairs = static_cast<int>(P);
       sm.total = total;
     }
@@ -506,7 +523,7 @@ __device__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
         }
         sm.b = b;
         sm.g = ga;
-        sm.us = lo + work_before(A, b, ga, n_q);
+        sm.rel = static_cast<int>(lo + work_before(A, b, ga, n_q) - x0);
       }
       carry = all;
     }
@@ -535,6 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       mbar_init(&sm.s_full[i], 1);
     }
     sm.abort = 0;
+    sm.k_loaded = 0;
     mbar_fence_init();
   }
   if (warp == kIssuer) {
@@ -559,6 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const uint32_t idesc2 = make_idesc(128, 256, 0, 0, 0, 1);    // fp16, P K-major, V MN-major
       const uint64_t dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024), dk = sw128_desc(smem_u32(sm.k[0]), 16, 1024);
       const uint64_t dp = sw128_desc(smem_u32(sm.p[0]), 16, 1024), dv = sw128_desc(smem_u32(sm.v[0]), kKeys * 128, 1024);
+      const uint32_t dq_lo = static_cast<uint32_t>(dq), dk_lo = static_cast<uint32_t>(dk), dp_lo = static_cast<uint32_t>(dp), dv_lo = static_cast<uint32_t>(dv);
+      const uint32_t dq_hi = static_cast<uint32_t>(dq >> 32), dk_hi = static_cast<uint32_t>(dk >> 32), dp_hi = static_cast<uint32_t>(dp >> 32), dv_hi = static_cast<uint32_t>(dv >> 32);
       uint32_t k1 = 0, k2 = 0, n = 0;  // MMA1s and MMA2s issued, units begun
       // S = Q . K^T of tile k1 into score buffer k1 % 2
       const auto mma1 = [&]() -> bool {
@@ -566,12 +586,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (!pair_wait(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1, err, &sm.abort)) return false;
         tc_fence_after();
         const uint32_t ts = tmem_s + (k1 & 1) * 64;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma2_f16(ts, dq + ((c * kCtaRows * 128 + x * 32) >> 4), dk + ((c * kCtaKeys * 128 + x * 32) >> 4), idesc1,
-                     (c | x) != 0);
+        unrolled<4 * kChunks>([&](auto i) {
+          constexpr int c = i() / 4, x = i() % 4;
+          mma2_f16<c * kCtaRows * 128 + x * 32, c * kCtaKeys * 128 + x * 32>(ts, dq_lo, dq_hi, dk_lo, dk_hi, idesc1, i() != 0);
+        });
         commit2(&sm.s_full[k1 & 1]);
         commit2(&sm.k_free);
         ++k1;
@@ -582,23 +600,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (!pair_wait(&sm.v_full, k2 & 1, err, &sm.abort)) return false;
         if (!pair_wait(&sm.p_full, k2 & 1, err, &sm.abort)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int x = 0; x < kKeys / 16; ++x)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma2_f16(tmem_o + j * 128, dp + (((x >> 2) * kCtaRows * 128 + (x & 3) * 32) >> 4),
-                     dv + ((2 * j * kKeys * 128 + x * 2048) >> 4), idesc2, !(first && x == 0));
+        unrolled<2 * (kKeys / 16)>([&](auto i) {
+          constexpr int x = i() / 2, j = i() % 2;
+          mma2_f16<(x >> 2) * kCtaRows * 128 + (x & 3) * 32, 2 * j * kKeys * 128 + x * 2048>(
+              tmem_o + j * 128, dp_lo, dp_hi, dv_lo, dv_hi, idesc2, !(first && x == 0));
+        });
         commit2(&sm.v_free);
         ++k2;
         return true;
       };
       Walk w;
       bool ok = true;
-      for (w.start(A, sm); w.on && ok; w.next(A), ++n) {
+      for (w.start(A, sm); w.on() && ok; w.next(A), ++n) {
         ok = pair_wait(&sm.q_full, n & 1, err, &sm.abort) && mma1();
-        for (int t = w.ta; t < w.tb && ok; ++t) {
-          if (t + 1 < w.tb) ok = mma1();  // the next tile's scores while this one's softmax works
-          ok = ok && mma2(t == w.ta);
+        const int ta = w.ta(A), tb = w.tb(A);
+        for (int t = ta; t < tb && ok; ++t) {
+          if (t + 1 < tb) ok = mma1();  // the next tile's scores while this one's softmax works
+          ok = ok && mma2(t == ta);
         }
       }
       if (k1 > 0) {  // nothing may still read or write the pair's memory when it leaves
@@ -607,146 +625,160 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
                      : "memory");
         pair_drain(&sm.final_bar, 0);
       }
+    } else if (warp == kIssuer + 1) {
+      // Requests this CTA's keys into L2 a few tiles before the K warps load them.
+      TileWalk tw;
+      tw.start(A, sm);
+      const uint64_t t0 = globaltimer_ns();
+      uint64_t last = t0;
+      uint32_t seen = 0;
+      for (uint32_t kk = 0; tw.on(); ++kk) {
+        for (;;) {
+          const uint32_t done = *static_cast<volatile uint32_t*>(&sm.k_loaded);
+          if (kk < done + kPrefetchAhead) break;
+          const uint64_t now = globaltimer_ns();
+          if (done != seen) last = now;
+          seen = done;
+          if (*static_cast<volatile int*>(&sm.abort) || now - last > kWaitLimitNs) break;  // requests only: nothing waits for them
+          __nanosleep(100);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          prefetch_l2_bulk(record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane, tw.w.nvis), 656);
+        }
+        tw.next(A);
+      }
     }
   } else if (warp >= kFirstV) {
     // ------------------------------ V: 128 keys x this CTA's 256 latent dims ------------------------------
-    // Warp vw takes keys 32 vw .. + 31 of a tile, two at a time (16 lanes of 16 codes each).
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    const int vw = warp - kFirstV;
-    const int sub = lane & 15, hi = lane >> 4;
-    const int c = sub >> 2, odd = c & 1, s0 = 2 * (sub & 3);
-    const int code_off = 256 * static_cast<int>(cta) + 16 * sub, scale_off = kDL + 4 * (2 * static_cast<int>(cta) + (sub >> 3));
+    // Warp vw takes keys 16 vw .. + 15 of a tile.  Lane l takes keys l % 8 and l % 8 + 8, of each 64-dim chunk
+    // the 16 dims 16 (l / 8): a lane needs no address but its own keys' and its own two slots of the chunk
+    // (the next chunk is a constant away), and a quarter-warp stores one slot of eight consecutive keys,
+    // which the swizzle spreads over all banks.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    const int key0 = kKeysPerV * (warp - kFirstV) + (lane & 7);
+    const int code_off = 256 * static_cast<int>(cta) + 16 * (lane >> 3), scale_off = kDL + 8 * static_cast<int>(cta);
+    const uint32_t dst0 = sw128_off(key0, 2 * (lane >> 3)), dst1 = sw128_off(key0, 2 * (lane >> 3) + 1);
     const uint32_t full = map_cta(smem_u32(&sm.v_full), 0);
-    uint4 codes[16];
-    float sc[16];
-    const auto lookup = [&](const TileWalk& tw) -> const uint8_t* {
-      return tw.w.on ? record_of(A.D, tw.w.b, tw.tile * kKeys + 32 * vw + lane, tw.w.nvis) : nullptr;
-    };
-    const auto load = [&](const uint8_t* ptr) {
+    uint4 codes[2][4];
+    float2 sc[2];
+    const uint8_t* rec[2];
+    const auto lookup = [&](const TileWalk& tw) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint8_t* r = shfl_ptr(ptr, 2 * i + hi);
-        codes[i] = make_uint4(0, 0, 0, 0);
-        sc[i] = 0.f;
-        if (r != nullptr) {
-          codes[i] = __ldg(reinterpret_cast<const uint4*>(r + code_off));
-          sc[i] = __ldg(reinterpret_cast<const float*>(r + scale_off));
+      for (int h = 0; h < 2; ++h)
+        rec[h] = tw.on() ? record_of(A, tw.w.b, tw.tile * kKeys + key0 + 8 * h, tw.w.nvis)
+                         : reinterpret_cast<const uint8_t*>(g_zero_record);
+    };
+    const auto load = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sc[h] = __ldg(reinterpret_cast<const float2*>(rec[h] + scale_off));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes[h][i] = __ldg(reinterpret_cast<const uint4*>(rec[h] + code_off + 64 * i));
+      }
+    };
+    const auto store = [&](auto slow) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 o0, o1;
+          dequant16_half<slow()>(codes[h][i], i < 2 ? sc[h].x : sc[h].y, o0, o1);
+          *reinterpret_cast<uint4*>(&sm.v[i][dst0 + 1024 * h]) = o0;
+          *reinterpret_cast<uint4*>(&sm.v[i][dst1 + 1024 * h]) = o1;
         }
       }
     };
     TileWalk tw;
     tw.start(A, sm);
-    bool on = tw.w.on;
-    load(lookup(tw));
+    bool on = tw.on();
+    lookup(tw);
+    load();
     tw.next(A);
-    bool on_next = tw.w.on;
-    const uint8_t* ptr = lookup(tw);
+    bool on_next = tw.on();
+    lookup(tw);
     for (uint32_t kk = 0; on; ++kk) {
-      bool small = false;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) small |= sc[i] < kSmallScale && sc[i] != 0.f;
-      const bool slow = __any_sync(0xffffffffu, small);
+      const bool slow = __any_sync(0xffffffffu, small_scale(sc[0].x) || small_scale(sc[0].y) || small_scale(sc[1].x) || small_scale(sc[1].y));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free, (kk & 1) ^ 1, err, &sm.abort))) break;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint4 o0, o1;
-        dequant16_half(codes[i], sc[i], slow, o0, o1);
-        const int key = 32 * vw + 2 * i + hi;
-        *reinterpret_cast<uint4*>(&sm.v[c][sw128_off(key, s0 + odd)]) = odd ? o1 : o0;
-        *reinterpret_cast<uint4*>(&sm.v[c][sw128_off(key, s0 + 1 - odd)]) = odd ? o0 : o1;
-      }
+      if (slow) store(std::true_type{});
+      else store(std::false_type{});
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full);
-      load(ptr);
+      load();
       on = on_next;
       tw.next(A);
-      on_next = tw.w.on;
-      ptr = lookup(tw);
+      on_next = tw.on();
+      lookup(tw);
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
-    // Warp kw takes keys 16 kw .. + 15: a key's 512 codes in one load (a lane per 16), the rope of four
-    // keys in another (eight lanes each).
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    const int kw = warp - kFirstK;
-    const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
-    const int scale_off = kDL + 4 * (lane >> 3), rope_off = kDL + 16 + 16 * (lane & 7);
+    // Warp kw takes keys 8 kw .. + 7, lane l key l % 8 and 16 dims of each chunk, as for V.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    const int key = kKeysPerK * (warp - kFirstK) + (lane & 7);
+    const int code_off = 16 * (lane >> 3), rope_off = kDL + 16 + 32 * (lane >> 3);
+    const uint32_t dst0 = sw128_off(key, 2 * (lane >> 3)), dst1 = sw128_off(key, 2 * (lane >> 3) + 1);
     const uint32_t full = map_cta(smem_u32(&sm.k_full), 0);
-    uint4 codes[16], rope[4];
-    float sc[16];
-    const auto lookup = [&](const TileWalk& tw) -> const uint8_t* {
-      return tw.w.on ? record_of(A.D, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 16 * kw + (lane & 15), tw.w.nvis)
-                     : nullptr;
+    uint4 codes[8], rope[2];
+    float4 sc;
+    const uint8_t* rec;
+    const auto lookup = [&](const TileWalk& tw) {
+      rec = tw.on() ? record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + key, tw.w.nvis)
+                    : reinterpret_cast<const uint8_t*>(g_zero_record);
     };
-    const auto load = [&](const uint8_t* ptr) {
+    const auto load = [&]() {
+      sc = __ldg(reinterpret_cast<const float4*>(rec + kDL));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint8_t* r = shfl_ptr(ptr, i);
-        codes[i] = make_uint4(0, 0, 0, 0);
-        sc[i] = 0.f;
-        if (r != nullptr) {
-          codes[i] = __ldg(reinterpret_cast<const uint4*>(r) + lane);
-          sc[i] = __ldg(reinterpret_cast<const float*>(r + scale_off));
-        }
-      }
+      for (int i = 0; i < 8; ++i) codes[i] = __ldg(reinterpret_cast<const uint4*>(rec + code_off + 64 * i));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* r = shfl_ptr(ptr, 4 * i + (lane >> 3));
-        rope[i] = r != nullptr ? __ldg(reinterpret_cast<const uint4*>(r + rope_off)) : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(rec + rope_off + 16 * i));
     };
-    TileWalk tw, ahead;  // the tile whose records are looked up next, and the one requested into L2
-    tw.start(A, sm);
-    ahead = tw;
-    for (int i = 0; i < kPrefetchAhead; ++i) ahead.next(A);
-    bool on = tw.w.on, bad = false;
-    load(lookup(tw));
-    tw.next(A);
-    bool on_next = tw.w.on;
-    const uint8_t* ptr = lookup(tw);
-    for (uint32_t kk = 0; on; ++kk) {
-      bool small = false;
+    const auto store = [&](auto slow) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        small |= sc[i] < kSmallScale && sc[i] != 0.f;
-        bad |= !(sc[i] <= kMaxScale);
-      }
-      const bool slow = __any_sync(0xffffffffu, small);
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         uint4 o0, o1;
-        dequant16_half(codes[i], sc[i], slow, o0, o1);
-        const int key = 16 * kw + i;
-        *reinterpret_cast<uint4*>(&sm.k[c][sw128_off(key, s0 + odd)]) = odd ? o1 : o0;
-        *reinterpret_cast<uint4*>(&sm.k[c][sw128_off(key, s0 + 1 - odd)]) = odd ? o0 : o1;
+        dequant16_half<slow()>(codes[i], i < 2 ? sc.x : i < 4 ? sc.y : i < 6 ? sc.z : sc.w, o0, o1);
+        *reinterpret_cast<uint4*>(&sm.k[i][dst0]) = o0;
+        *reinterpret_cast<uint4*>(&sm.k[i][dst1]) = o1;
       }
+    };
+    TileWalk tw;
+    tw.start(A, sm);
+    bool on = tw.on(), bad = false;
+    lookup(tw);
+    load();
+    tw.next(A);
+    bool on_next = tw.on();
+    lookup(tw);
+    for (uint32_t kk = 0; on; ++kk) {
+      bad |= !(fmaxf(fmaxf(sc.x, sc.y), fmaxf(sc.z, sc.w)) <= kMaxScale);
+      const bool slow = __any_sync(0xffffffffu, small_scale(sc.x) || small_scale(sc.y) || small_scale(sc.z) || small_scale(sc.w));
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
+      if (slow) store(std::true_type{});
+      else store(std::false_type{});
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
         uint32_t o[4];
+        uint32_t top = 0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float lo = __uint_as_float(w[x] << 16), h = __uint_as_float(w[x] & 0xFFFF0000u);
-          bad |= fmaxf(fabsf(lo), fabsf(h)) > kMaxHalf;
-          o[x] = pack_half2(lo, h);
+          top = __vmaxu2(top, w[x] & 0x7FFF7FFFu);
+          o[x] = pack_half2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xFFFF0000u));
         }
-        *reinterpret_cast<uint4*>(&sm.k[8][sw128_off(16 * kw + 4 * i + (lane >> 3), lane & 7)]) = make_uint4(o[0], o[1], o[2], o[3]);
+        bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
+        *reinterpret_cast<uint4*>(&sm.k[8][i == 0 ? dst0 : dst1]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full);
-      load(ptr);
+      load();
       on = on_next;
       tw.next(A);
-      on_next = tw.w.on;
-      ptr = lookup(tw);
-      if (lane < 16) {
-        const uint8_t* r = lookup(ahead);
-        if (r != nullptr) prefetch_l2_bulk(r, 656);
-      }
-      ahead.next(A);
+      on_next = tw.on();
+      lookup(tw);
+      if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
     if (bad) latch_error(err, SMLA_ERR_RANGE);
   } else {
@@ -754,6 +786,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     // Thread: TMEM lane L = 32 (warp % 4) + lane, which is row L % 64 and half kh = L / 64 of a tile's
     // keys (of O's dims); warps 0-3 take the first 32 columns of the half (the first 128 of O's), warps
     // 4-7 the others.  The four threads of a row agree on its running maximum.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int sp = warp & 3, wg = warp >> 2;
     const int L = 32 * sp + lane, row = L & 63, kh = L >> 6;
     const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
@@ -764,8 +797,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     // scaled by a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's
     // eight bits exactly down to 2^-23 of that element.
     const auto load_q = [&](const Walk& w, int slot) {
-      const int rows = w.ntok * H - kCtaRows * static_cast<int>(cta);
-      const int64_t first = static_cast<int64_t>(w.tok0) * H + kCtaRows * cta;
+      const int rows = w.ntok(A) * H - kCtaRows * static_cast<int>(cta);
+      const int64_t first = static_cast<int64_t>(w.tok0(A)) * H + kCtaRows * cta;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         uint4 a[4], b[4];
@@ -825,19 +858,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     Walk w;
     w.start(A, sm);
     if (A.meta != nullptr && cta == 0 && threadIdx.x == 0) A.meta[pair].ntok = 0;
-    if (w.on) load_q(w, 0);
+    if (w.on()) load_q(w, 0);
     named_bar_sync(1, 32 * kSoftmaxWarps);  // row_f
     uint32_t kk = 0, n = 0;
     bool failed = false;
-    while (w.on && !failed) {
+    while (w.on() && !failed) {
       const int grow = kCtaRows * static_cast<int>(cta) + row;  // row of the unit
-      const bool real = grow < w.ntok * H;
-      const int vis = real ? static_cast<int>(visible(A.D, w.b, w.tok0 - w.q0 + grow / H, w.n_q)) : 0;
+      const bool real = grow < w.ntok(A) * H;
+      const int vis = real ? static_cast<int>(visible(A.D, w.b, w.g * A.group + grow / H, w.n_q)) : 0;
+      const int ta = w.ta(A), tb = w.tb(A);
       // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
       const float f = fmaxf(sm.row_f[n & 1][row], 1.2e-38f);
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int tile = w.ta; tile < w.tb; ++tile, ++kk) {
+      for (int tile = ta; tile < tb; ++tile, ++kk) {
         const int buf = kk & 1;
         ok = ok && pair_wait(&sm.s_full[buf], (kk >> 1) & 1, err, &sm.abort);
         __syncwarp();
@@ -864,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         mx = mx == -INFINITY ? -INFINITY : mx * f;
         // The maximum of a row moves only when a score passes it by 2^8; only then (and on the first
         // tile) the four threads of every row compare notes.
-        const bool first = tile == w.ta;
+        const bool first = tile == ta;
         if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || mx > m + kRescale)) {
           sm.red[2 * wg + kh][row] = mx;
           if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) {
@@ -919,7 +953,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       // the next unit's queries while the last MMAs run (the last scores are read: Q is free)
       Walk nx = w;
       nx.next(A);
-      if (nx.on) load_q(nx, (n + 1) & 1);
+      if (nx.on()) load_q(nx, (n + 1) & 1);
       // ---- end of unit ----
       ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;
       __syncwarp();
@@ -929,9 +963,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const float lt = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
       const float inv = lt == 0.f ? 0.f : 1.f / lt;  // no visible key: zeros
       const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
-      const bool partial = w.ta > 0 || w.tb < w.tiles;
-      const int64_t slot = 2 * pair + (w.ta > 0 ? 0 : 1);
-      const int64_t orow = static_cast<int64_t>(w.tok0) * H + grow;
+      const bool partial = ta > 0 || tb < w.tiles();
+      const int64_t slot = 2 * pair + (ta > 0 ? 0 : 1);
+      const int64_t orow = static_cast<int64_t>(w.tok0(A)) * H + grow;
       const int d0 = 256 * kh + 128 * wg;
       if (kh == 0 && wg == 0 && real) {
         if (partial) A.part_lse[slot * kRows + grow] = lse;
@@ -964,7 +998,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       tc_fence_before();
       named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read, row_f of the next unit is written
       // the unit that goes on in the next pair: what the merge has to join
-      if (cta == 0 && threadIdx.x == 0 && w.ta == 0 && w.tb < w.tiles) A.meta[pair] = {w.us + w.tiles, sm.total, sm.pairs, w.tok0, w.ntok};
+      if (cta == 0 && threadIdx.x == 0 && ta == 0 && tb < w.tiles())
+        A.meta[pair] = {sm.x0 + w.rel + w.tiles(), sm.total, sm.pairs, w.tok0(A), w.ntok(A)};
       w = nx;
       ++n;
     }
@@ -1101,6 +1136,12 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.abs_scale = fabsf(softmax_scale) * kLog2e;
   A.sign = softmax_scale < 0.f ? -1.f : 1.f;
   A.q_vec = (reinterpret_cast<uintptr_t>(D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(D.q_pe) & 3) == 0;
+  A.records = D.pool + static_cast<int64_t>(D.layer) * D.L.layer_stride + D.L.rec_off;
+  uint32_t log2 = 0;
+  while ((1ull << log2) < static_cast<uint64_t>(D.L.block_size)) ++log2;
+  A.bs_mul = static_cast<uint32_t>((((1ull << log2) - D.L.block_size) << 32) / D.L.block_size + 1);
+  A.bs_shift1 = log2 > 0 ? 1 : 0;
+  A.bs_shift2 = log2 > 0 ? log2 - 1 : 0;
   const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
   if (split) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
