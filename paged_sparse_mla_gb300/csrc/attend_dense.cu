@@ -195,6 +195,7 @@ constexpr float kMaxScale = 65504.0f / 448.0f;
 constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
 constexpr float kSmallScale = 1.220703125e-4f;  // 2^-13: below it a scale loses bits in fp16
 constexpr int kMaxPairs = 128;
+constexpr int kRec = kDL + 16 + 2 * kDR;  // bytes of a record: codes, four scales, rope
 constexpr int kMinTiles = 2;           // key tiles a pair takes at least
 constexpr int kPrefetchAhead = 4;      // tiles requested into L2 ahead of the loads
 
@@ -425,49 +426,74 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 16 E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale rounds to 11 bits and
+// Eight E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale rounds to 11 bits and
 // the product once more (2 x 2^-11 in all).  kSlow: the scale may be so small that fp16 would hold it with
-// fewer bits, so the products are formed in fp32.
+// fewer bits, so the products are formed in fp32.  `sc`: the scale, as two halves or in fp32.
 template <bool kSlow>
-__device__ __forceinline__ void dequant16_half(const uint4& codes, float sc, uint4& o0, uint4& o1) {
-  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t ow[8];
-  const __half2 s2 = __float2half2_rn(sc);
+__device__ __forceinline__ uint4 dequant8(const uint2& codes, uint32_t sc) {
+  uint32_t o[4];
 #pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(cw[x >> 1] >> (16 * (x & 1))), __NV_E4M3);
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t w = x < 2 ? codes.x : codes.y;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (x & 1))), __NV_E4M3);
     const __half2 c = *reinterpret_cast<const __half2*>(&h);
     if constexpr (!kSlow) {
-      const __half2 y = __hmul2(c, s2);
-      ow[x] = *reinterpret_cast<const uint32_t*>(&y);
+      const __half2 y = __hmul2(c, *reinterpret_cast<const __half2*>(&sc));
+      o[x] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
       const float2 f = __half22float2(c);
-      ow[x] = pack_half2(f.x * sc, f.y * sc);
+      o[x] = pack_half2(f.x * __uint_as_float(sc), f.y * __uint_as_float(sc));
     }
   }
-  o0 = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-  o1 = make_uint4(ow[4], ow[5], ow[6], ow[7]);
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale && s != 0.f; }
 
 // What masked and unreadable positions read as: scales and rope of zero.
 __device__ uint4 g_zero_record[41];
 
-// Address of the record of position j of sequence b: zeros at or past nvis, or for a bad block id.
+// Address of the record of position j of sequence b (nullptr at or past nvis, or for a bad block id).
 __device__ __forceinline__ const uint8_t* record_of(const PairArgs& A, int b, int j, int nvis) {
   const DenseArgs& D = A.D;
-  const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_record);
-  if (j >= nvis) return zero;
+  if (j >= nvis) return nullptr;
   // j / block_size by multiplication (Granlund and Montgomery's round-up method)
   const uint32_t t = __umulhi(static_cast<uint32_t>(j), A.bs_mul);
   const int pg = static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
   const int blk = __ldg(D.block_table + static_cast<int64_t>(b) * D.bt_stride + pg);
   if (blk < 0 || blk >= D.L.num_blocks) {
     latch_error(D.err, SMLA_ERR_BAD_INDEX);
-    return zero;
+    return nullptr;
   }
-  return A.records + static_cast<int64_t>(blk) * D.L.block_stride + (j - pg * D.L.block_size) * 656;
+  return A.records + static_cast<int64_t>(blk) * D.L.block_stride + (j - pg * D.L.block_size) * kRec;
 }
+
+// The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
+// of 16, so that they lie one after another in a block and every lane knows them all from the first;
+// otherwise lane i looks up the i-th and the lanes pass the addresses around (two shuffles a record:
+// 0.447 against 0.412 ms on 304 query tokens of 8,192 positions).
+template <bool kRuns, int kN>
+struct Records {
+  const uint8_t* at;
+  int n;  // kRuns: readable records
+  __device__ __forceinline__ void find(const PairArgs& A, const TileWalk& tw, int key0, int lane) {
+    at = nullptr;
+    n = 0;
+    if (!tw.on()) return;
+    const int j = tw.tile * kKeys + key0;
+    if constexpr (kRuns) {
+      at = record_of(A, tw.w.b, j, tw.w.nvis);
+      n = at != nullptr ? min(tw.w.nvis - j, kN) : 0;
+    } else {
+      at = record_of(A, tw.w.b, j + (lane & (kN - 1)), tw.w.nvis);
+    }
+  }
+  __device__ __forceinline__ const uint8_t* get(int i) const {
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_record);
+    if constexpr (kRuns) return i < n ? at + i * kRec : zero;
+    const uint8_t* r = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), i));
+    return r != nullptr ? r : zero;
+  }
+};
 
 // The pair's range of work: every thread takes sequences, a scan over the CTA finds the total and the
 // unit in which the range begins.
@@ -531,6 +557,7 @@ __device__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
   }
 }
 
+template <bool kRuns>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_pair_kernel(const PairArgs A) {
   extern __shared__ uint8_t smem_raw[];
   PairSmem& sm = *reinterpret_cast<PairSmem*>(
@@ -645,61 +672,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          prefetch_l2_bulk(record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane, tw.w.nvis), 656);
+          const uint8_t* r = record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane, tw.w.nvis);
+          if (r != nullptr) prefetch_l2_bulk(r, kRec);
         }
         tw.next(A);
       }
     }
   } else if (warp >= kFirstV) {
     // ------------------------------ V: 128 keys x this CTA's 256 latent dims ------------------------------
-    // Warp vw takes keys 16 vw .. + 15 of a tile.  Lane l takes keys l % 8 and l % 8 + 8, of each 64-dim chunk
-    // the 16 dims 16 (l / 8): a lane needs no address but its own keys' and its own two slots of the chunk
-    // (the next chunk is a constant away), and a quarter-warp stores one slot of eight consecutive keys,
-    // which the swizzle spreads over all banks.
+    // Warp vw takes keys 16 vw .. + 15 of a tile.  A lane loads eight codes of a key, which become one
+    // 16-byte slot of a chunk: a key's 256 codes are one coalesced load, and a quarter-warp stores the
+    // eight slots of a key's chunk, which lie in different banks.  (Loads of 64 bytes from each of eight
+    // keys need no shuffles, but took 24 passes of the load pipe each instead of three; the pipe was 82% busy.)
+    // Lane 2 i + x keeps scale x of key i.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    const int key0 = kKeysPerV * (warp - kFirstV) + (lane & 7);
-    const int code_off = 256 * static_cast<int>(cta) + 16 * (lane >> 3), scale_off = kDL + 8 * static_cast<int>(cta);
-    const uint32_t dst0 = sw128_off(key0, 2 * (lane >> 3)), dst1 = sw128_off(key0, 2 * (lane >> 3) + 1);
+    constexpr int kN = kKeysPerV;
+    const int key0 = kN * (warp - kFirstV);
+    const int code_off = 256 * static_cast<int>(cta) + 8 * lane, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
+    const uint32_t dst = (lane >> 3) * kKeys * 128 + sw128_off(key0, lane & 7);
     const uint32_t full = map_cta(smem_u32(&sm.v_full), 0);
-    uint4 codes[2][4];
-    float2 sc[2];
-    const uint8_t* rec[2];
-    const auto lookup = [&](const TileWalk& tw) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        rec[h] = tw.on() ? record_of(A, tw.w.b, tw.tile * kKeys + key0 + 8 * h, tw.w.nvis)
-                         : reinterpret_cast<const uint8_t*>(g_zero_record);
-    };
+    uint2 codes[kN];
+    float sc;
+    Records<kRuns, kN> rec;
     const auto load = [&]() {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sc[h] = __ldg(reinterpret_cast<const float2*>(rec[h] + scale_off));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) codes[h][i] = __ldg(reinterpret_cast<const uint4*>(rec[h] + code_off + 64 * i));
-      }
+      for (int i = 0; i < kN; ++i) codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off));
+      sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 1) + scale_off));
     };
     const auto store = [&](auto slow) {
+      const uint32_t mine = slow() ? __float_as_uint(sc) : pack_half2(sc, sc);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 o0, o1;
-          dequant16_half<slow()>(codes[h][i], i < 2 ? sc[h].x : sc[h].y, o0, o1);
-          *reinterpret_cast<uint4*>(&sm.v[i][dst0 + 1024 * h]) = o0;
-          *reinterpret_cast<uint4*>(&sm.v[i][dst1 + 1024 * h]) = o1;
-        }
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * i + (lane >> 4));
+        *reinterpret_cast<uint4*>(&sm.v[0][0] + ((dst ^ ((i & 7) << 4)) + 128 * i)) = dequant8<slow()>(codes[i], s);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on();
-    lookup(tw);
+    rec.find(A, tw, key0, lane);
     load();
     tw.next(A);
     bool on_next = tw.on();
-    lookup(tw);
+    rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
-      const bool slow = __any_sync(0xffffffffu, small_scale(sc[0].x) || small_scale(sc[0].y) || small_scale(sc[1].x) || small_scale(sc[1].y));
+      const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free, (kk & 1) ^ 1, err, &sm.abort))) break;
       if (slow) store(std::true_type{});
       else store(std::false_type{});
@@ -710,50 +727,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       on = on_next;
       tw.next(A);
       on_next = tw.on();
-      lookup(tw);
+      rec.find(A, tw, key0, lane);
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
-    // Warp kw takes keys 8 kw .. + 7, lane l key l % 8 and 16 dims of each chunk, as for V.
+    // Warp kw takes keys 8 kw .. + 7, as for V: a key's codes are two loads, the rope of four keys another.
+    // Lane 4 i + x keeps scale x of key i.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
-    const int key = kKeysPerK * (warp - kFirstK) + (lane & 7);
-    const int code_off = 16 * (lane >> 3), rope_off = kDL + 16 + 32 * (lane >> 3);
-    const uint32_t dst0 = sw128_off(key, 2 * (lane >> 3)), dst1 = sw128_off(key, 2 * (lane >> 3) + 1);
+    constexpr int kN = kKeysPerK;
+    const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
+    const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
     const uint32_t full = map_cta(smem_u32(&sm.k_full), 0);
-    uint4 codes[8], rope[2];
-    float4 sc;
-    const uint8_t* rec;
-    const auto lookup = [&](const TileWalk& tw) {
-      rec = tw.on() ? record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + key, tw.w.nvis)
-                    : reinterpret_cast<const uint8_t*>(g_zero_record);
-    };
+    uint2 codes[kN][2];
+    uint4 rope[2];
+    float sc;
+    Records<kRuns, kN> rec;
     const auto load = [&]() {
-      sc = __ldg(reinterpret_cast<const float4*>(rec + kDL));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) codes[i] = __ldg(reinterpret_cast<const uint4*>(rec + code_off + 64 * i));
+      for (int i = 0; i < kN; ++i) {
+        const uint8_t* r = rec.get(i) + 8 * lane;
+        codes[i][0] = __ldg(reinterpret_cast<const uint2*>(r));
+        codes[i][1] = __ldg(reinterpret_cast<const uint2*>(r + 256));
+      }
+      sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3)));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(rec + rope_off + 16 * i));
+      for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
     const auto store = [&](auto slow) {
+      const uint32_t mine = slow() ? __float_as_uint(sc) : pack_half2(sc, sc);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint4 o0, o1;
-        dequant16_half<slow()>(codes[i], i < 2 ? sc.x : i < 4 ? sc.y : i < 6 ? sc.z : sc.w, o0, o1);
-        *reinterpret_cast<uint4*>(&sm.k[i][dst0]) = o0;
-        *reinterpret_cast<uint4*>(&sm.k[i][dst1]) = o1;
+      for (int i = 0; i < kN; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h + (lane >> 4));
+          *reinterpret_cast<uint4*>(&sm.k[0][0] + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h)) = dequant8<slow()>(codes[i][h], s);
+        }
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on(), bad = false;
-    lookup(tw);
+    rec.find(A, tw, key0, lane);
     load();
     tw.next(A);
     bool on_next = tw.on();
-    lookup(tw);
+    rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
-      bad |= !(fmaxf(fmaxf(sc.x, sc.y), fmaxf(sc.z, sc.w)) <= kMaxScale);
-      const bool slow = __any_sync(0xffffffffu, small_scale(sc.x) || small_scale(sc.y) || small_scale(sc.z) || small_scale(sc.w));
+      bad |= !(sc <= kMaxScale);
+      const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
       if (slow) store(std::true_type{});
       else store(std::false_type{});
@@ -768,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           o[x] = pack_half2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xFFFF0000u));
         }
         bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
-        *reinterpret_cast<uint4*>(&sm.k[8][i == 0 ? dst0 : dst1]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(&sm.k[8][sw128_off(kN * kw + 4 * i + (lane >> 3), lane & 7)]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async();
       __syncwarp();
@@ -777,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       on = on_next;
       tw.next(A);
       on_next = tw.on();
-      lookup(tw);
+      rec.find(A, tw, key0, lane);
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
     if (bad) latch_error(err, SMLA_ERR_RANGE);
@@ -1104,17 +1125,18 @@ constexpr size_t kMetaBytes = (kMaxPairs * sizeof(PairMeta) + 255) / 256 * 256;
 constexpr size_t kPartLseBytes = 2 * kMaxPairs * kRows * sizeof(float);
 constexpr size_t kPartOutBytes = size_t(2) * kMaxPairs * kRows * kDL * sizeof(float);
 
-smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* workspace, size_t workspace_bytes,
-                                cudaStream_t s) {
-  static std::atomic<int> pairs_of[kMaxDeviceSlots] = {};  // pairs resident at once
+template <bool kRuns>
+smla_status_t resident_pairs(int* out) {
+  static std::atomic<int> pairs_of[kMaxDeviceSlots] = {};
   const int dev = current_device_index();
   if (dev < 0) return SMLA_ERR_CUDA;
   int pairs = pairs_of[dev].load(std::memory_order_acquire);
   if (pairs == 0) {
-    if (cudaFuncSetAttribute(dense_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPairSmemBytes)) != cudaSuccess)
+    const auto kernel = dense_pair_kernel<kRuns>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPairSmemBytes)) != cudaSuccess)
       return SMLA_ERR_CUDA;
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, dense_pair_kernel) != cudaSuccess) return SMLA_ERR_CUDA;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return SMLA_ERR_CUDA;
     if (fa.numRegs < kLaunchRegs) return SMLA_ERR_UNSUPPORTED;  // setmaxnreg.inc draws on the launch's registers
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * kMaxPairs);
@@ -1126,10 +1148,20 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&pairs, dense_pair_kernel, &cfg) != cudaSuccess || pairs <= 0) return SMLA_ERR_CUDA;
+    if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0) return SMLA_ERR_CUDA;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     pairs_of[dev].store(pairs, std::memory_order_release);
   }
+  *out = pairs;
+  return SMLA_OK;
+}
+
+smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                cudaStream_t s) {
+  const bool runs = D.L.block_size % 16 == 0;
+  int pairs = 0;  // resident at once
+  const smla_status_t st = runs ? resident_pairs<true>(&pairs) : resident_pairs<false>(&pairs);
+  if (st != SMLA_OK) return st;
   PairArgs A{};
   A.D = D;
   A.group = kRows / D.n_heads;
@@ -1149,7 +1181,8 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
     A.part_lse = reinterpret_cast<float*>(w + kMetaBytes);
     A.part_out = reinterpret_cast<float*>(w + kMetaBytes + kPartLseBytes);
   }
-  dense_pair_kernel<<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
+  if (runs) dense_pair_kernel<true><<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
+  else dense_pair_kernel<false><<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   if (split) {
     dense_merge_kernel<<<8 * device_sm_count(), kMergeThreads, 0, s>>>(A.meta, A.part_lse, A.part_out, pairs, D.n_heads, D.out, D.lse);
