@@ -386,19 +386,28 @@ __device__ __forceinline__ void pair_drain(uint64_t* bar, uint32_t parity) {
   while (!mbar_try_wait(addr, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {
   }
 }
-// D (+)= A . B over both CTAs.  The operands move by constant byte offsets from a descriptor's low word
-// (its address field counts 16 bytes); the sums stand inside the statement, so that the compiler does not
-// keep dozens of 64-bit descriptors.
+// D (+)= A . B over both CTAs, issued by the lane whose `elected` is set; the whole warp comes here, so
+// that the operands live in uniform registers (issued from a branch of one lane, each instruction moved
+// them there again and took about 60 cycles whatever its size).  The operands move by constant byte
+// offsets from a descriptor's low word (its address field counts 16 bytes); the loops around are short,
+// since this warp shares the instruction cache with 24 others (all 36 products of a tile unrolled were
+// issued at 65 cycles each).
 template <int kAOff, int kBOff>
 __device__ __forceinline__ void mma2_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                         uint32_t idesc, uint32_t accumulate) {
+                                         uint32_t idesc, uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
       "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
-      "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(kAOff >> 4), "n"(kBOff >> 4)
+      "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(kAOff >> 4), "n"(kBOff >> 4),
+      "r"(elected)
       : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
 }
 // f(integral_constant 0) .. f(integral_constant N - 1)
 template <int N, int I = 0, typename F>
@@ -408,12 +417,13 @@ __device__ __forceinline__ void unrolled(F&& f) {
     unrolled<N, I + 1>(f);
   }
 }
-// Arrive on `bar` of both CTAs when every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void commit2(uint64_t* bar) {
+// Arrive on `bar` of both CTAs when every MMA issued so far by the elected lane has completed.
+__device__ __forceinline__ void commit2(uint64_t* bar, uint32_t elected) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3)), "r"(elected)
       : "memory");
 }
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -562,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
   extern __shared__ uint8_t smem_raw[];
   PairSmem& sm = *reinterpret_cast<PairSmem*>(
       smem_raw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u)) & 1023u));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform to the compiler
   const uint32_t cta = cluster_rank();
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   unsigned* err = A.D.err;
@@ -593,13 +603,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before either arrives on the other's
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_slot, 0);
   const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
 
   if (warp >= kIssuer) {
-    // ------------------------------ MMA issuer (one thread of the first CTA) ------------------------------
+    // ------------------------------ MMA issuer (one warp of the first CTA) ------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
-    if (warp == kIssuer && lane == 0 && cta == 0) {
+    if (warp == kIssuer && cta == 0) {
+      const uint32_t elected = elect_one();
       const uint32_t idesc1 = make_idesc(128, kKeys, 0, 0, 0, 0);  // fp16, both K-major
       const uint32_t idesc2 = make_idesc(128, 256, 0, 0, 0, 1);    // fp16, P K-major, V MN-major
       const uint64_t dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024), dk = sw128_desc(smem_u32(sm.k[0]), 16, 1024);
@@ -607,39 +618,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const uint32_t dq_lo = static_cast<uint32_t>(dq), dk_lo = static_cast<uint32_t>(dk), dp_lo = static_cast<uint32_t>(dp), dv_lo = static_cast<uint32_t>(dv);
       const uint32_t dq_hi = static_cast<uint32_t>(dq >> 32), dk_hi = static_cast<uint32_t>(dk >> 32), dp_hi = static_cast<uint32_t>(dp >> 32), dv_hi = static_cast<uint32_t>(dv >> 32);
       uint32_t k1 = 0, k2 = 0, n = 0;  // MMA1s and MMA2s issued, units begun
+      const auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, pair_wait(bar, parity, err, &sm.abort));
+      };
       // S = Q . K^T of tile k1 into score buffer k1 % 2
       const auto mma1 = [&]() -> bool {
-        if (!pair_wait(&sm.k_full, k1 & 1, err, &sm.abort)) return false;
-        if (!pair_wait(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1, err, &sm.abort)) return false;
+        if (!wait_all(&sm.k_full, k1 & 1)) return false;
+        if (!wait_all(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1)) return false;
         tc_fence_after();
         const uint32_t ts = tmem_s + (k1 & 1) * 64;
-        unrolled<4 * kChunks>([&](auto i) {
-          constexpr int c = i() / 4, x = i() % 4;
-          mma2_f16<c * kCtaRows * 128 + x * 32, c * kCtaKeys * 128 + x * 32>(ts, dq_lo, dq_hi, dk_lo, dk_hi, idesc1, i() != 0);
-        });
-        commit2(&sm.s_full[k1 & 1]);
-        commit2(&sm.k_free);
+#pragma unroll 1
+        for (int c = 0; c < kChunks; ++c)
+          unrolled<4>([&](auto x) {
+            mma2_f16<x() * 32, x() * 32>(ts, dq_lo + c * (kCtaRows * 128 >> 4), dq_hi, dk_lo + c * (kCtaKeys * 128 >> 4), dk_hi,
+                                         idesc1, (c | x()) != 0, elected);
+          });
+        commit2(&sm.s_full[k1 & 1], elected);
+        commit2(&sm.k_free, elected);
         ++k1;
         return true;
       };
       // O (+)= P . V of tile k2
       const auto mma2 = [&](bool first) -> bool {
-        if (!pair_wait(&sm.v_full, k2 & 1, err, &sm.abort)) return false;
-        if (!pair_wait(&sm.p_full, k2 & 1, err, &sm.abort)) return false;
+        if (!wait_all(&sm.v_full, k2 & 1)) return false;
+        if (!wait_all(&sm.p_full, k2 & 1)) return false;
         tc_fence_after();
-        unrolled<2 * (kKeys / 16)>([&](auto i) {
-          constexpr int x = i() / 2, j = i() % 2;
-          mma2_f16<(x >> 2) * kCtaRows * 128 + (x & 3) * 32, 2 * j * kKeys * 128 + x * 2048>(
-              tmem_o + j * 128, dp_lo, dp_hi, dv_lo, dv_hi, idesc2, !(first && x == 0));
-        });
-        commit2(&sm.v_free);
+#pragma unroll 1
+        for (int c = 0; c < kKeys / 64; ++c)
+          unrolled<8>([&](auto i) {
+            constexpr int x = i() / 2, j = i() % 2;
+            mma2_f16<x * 32, 2 * j * kKeys * 128 + x * 2048>(tmem_o + j * 128, dp_lo + c * (kCtaRows * 128 >> 4), dp_hi,
+                                                              dv_lo + c * (4 * 2048 >> 4), dv_hi, idesc2, !(first && (c | x) == 0),
+                                                              elected);
+          });
+        commit2(&sm.v_free, elected);
         ++k2;
         return true;
       };
       Walk w;
       bool ok = true;
       for (w.start(A, sm); w.on() && ok; w.next(A), ++n) {
-        ok = pair_wait(&sm.q_full, n & 1, err, &sm.abort) && mma1();
+        ok = wait_all(&sm.q_full, n & 1) && mma1();
         const int ta = w.ta(A), tb = w.tb(A);
         for (int t = ta; t < tb && ok; ++t) {
           if (t + 1 < tb) ok = mma1();  // the next tile's scores while this one's softmax works
@@ -647,9 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         }
       }
       if (k1 > 0) {  // nothing may still read or write the pair's memory when it leaves
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                         smem_u32(&sm.final_bar))
-                     : "memory");
+        commit2(&sm.final_bar, elected);
         pair_drain(&sm.final_bar, 0);
       }
     } else if (warp == kIssuer + 1) {
