@@ -459,8 +459,8 @@ __device__ __forceinline__ uint4 dequant8(const uint2& codes, uint32_t sc) {
 }
 __device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale && s != 0.f; }
 
-// What masked and unreadable positions read as: scales and rope of zero.
-__device__ uint4 g_zero_record[41];
+// What unreadable records read as (bad block ids, and nothing left to read): 16 records of zeros.
+__device__ uint4 g_zero_records[16 * 41];
 
 // Address of the record of position j of sequence b (nullptr at or past nvis, or for a bad block id).
 __device__ __forceinline__ const uint8_t* record_of(const PairArgs& A, int b, int j, int nvis) {
@@ -478,32 +478,46 @@ __device__ __forceinline__ const uint8_t* record_of(const PairArgs& A, int b, in
 }
 
 // The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
-// of 16, so that they lie one after another in a block and every lane knows them all from the first;
-// otherwise lane i looks up the i-th and the lanes pass the addresses around (two shuffles a record:
-// 0.447 against 0.412 ms on 304 query tokens of 8,192 positions).
+// of 16, so that they lie one after another in a block and every lane knows them all from the first
+// (`n` of them hold visible positions; what follows in the block is read too and zeroed by the caller).
+// Otherwise lane i looks up the i-th and the lanes pass the addresses around, two shuffles a record.
 template <bool kRuns, int kN>
 struct Records {
   const uint8_t* at;
-  int n;  // kRuns: readable records
+  int n;
   __device__ __forceinline__ void find(const PairArgs& A, const TileWalk& tw, int key0, int lane) {
-    at = nullptr;
-    n = 0;
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_records);
+    at = zero;
+    n = kN;
     if (!tw.on()) return;
     const int j = tw.tile * kKeys + key0;
-    if constexpr (kRuns) {
-      at = record_of(A, tw.w.b, j, tw.w.nvis);
-      n = at != nullptr ? min(tw.w.nvis - j, kN) : 0;
-    } else {
-      at = record_of(A, tw.w.b, j + (lane & (kN - 1)), tw.w.nvis);
-    }
+    const uint8_t* r = record_of(A, tw.w.b, kRuns ? j : j + (lane & (kN - 1)), tw.w.nvis);
+    if (r == nullptr) return;
+    at = r;
+    if constexpr (kRuns) n = min(tw.w.nvis - j, kN);
   }
   __device__ __forceinline__ const uint8_t* get(int i) const {
-    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_record);
-    if constexpr (kRuns) return i < n ? at + i * kRec : zero;
-    const uint8_t* r = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), i));
-    return r != nullptr ? r : zero;
+    if constexpr (kRuns) return at + i * kRec;
+    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), i));
   }
 };
+
+// (a, b) * (c, c) + (d, d) and (a, b) + (c, d) as packed fp32 operations
+__device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmov.b64 z, {%4, %4};\n\t"
+      "fma.rn.f32x2 %0, x, y, z;\n\t}"
+      : "=l"(r)
+      : "f"(a.x), "f"(a.y), "f"(c), "f"(d));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tadd.rn.f32x2 %0, x, y;\n\t}"
+      : "=l"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
+}
 
 // The pair's range of work: every thread takes sequences, a scan over the CTA finds the total and the
 // unit in which the range begins.
@@ -711,28 +725,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     uint2 codes[kN];
     float sc;
     Records<kRuns, kN> rec;
-    const auto load = [&]() {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off));
+    int n = kN;  // visible records among the loaded ones
+    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off)); };
+    const auto load_rest = [&]() {
       sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 1) + scale_off));
+      n = rec.n;
     };
+    // Stores a tile and asks for the next: a key's registers take their next codes as soon as they are stored.
     const auto store = [&](auto slow) {
       const uint32_t mine = slow() ? __float_as_uint(sc) : pack_half2(sc, sc);
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * i + (lane >> 4));
         *reinterpret_cast<uint4*>(&sm.v[0][0] + ((dst ^ ((i & 7) << 4)) + 128 * i)) = dequant8<slow()>(codes[i], s);
+        load(i);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on();
     rec.find(A, tw, key0, lane);
-    load();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) load(i);
+    load_rest();
     tw.next(A);
     bool on_next = tw.on();
     rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
+      if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (i >= n) codes[i] = make_uint2(0, 0);
+        if ((lane >> 1) >= n) sc = 0.f;
+      }
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free, (kk & 1) ^ 1, err, &sm.abort))) break;
       if (slow) store(std::true_type{});
@@ -740,7 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full);
-      load();
+      load_rest();
       on = on_next;
       tw.next(A);
       on_next = tw.on();
@@ -759,14 +784,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     uint4 rope[2];
     float sc;
     Records<kRuns, kN> rec;
-    const auto load = [&]() {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint8_t* r = rec.get(i) + 8 * lane;
-        codes[i][0] = __ldg(reinterpret_cast<const uint2*>(r));
-        codes[i][1] = __ldg(reinterpret_cast<const uint2*>(r + 256));
-      }
+    int n = kN;  // visible records among the loaded ones
+    const auto load = [&](int i) {
+      const uint8_t* r = rec.get(i) + 8 * lane;
+      codes[i][0] = __ldg(reinterpret_cast<const uint2*>(r));
+      codes[i][1] = __ldg(reinterpret_cast<const uint2*>(r + 256));
+    };
+    const auto load_rest = [&]() {
       sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3)));
+      n = rec.n;
 #pragma unroll
       for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
@@ -779,17 +805,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h + (lane >> 4));
           *reinterpret_cast<uint4*>(&sm.k[0][0] + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h)) = dequant8<slow()>(codes[i][h], s);
         }
+        load(i);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on(), bad = false;
     rec.find(A, tw, key0, lane);
-    load();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) load(i);
+    load_rest();
     tw.next(A);
     bool on_next = tw.on();
     rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
+      if (n < kN) {  // the end of a context
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (i >= n) codes[i][0] = codes[i][1] = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
+        if ((lane >> 2) >= n) sc = 0.f;
+      }
       bad |= !(sc <= kMaxScale);
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
@@ -811,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full);
-      load();
+      load_rest();
       on = on_next;
       tw.next(A);
       on_next = tw.on();
@@ -969,15 +1007,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         }
         const float mu = m == -INFINITY ? 0.f : m;
         uint32_t pw[16];
-        float l0 = 0.f, l1 = 0.f;
+        float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(r[i]), f, -mu)), p1 = fast_exp2(fmaf(__uint_as_float(r[i + 1]), f, -mu));
-          l0 += p0;
-          l1 += p1;
-          pw[i / 2] = pack_half2(p0, p1);
+          const float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f, -mu);
+          const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          ls = add2(ls, p);
+          pw[i / 2] = pack_half2(p.x, p.y);
         }
-        l += l0 + l1;
+        l += ls.x + ls.y;
         if (kk > 0) ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;  // P is read
 #pragma unroll
         for (int v = 0; v < 4; ++v)
