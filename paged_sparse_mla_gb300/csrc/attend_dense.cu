@@ -4,6 +4,7 @@
 // attention is MQA over the latent; V is the latent.  [GLM-5.3 "How to try"]: a prompt that fits the
 // top-k attends over all of its positions; here that holds at any length.
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -206,8 +207,9 @@ struct __align__(1024) PairSmem {
   uint8_t p[2][kCtaRows * 128];        // chunk c: [64 rows][keys 64 c .. 64 c + 63]
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
-  uint64_t k_full, v_full, p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
-  uint64_t k_free, v_free, s_full[2];                  // completed by the MMAs in both CTAs
+  // K is handed over in two parts, latent dims 0-255 and the rest with the rope, V in keys 0-63 and 64-127
+  uint64_t k_full[2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
+  uint64_t k_free[2], v_free[2], s_full[2];                  // completed by the MMAs in both CTAs
   uint64_t final_bar;
   int64_t x0, total;                   // start of the pair's range of work; all work, over `pairs` pairs
   int pairs, b, g, rel, len;           // the range's first unit and its position (see Walk)
@@ -462,39 +464,42 @@ __device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale &&
 // What unreadable records read as (bad block ids, and nothing left to read): 16 records of zeros.
 __device__ uint4 g_zero_records[16 * 41];
 
-// Address of the record of position j of sequence b (nullptr at or past nvis, or for a bad block id).
-__device__ __forceinline__ const uint8_t* record_of(const PairArgs& A, int b, int j, int nvis) {
-  const DenseArgs& D = A.D;
-  if (j >= nvis) return nullptr;
-  // j / block_size by multiplication (Granlund and Montgomery's round-up method)
+// Page of position j: j / block_size by multiplication (Granlund and Montgomery's round-up method).
+__device__ __forceinline__ int page_of(const PairArgs& A, int j) {
   const uint32_t t = __umulhi(static_cast<uint32_t>(j), A.bs_mul);
-  const int pg = static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
-  const int blk = __ldg(D.block_table + static_cast<int64_t>(b) * D.bt_stride + pg);
-  if (blk < 0 || blk >= D.L.num_blocks) {
-    latch_error(D.err, SMLA_ERR_BAD_INDEX);
-    return nullptr;
-  }
-  return A.records + static_cast<int64_t>(blk) * D.L.block_stride + (j - pg * D.L.block_size) * kRec;
+  return static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
 }
 
 // The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
 // of 16, so that they lie one after another in a block and every lane knows them all from the first
 // (`n` of them hold visible positions; what follows in the block is read too and zeroed by the caller).
 // Otherwise lane i looks up the i-th and the lanes pass the addresses around, two shuffles a record.
+// find() asks for the block id, take() turns it into the address: a tile later, so that nothing waits for
+// the block table.
 template <bool kRuns, int kN>
 struct Records {
   const uint8_t* at;
-  int n;
+  int blk, off, n;  // blk = INT_MIN: past the visible positions
   __device__ __forceinline__ void find(const PairArgs& A, const TileWalk& tw, int key0, int lane) {
-    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_records);
-    at = zero;
-    n = kN;
+    blk = INT_MIN;
     if (!tw.on()) return;
-    const int j = tw.tile * kKeys + key0;
-    const uint8_t* r = record_of(A, tw.w.b, kRuns ? j : j + (lane & (kN - 1)), tw.w.nvis);
-    if (r == nullptr) return;
-    at = r;
-    if constexpr (kRuns) n = min(tw.w.nvis - j, kN);
+    const int j = tw.tile * kKeys + key0 + (kRuns ? 0 : lane & (kN - 1));
+    if (j >= tw.w.nvis) return;
+    const int pg = page_of(A, j);
+    off = (j - pg * A.D.L.block_size) * kRec;
+    n = kRuns ? min(tw.w.nvis - j, kN) : kN;
+    blk = max(__ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg), -1);
+  }
+  // returns how many of the records hold visible positions
+  __device__ __forceinline__ int take(const PairArgs& A) {
+    at = reinterpret_cast<const uint8_t*>(g_zero_records);
+    if (blk == INT_MIN) return kN;
+    if (blk < 0 || blk >= A.D.L.num_blocks) {
+      latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
+      return kN;
+    }
+    at = A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + off;
+    return n;
   }
   __device__ __forceinline__ const uint8_t* get(int i) const {
     if constexpr (kRuns) return at + i * kRec;
@@ -591,14 +596,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   unsigned* err = A.D.err;
   if (threadIdx.x == 0) {
-    mbar_init(&sm.k_full, 2 * kKWarps);
-    mbar_init(&sm.v_full, 2 * kVWarps);
     mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.q_full, 2 * kSoftmaxWarps);
-    mbar_init(&sm.k_free, 1);
-    mbar_init(&sm.v_free, 1);
     mbar_init(&sm.final_bar, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], 2 * kKWarps);
+      mbar_init(&sm.v_full[i], kVWarps);  // half of the warps of each CTA
+      mbar_init(&sm.k_free[i], 1);
+      mbar_init(&sm.v_free[i], 1);
       mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
       mbar_init(&sm.s_full[i], 1);
     }
@@ -637,35 +642,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       };
       // S = Q . K^T of tile k1 into score buffer k1 % 2
       const auto mma1 = [&]() -> bool {
-        if (!wait_all(&sm.k_full, k1 & 1)) return false;
         if (!wait_all(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1)) return false;
-        tc_fence_after();
         const uint32_t ts = tmem_s + (k1 & 1) * 64;
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c)
-          unrolled<4>([&](auto x) {
-            mma2_f16<x() * 32, x() * 32>(ts, dq_lo + c * (kCtaRows * 128 >> 4), dq_hi, dk_lo + c * (kCtaKeys * 128 >> 4), dk_hi,
-                                         idesc1, (c | x()) != 0, elected);
-          });
-        commit2(&sm.s_full[k1 & 1], elected);
-        commit2(&sm.k_free, elected);
+        for (int part = 0; part < 2; ++part) {
+          if (!wait_all(&sm.k_full[part], k1 & 1)) return false;
+          tc_fence_after();
+          const int end = part == 0 ? 4 : kChunks;
+#pragma unroll 1
+          for (int c = 4 * part; c < end; ++c)
+            unrolled<4>([&](auto x) {
+              mma2_f16<x() * 32, x() * 32>(ts, dq_lo + c * (kCtaRows * 128 >> 4), dq_hi, dk_lo + c * (kCtaKeys * 128 >> 4), dk_hi,
+                                           idesc1, (c | x()) != 0, elected);
+            });
+          if (part == 1) commit2(&sm.s_full[k1 & 1], elected);
+          commit2(&sm.k_free[part], elected);
+        }
         ++k1;
         return true;
       };
       // O (+)= P . V of tile k2
       const auto mma2 = [&](bool first) -> bool {
-        if (!wait_all(&sm.v_full, k2 & 1)) return false;
         if (!wait_all(&sm.p_full, k2 & 1)) return false;
-        tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kKeys / 64; ++c)
+        for (int part = 0; part < 2; ++part) {
+          if (!wait_all(&sm.v_full[part], k2 & 1)) return false;
+          tc_fence_after();
           unrolled<8>([&](auto i) {
             constexpr int x = i() / 2, j = i() % 2;
-            mma2_f16<x * 32, 2 * j * kKeys * 128 + x * 2048>(tmem_o + j * 128, dp_lo + c * (kCtaRows * 128 >> 4), dp_hi,
-                                                              dv_lo + c * (4 * 2048 >> 4), dv_hi, idesc2, !(first && (c | x) == 0),
-                                                              elected);
+            mma2_f16<x * 32, 2 * j * kKeys * 128 + x * 2048>(tmem_o + j * 128, dp_lo + part * (kCtaRows * 128 >> 4), dp_hi,
+                                                              dv_lo + part * (4 * 2048 >> 4), dv_hi, idesc2,
+                                                              !(first && (part | x) == 0), elected);
           });
-        commit2(&sm.v_free, elected);
+          commit2(&sm.v_free[part], elected);
+        }
         ++k2;
         return true;
       };
@@ -703,8 +713,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint8_t* r = record_of(A, tw.w.b, tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane, tw.w.nvis);
-          if (r != nullptr) prefetch_l2_bulk(r, kRec);
+          const int j = tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane;
+          if (j < tw.w.nvis) {
+            const int pg = page_of(A, j);
+            const int blk = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg);
+            if (blk >= 0 && blk < A.D.L.num_blocks)
+              prefetch_l2_bulk(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + (j - pg * A.D.L.block_size) * kRec, kRec);
+          }
         }
         tw.next(A);
       }
@@ -721,19 +736,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     const int key0 = kN * (warp - kFirstV);
     const int code_off = 256 * static_cast<int>(cta) + 8 * lane, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
     const uint32_t dst = (lane >> 3) * kKeys * 128 + sw128_off(key0, lane & 7);
-    const uint32_t full = map_cta(smem_u32(&sm.v_full), 0);
     uint2 codes[kN];
     float sc;
     Records<kRuns, kN> rec;
-    int n = kN;  // visible records among the loaded ones
     const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off)); };
-    const auto load_rest = [&]() {
-      sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 1) + scale_off));
-      n = rec.n;
-    };
+    const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 1) + scale_off)); };
     // Stores a tile and asks for the next: a key's registers take their next codes as soon as they are stored.
-    const auto store = [&](auto slow) {
-      const uint32_t mine = slow() ? __float_as_uint(sc) : pack_half2(sc, sc);
+    const auto store = [&](auto slow, uint32_t mine) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * i + (lane >> 4));
@@ -741,15 +750,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         load(i);
       }
     };
+    const int part = (warp - kFirstV) / (kVWarps / 2);
+    const uint32_t full = map_cta(smem_u32(&sm.v_full[part]), 0);
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on();
     rec.find(A, tw, key0, lane);
+    int n = rec.take(A);  // visible records among the loaded ones
 #pragma unroll
     for (int i = 0; i < kN; ++i) load(i);
-    load_rest();
+    load_scale();
     tw.next(A);
-    bool on_next = tw.on();
     rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
       if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
@@ -759,16 +770,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if ((lane >> 1) >= n) sc = 0.f;
       }
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free, (kk & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{});
-      else store(std::false_type{});
+      const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
+      n = rec.take(A);
+      on = tw.on();
+      load_scale();
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free[part], (kk & 1) ^ 1, err, &sm.abort))) break;
+      if (slow) store(std::true_type{}, mine);
+      else store(std::false_type{}, mine);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full);
-      load_rest();
-      on = on_next;
       tw.next(A);
-      on_next = tw.on();
       rec.find(A, tw, key0, lane);
     }
   } else if (warp >= kFirstK) {
@@ -779,50 +791,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     constexpr int kN = kKeysPerK;
     const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
     const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
-    const uint32_t full = map_cta(smem_u32(&sm.k_full), 0);
-    uint2 codes[kN][2];
+    const uint32_t full[2] = {map_cta(smem_u32(&sm.k_full[0]), 0), map_cta(smem_u32(&sm.k_full[1]), 0)};
+    uint2 codes[2][kN];
     uint4 rope[2];
     float sc;
     Records<kRuns, kN> rec;
-    int n = kN;  // visible records among the loaded ones
-    const auto load = [&](int i) {
-      const uint8_t* r = rec.get(i) + 8 * lane;
-      codes[i][0] = __ldg(reinterpret_cast<const uint2*>(r));
-      codes[i][1] = __ldg(reinterpret_cast<const uint2*>(r + 256));
+    const auto load = [&](int h, int i) { codes[h][i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + 256 * h + 8 * lane)); };
+    const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3))); };
+    const auto load_rope = [&](int i) {
+      rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
-    const auto load_rest = [&]() {
-      sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3)));
-      n = rec.n;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
-    };
-    const auto store = [&](auto slow) {
-      const uint32_t mine = slow() ? __float_as_uint(sc) : pack_half2(sc, sc);
+    const auto store = [&](auto slow, auto h, uint32_t mine) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h + (lane >> 4));
-          *reinterpret_cast<uint4*>(&sm.k[0][0] + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h)) = dequant8<slow()>(codes[i][h], s);
-        }
-        load(i);
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h() + (lane >> 4));
+        *reinterpret_cast<uint4*>(&sm.k[0][0] + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h())) = dequant8<slow()>(codes[h()][i], s);
+        load(h(), i);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on(), bad = false;
     rec.find(A, tw, key0, lane);
+    int n = rec.take(A);  // visible records among the loaded ones
 #pragma unroll
-    for (int i = 0; i < kN; ++i) load(i);
-    load_rest();
+    for (int i = 0; i < kN; ++i) {
+      load(0, i);
+      load(1, i);
+    }
+    load_scale();
+    load_rope(0);
+    load_rope(1);
     tw.next(A);
-    bool on_next = tw.on();
     rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
       if (n < kN) {  // the end of a context
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          if (i >= n) codes[i][0] = codes[i][1] = make_uint2(0, 0);
+          if (i >= n) codes[0][i] = codes[1][i] = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
@@ -830,9 +836,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       }
       bad |= !(sc <= kMaxScale);
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free, (kk & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{});
-      else store(std::false_type{});
+      const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
+      n = rec.take(A);
+      on = tw.on();
+      load_scale();
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free[0], (kk & 1) ^ 1, err, &sm.abort))) break;
+      if (slow) store(std::true_type{}, std::integral_constant<int, 0>{}, mine);
+      else store(std::false_type{}, std::integral_constant<int, 0>{}, mine);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(full[0]);
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free[1], (kk & 1) ^ 1, err, &sm.abort))) break;
+      if (slow) store(std::true_type{}, std::integral_constant<int, 1>{}, mine);
+      else store(std::false_type{}, std::integral_constant<int, 1>{}, mine);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
@@ -845,14 +861,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         }
         bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
         *reinterpret_cast<uint4*>(&sm.k[8][sw128_off(kN * kw + 4 * i + (lane >> 3), lane & 7)]) = make_uint4(o[0], o[1], o[2], o[3]);
+        load_rope(i);
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_cluster(full);
-      load_rest();
-      on = on_next;
+      if (lane == 0) arrive_cluster(full[1]);
       tw.next(A);
-      on_next = tw.on();
       rec.find(A, tw, key0, lane);
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
@@ -989,7 +1003,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           m = mn;
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O holds the tiles before this one once their last MMA is done; this tile's waits for p_full
-            ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;
+            ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -1016,7 +1030,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           pw[i / 2] = pack_half2(p.x, p.y);
         }
         l += ls.x + ls.y;
-        if (kk > 0) ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;  // P is read
+        if (kk > 0) ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;  // P is read
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           *reinterpret_cast<uint4*>(&sm.p[kh][sw128_off(row, 4 * wg + v)]) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
@@ -1031,7 +1045,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       nx.next(A);
       if (nx.on()) load_q(nx, (n + 1) & 1);
       // ---- end of unit ----
-      ok = pair_wait(&sm.v_free, (kk - 1) & 1, err, &sm.abort) && ok;
+      ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;
       __syncwarp();
       tc_fence_after();
       sm.red[2 * wg + kh][row] = l;
