@@ -179,16 +179,25 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // the columns, lanes 64-127 the second.  So O (64 rows x 512 dims in fp32) takes 256 tensor-memory
 // columns of each CTA, which leaves room for two score buffers; with one SM per 128 rows it would
 // fill all 512.
+//
+// K and V are the same latents, but a CTA needs 64 keys x 512 dims of them as K and 128 keys x 256 dims
+// as V, and one MMA reads the same addresses in both CTAs.  So a tile buffer holds the CTA's own keys
+// in eight 64-dim chunks (and the rope in a ninth), and once S is formed, the half of the chunks that
+// the CTA does not need as V makes room for the other CTA's keys: in the first CTA chunks 0-3 are
+// already V's keys 0-63 of its dims 0-255 and chunks 4-7 are refilled with keys 64-127 of the same
+// dims; in the second, chunks 4-7 are keys 64-127 of dims 256-511 and chunks 0-3 are refilled with
+// keys 0-63 of those.  The rope chunk, free then too, takes the first half of P.  That leaves shared
+// memory for two tile buffers beside the queries.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128, kKeys = 128;      // of a pair
 constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
 constexpr int kDL = 512, kDR = 64, kChunks = 9;  // 64-dim chunks: 8 latent, 1 rope
 constexpr int kSoftmaxWarps = 8, kKWarps = 8, kVWarps = 8;
-constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kKeys / kVWarps;  // of a warp, in a tile
+constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kCtaKeys / kVWarps;  // of a warp, in a tile
 constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
 constexpr int kThreads = 32 * (kIssuer + 4);  // the issuer's warpgroup: one warp issues, three only lend registers
-constexpr int kLaunchRegs = 72, kSoftmaxRegs = 96, kProducerRegs = 64, kIssuerRegs = 56;
-static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + (kKWarps + kVWarps) * kProducerRegs + 4 * kIssuerRegs) <=
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 96, kKRegs = 72, kVRegs = 48, kIssuerRegs = 56;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * kVRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
 constexpr float kRescale = 8.0f;       // the running maximum moves when a score passes it by 2^8
@@ -201,15 +210,13 @@ constexpr int kMinTiles = 2;           // key tiles a pair takes at least
 constexpr int kPrefetchAhead = 4;      // tiles requested into L2 ahead of the loads
 
 struct __align__(1024) PairSmem {
-  uint8_t k[kChunks][kCtaKeys * 128];  // chunk c: [own 64 keys][64 dims] fp16, 128-byte swizzle
-  uint8_t v[4][kKeys * 128];           // chunk c: [128 keys][64 of the CTA's 256 latent dims]
+  uint8_t kv[2][kChunks][kCtaKeys * 128];  // tile buffer, chunk: [64 keys][64 dims] fp16, 128-byte swizzle; see above
   uint8_t q[kChunks][kCtaRows * 128];
-  uint8_t p[2][kCtaRows * 128];        // chunk c: [64 rows][keys 64 c .. 64 c + 63]
+  uint8_t p1[kCtaRows * 128];              // P for keys 64-127 of a tile (keys 0-63: the tile's rope chunk): [64 rows][64 keys]
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
-  // K is handed over in two parts, latent dims 0-255 and the rest with the rope, V in keys 0-63 and 64-127
   uint64_t k_full[2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
-  uint64_t k_free[2], v_free[2], s_full[2];                  // completed by the MMAs in both CTAs
+  uint64_t s_full[2], kv_free[2];                            // completed by the MMAs in both CTAs
   uint64_t final_bar;
   int64_t x0, total;                   // start of the pair's range of work; all work, over `pairs` pairs
   int pairs, b, g, rel, len;           // the range's first unit and its position (see Walk)
@@ -361,6 +368,23 @@ __device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void arrive_cluster(uint32_t mapped) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
+// Ends the work of both CTAs; `timeout`: because a wait gave up.
+__device__ __forceinline__ void raise_abort(unsigned* err, int* abort, bool timeout) {
+  if (timeout) latch_error(err, SMLA_ERR_TIMEOUT);
+  for (uint32_t r = 0; r < 2; ++r)
+    asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_cta(smem_u32(abort), r)) : "memory");
+}
+// Non-blocking test of a barrier's phase.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait as mbar_wait; a wait that gives up raises the abort flag of both CTAs.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsigned* err, int* abort) {
   const uint32_t addr = smem_u32(bar);
@@ -374,9 +398,7 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsign
       if (t0 == 0) {
         t0 = t;
       } else if (t - t0 > kWaitLimitNs) {
-        latch_error(err, SMLA_ERR_TIMEOUT);
-        for (uint32_t r = 0; r < 2; ++r)
-          asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_cta(smem_u32(abort), r)) : "memory");
+        raise_abort(err, abort, true);
         return false;
       }
     }
@@ -601,9 +623,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     mbar_init(&sm.final_bar, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_full[i], 2 * kKWarps);
-      mbar_init(&sm.v_full[i], kVWarps);  // half of the warps of each CTA
-      mbar_init(&sm.k_free[i], 1);
-      mbar_init(&sm.v_free[i], 1);
+      mbar_init(&sm.v_full[i], 2 * kVWarps);
+      mbar_init(&sm.kv_free[i], 1);
       mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
       mbar_init(&sm.s_full[i], 1);
     }
@@ -632,61 +653,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const uint32_t elected = elect_one();
       const uint32_t idesc1 = make_idesc(128, kKeys, 0, 0, 0, 0);  // fp16, both K-major
       const uint32_t idesc2 = make_idesc(128, 256, 0, 0, 0, 1);    // fp16, P K-major, V MN-major
-      const uint64_t dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024), dk = sw128_desc(smem_u32(sm.k[0]), 16, 1024);
-      const uint64_t dp = sw128_desc(smem_u32(sm.p[0]), 16, 1024), dv = sw128_desc(smem_u32(sm.v[0]), kKeys * 128, 1024);
+      constexpr int kChunk = kCtaKeys * 128, kTileBytes = kChunks * kChunk;
+      const uint64_t dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024), dk = sw128_desc(smem_u32(sm.kv[0][0]), 16, 1024);
+      const uint64_t dp = sw128_desc(smem_u32(sm.p1), 16, 1024), dv = sw128_desc(smem_u32(sm.kv[0][0]), kChunk, 1024);
       const uint32_t dq_lo = static_cast<uint32_t>(dq), dk_lo = static_cast<uint32_t>(dk), dp_lo = static_cast<uint32_t>(dp), dv_lo = static_cast<uint32_t>(dv);
-      const uint32_t dq_hi = static_cast<uint32_t>(dq >> 32), dk_hi = static_cast<uint32_t>(dk >> 32), dp_hi = static_cast<uint32_t>(dp >> 32), dv_hi = static_cast<uint32_t>(dv >> 32);
+      const uint32_t dk_hi = static_cast<uint32_t>(dk >> 32), dv_hi = static_cast<uint32_t>(dv >> 32);  // Q and P as K
       uint32_t k1 = 0, k2 = 0, n = 0;  // MMA1s and MMA2s issued, units begun
-      const auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, pair_wait(bar, parity, err, &sm.abort));
+      const auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_test(bar, parity));
       };
       // S = Q . K^T of tile k1 into score buffer k1 % 2
-      const auto mma1 = [&]() -> bool {
-        if (!wait_all(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1)) return false;
-        const uint32_t ts = tmem_s + (k1 & 1) * 64;
+      const auto mma1 = [&]() {
+        const uint32_t buf = k1 & 1;
+        tc_fence_after();
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          if (!wait_all(&sm.k_full[part], k1 & 1)) return false;
-          tc_fence_after();
-          const int end = part == 0 ? 4 : kChunks;
-#pragma unroll 1
-          for (int c = 4 * part; c < end; ++c)
-            unrolled<4>([&](auto x) {
-              mma2_f16<x() * 32, x() * 32>(ts, dq_lo + c * (kCtaRows * 128 >> 4), dq_hi, dk_lo + c * (kCtaKeys * 128 >> 4), dk_hi,
-                                           idesc1, (c | x()) != 0, elected);
-            });
-          if (part == 1) commit2(&sm.s_full[k1 & 1], elected);
-          commit2(&sm.k_free[part], elected);
-        }
+        for (int c = 0; c < kChunks; ++c)
+          unrolled<4>([&](auto x) {
+            mma2_f16<x() * 32, x() * 32>(tmem_s + buf * 64, dq_lo + c * (kChunk >> 4), dk_hi,
+                                         dk_lo + (buf * kTileBytes + c * kChunk) / 16, dk_hi, idesc1, (c | x()) != 0, elected);
+          });
+        commit2(&sm.s_full[buf], elected);
         ++k1;
-        return true;
       };
       // O (+)= P . V of tile k2
-      const auto mma2 = [&](bool first) -> bool {
-        if (!wait_all(&sm.p_full, k2 & 1)) return false;
+      const auto mma2 = [&](bool first) {
+        const uint32_t buf = k2 & 1;
+        tc_fence_after();
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          if (!wait_all(&sm.v_full[part], k2 & 1)) return false;
-          tc_fence_after();
+        for (int h = 0; h < 2; ++h) {  // keys 0-63 and 64-127
+          const uint32_t p = h == 0 ? dk_lo + (buf * kTileBytes + 8 * kChunk) / 16 : dp_lo;
           unrolled<8>([&](auto i) {
             constexpr int x = i() / 2, j = i() % 2;
-            mma2_f16<x * 32, 2 * j * kKeys * 128 + x * 2048>(tmem_o + j * 128, dp_lo + part * (kCtaRows * 128 >> 4), dp_hi,
-                                                              dv_lo + part * (4 * 2048 >> 4), dv_hi, idesc2,
-                                                              !(first && (part | x) == 0), elected);
+            mma2_f16<x * 32, 2 * j * kChunk + x * 2048>(tmem_o + j * 128, p, dk_hi, dv_lo + (buf * kTileBytes + 4 * h * kChunk) / 16,
+                                                         dv_hi, idesc2, !(first && (h | x) == 0), elected);
           });
-          commit2(&sm.v_free[part], elected);
         }
+        commit2(&sm.kv_free[buf], elected);
         ++k2;
-        return true;
       };
       Walk w;
       bool ok = true;
       for (w.start(A, sm); w.on() && ok; w.next(A), ++n) {
-        ok = wait_all(&sm.q_full, n & 1) && mma1();
-        const int ta = w.ta(A), tb = w.tb(A);
-        for (int t = ta; t < tb && ok; ++t) {
-          if (t + 1 < tb) ok = mma1();  // the next tile's scores while this one's softmax works
-          ok = ok && mma2(t == ta);
+        ok = __all_sync(0xffffffffu, pair_wait(&sm.q_full, n & 1, err, &sm.abort));
+        const uint32_t begin = k1, end = begin + w.tb(A) - w.ta(A);
+        // Whichever is ready: P . V of the oldest tile with written probabilities (it frees the tile
+        // buffer), else the next tile's scores (so that they are formed while the softmax works).
+        uint64_t t0 = 0;
+        for (uint32_t idle = 0; ok && k2 < end;) {
+          if (k2 < k1 && ready(&sm.p_full, k2 & 1) && ready(&sm.v_full[k2 & 1], (k2 >> 1) & 1)) {
+            mma2(k2 == begin);
+            idle = 0;
+          } else if (k1 < end && ready(&sm.k_full[k1 & 1], (k1 >> 1) & 1) && ready(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1)) {
+            mma1();
+            idle = 0;
+          } else if ((++idle & 63u) == 0) {  // as pair_wait: give up after kWaitLimitNs
+            const uint64_t t = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+            if (idle == 64) t0 = t;
+            ok = *static_cast<volatile int*>(&sm.abort) == 0 && t - t0 <= kWaitLimitNs;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) raise_abort(err, &sm.abort, t - t0 > kWaitLimitNs);
+          }
         }
       }
       if (k1 > 0) {  // nothing may still read or write the pair's memory when it leaves
@@ -725,33 +751,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       }
     }
   } else if (warp >= kFirstV) {
-    // ------------------------------ V: 128 keys x this CTA's 256 latent dims ------------------------------
-    // Warp vw takes keys 16 vw .. + 15 of a tile.  A lane loads eight codes of a key, which become one
-    // 16-byte slot of a chunk: a key's 256 codes are one coalesced load, and a quarter-warp stores the
-    // eight slots of a key's chunk, which lie in different banks.  (Loads of 64 bytes from each of eight
-    // keys need no shuffles, but took 24 passes of the load pipe each instead of three; the pipe was 82% busy.)
+    // ------------------------------ V: the other CTA's 64 keys x this CTA's 256 latent dims ------------------------------
+    // Warp vw takes 8 of the keys.  A lane loads eight codes of a key, which become one 16-byte slot of a
+    // chunk: a key's 256 codes are one coalesced load, and a quarter-warp stores the eight slots of a
+    // key's chunk, which lie in different banks.  (Loads of 64 bytes from each of eight keys need no
+    // shuffles, but took 24 passes of the load pipe each instead of three; the pipe was 82% busy.)
     // Lane 2 i + x keeps scale x of key i.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kVRegs));
     constexpr int kN = kKeysPerV;
-    const int key0 = kN * (warp - kFirstV);
+    const int vw = warp - kFirstV, other = 1 - static_cast<int>(cta);
+    const int key0 = kCtaKeys * other + kN * vw;
     const int code_off = 256 * static_cast<int>(cta) + 8 * lane, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
-    const uint32_t dst = (lane >> 3) * kKeys * 128 + sw128_off(key0, lane & 7);
+    const uint32_t dst = (4 * other + (lane >> 3)) * kCtaKeys * 128 + sw128_off(kN * vw, lane & 7);
+    const uint32_t full[2] = {map_cta(smem_u32(&sm.v_full[0]), 0), map_cta(smem_u32(&sm.v_full[1]), 0)};
     uint2 codes[kN];
     float sc;
     Records<kRuns, kN> rec;
     const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off)); };
-    const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 1) + scale_off)); };
+    const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get((lane >> 1) & (kN - 1)) + scale_off)); };
     // Stores a tile and asks for the next: a key's registers take their next codes as soon as they are stored.
-    const auto store = [&](auto slow, uint32_t mine) {
+    const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * i + (lane >> 4));
-        *reinterpret_cast<uint4*>(&sm.v[0][0] + ((dst ^ ((i & 7) << 4)) + 128 * i)) = dequant8<slow()>(codes[i], s);
+        *reinterpret_cast<uint4*>(tile + ((dst ^ ((i & 7) << 4)) + 128 * i)) = dequant8<slow()>(codes[i], s);
         load(i);
       }
     };
-    const int part = (warp - kFirstV) / (kVWarps / 2);
-    const uint32_t full = map_cta(smem_u32(&sm.v_full[part]), 0);
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on();
@@ -767,19 +793,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 #pragma unroll
         for (int i = 0; i < kN; ++i)
           if (i >= n) codes[i] = make_uint2(0, 0);
-        if ((lane >> 1) >= n) sc = 0.f;
+        if (((lane >> 1) & (kN - 1)) >= n) sc = 0.f;
       }
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
       n = rec.take(A);
       on = tw.on();
       load_scale();
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.v_free[part], (kk & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{}, mine);
-      else store(std::false_type{}, mine);
+      // the tile's scores are formed: the chunks that V does not need are free
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.s_full[kk & 1], (kk >> 1) & 1, err, &sm.abort))) break;
+      if (slow) store(std::true_type{}, mine, sm.kv[kk & 1][0]);
+      else store(std::false_type{}, mine, sm.kv[kk & 1][0]);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_cluster(full);
+      if (lane == 0) arrive_cluster(full[kk & 1]);
       tw.next(A);
       rec.find(A, tw, key0, lane);
     }
@@ -787,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
     // Warp kw takes keys 8 kw .. + 7, as for V: a key's codes are two loads, the rope of four keys another.
     // Lane 4 i + x keeps scale x of key i.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    static_assert(kKRegs == kLaunchRegs, "no change of registers");
     constexpr int kN = kKeysPerK;
     const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
     const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
@@ -801,12 +828,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     const auto load_rope = [&](int i) {
       rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
-    const auto store = [&](auto slow, auto h, uint32_t mine) {
+    const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h() + (lane >> 4));
-        *reinterpret_cast<uint4*>(&sm.k[0][0] + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h())) = dequant8<slow()>(codes[h()][i], s);
-        load(h(), i);
+      for (int u = 0; u < 2 * kN; ++u) {
+        const int h = u / kN, i = u % kN;
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h + (lane >> 4));
+        *reinterpret_cast<uint4*>(tile + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h)) = dequant8<slow()>(codes[h][i], s);
+        load(h, i);
       }
     };
     TileWalk tw;
@@ -840,15 +868,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       n = rec.take(A);
       on = tw.on();
       load_scale();
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free[0], (kk & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{}, std::integral_constant<int, 0>{}, mine);
-      else store(std::false_type{}, std::integral_constant<int, 0>{}, mine);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(full[0]);
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.k_free[1], (kk & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{}, std::integral_constant<int, 1>{}, mine);
-      else store(std::false_type{}, std::integral_constant<int, 1>{}, mine);
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
+      uint8_t* tile = sm.kv[kk & 1][0];
+      if (slow) store(std::true_type{}, mine, tile);
+      else store(std::false_type{}, mine, tile);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
@@ -860,12 +883,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           o[x] = pack_half2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xFFFF0000u));
         }
         bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
-        *reinterpret_cast<uint4*>(&sm.k[8][sw128_off(kN * kw + 4 * i + (lane >> 3), lane & 7)]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(tile + 8 * kCtaKeys * 128 + sw128_off(kN * kw + 4 * i + (lane >> 3), lane & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         load_rope(i);
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_cluster(full[1]);
+      if (lane == 0) arrive_cluster(full[kk & 1]);
       tw.next(A);
       rec.find(A, tw, key0, lane);
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
@@ -1003,7 +1026,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           m = mn;
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O holds the tiles before this one once their last MMA is done; this tile's waits for p_full
-            ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;
+            ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -1030,10 +1053,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           pw[i / 2] = pack_half2(p.x, p.y);
         }
         l += ls.x + ls.y;
-        if (kk > 0) ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;  // P is read
+        // keys 0-63 go to this tile's rope chunk; p1 is free once the last tile's MMAs have read it
+        if (kh == 1 && kk > 0) ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+        uint8_t* p = kh == 0 ? sm.kv[buf][8] : sm.p1;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          *reinterpret_cast<uint4*>(&sm.p[kh][sw128_off(row, 4 * wg + v)]) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
+          *reinterpret_cast<uint4*>(p + sw128_off(row, 4 * wg + v)) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
@@ -1045,7 +1070,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       nx.next(A);
       if (nx.on()) load_q(nx, (n + 1) & 1);
       // ---- end of unit ----
-      ok = pair_wait(&sm.v_free[1], (kk - 1) & 1, err, &sm.abort) && ok;
+      ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
       __syncwarp();
       tc_fence_after();
       sm.red[2 * wg + kh][row] = l;
