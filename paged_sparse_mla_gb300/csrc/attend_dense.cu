@@ -30,10 +30,10 @@ struct DenseArgs {
   unsigned* err;
 };
 
-// Positions that query token t (the i-th of sequence b's n_q) sees: seq_len - n_q + i + 1, at least
+// Positions that the i-th of n_q query tokens of a sequence of len positions sees: len - n_q + i + 1, at least
 // none and at most what the block-table row holds.
-__device__ __forceinline__ int64_t visible(const DenseArgs& A, int b, int i, int n_q) {
-  const int64_t n = static_cast<int64_t>(__ldg(A.seq_lens + b)) - n_q + i + 1;
+__device__ __forceinline__ int64_t visible(const DenseArgs& A, int len, int i, int n_q) {
+  const int64_t n = static_cast<int64_t>(len) - n_q + i + 1;
   const int64_t most = static_cast<int64_t>(A.bt_stride) * A.L.block_size;
   return n < 0 ? 0 : n < most ? n : most;
 }
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kSThreads) dense_fp32_kernel(const DenseArgs A
   if (t >= __ldg(A.qsl + A.batch)) return;  // behind the last sequence: left as it was
   const int b = seq_of_token(A.qsl, A.batch, t);
   const int q0 = __ldg(A.qsl + b), n_q = __ldg(A.qsl + b + 1) - q0;
-  const int64_t n = visible(A, b, t - q0, n_q);
+  const int64_t n = visible(A, __ldg(A.seq_lens + b), t - q0, n_q);
   if (threadIdx.x == 0 && __ldg(A.seq_lens + b) > static_cast<int64_t>(A.bt_stride) * L.block_size)
     latch_error(A.err, SMLA_ERR_BAD_INDEX);
   for (int u = threadIdx.x; u < kSHeads * D; u += kSThreads) {
@@ -218,8 +218,8 @@ struct __align__(1024) PairSmem {
   uint64_t k_full[2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
   uint64_t s_full[2], kv_free[2];                            // completed by the MMAs in both CTAs
   uint64_t final_bar;
-  int64_t x0, total;                   // start of the pair's range of work; all work, over `pairs` pairs
-  int pairs, b, g, rel, len;           // the range's first unit and its position (see Walk)
+  int64_t x0, total, seq_at;           // start of the pair's range of work; all work, over `pairs` pairs; (plan)
+  int pairs, b, g, rel, len, q0, n_q, seq_len;  // the range's first unit, its position (see Walk) and sequence
   int abort;
   uint32_t tmem_slot;
   uint32_t k_loaded;                   // tiles whose keys the first K warp has asked for
@@ -246,18 +246,19 @@ struct PairArgs {
   uint32_t bs_mul, bs_shift1, bs_shift2;  // division by block_size
 };
 
-// sum_{g < n} floor((a g + b) / m), all non-negative (Euclid's algorithm on the lattice points).
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum_{g < n} floor((a g + b) / m), with a n + b and the sums of the descent below 2^32 (Euclid's algorithm
+// on the lattice points below a line).
+__device__ __noinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t s = 0;
   while (n > 0) {
-    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    s += static_cast<int64_t>(n - 1) * n / 2 * (a / m) + static_cast<int64_t>(n) * (b / m);
     a %= m;
     b %= m;
-    const int64_t y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const int64_t t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -266,16 +267,18 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 
 // A unit is `group` query tokens of a sequence (fewer at its end) with the key tiles its last token sees
 // (at least one, so that tokens which see nothing are written too).
-__device__ __forceinline__ int unit_tiles(const PairArgs& A, int b, int g, int n_q) {
+__device__ __forceinline__ int unit_tiles(const PairArgs& A, int len, int g, int n_q) {
   const int last = min((g + 1) * A.group, n_q) - 1;
-  return max(1, static_cast<int>((visible(A.D, b, last, n_q) + kKeys - 1) / kKeys));
+  return max(1, static_cast<int>((visible(A.D, len, last, n_q) + kKeys - 1) / kKeys));
 }
 
-// Work of the first g units of sequence b: their tiles, or their number where units are not split.
-__device__ int64_t work_before(const PairArgs& A, int b, int g, int n_q) {
+// Work of the first g units of a sequence of len positions and n_q query tokens: their tiles, or their
+// number where units are not split.
+__device__ int64_t work_before(const PairArgs& A, int len, int g, int n_q) {
   if (A.part_out == nullptr) return g;
-  const int64_t len = __ldg(A.D.seq_lens + b), most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
+  const int64_t most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
   const int units = (n_q + A.group - 1) / A.group;
+  if (units == 1) return g == 0 ? 0 : unit_tiles(A, len, 0, n_q);
   if (len >= n_q && len <= most) {
     const int whole = min(g, units - 1);
     int64_t s = floor_sum(whole, kKeys, A.group, len - n_q + A.group + kKeys - 1);
@@ -283,19 +286,22 @@ __device__ int64_t work_before(const PairArgs& A, int b, int g, int n_q) {
     return s;
   }
   int64_t s = 0;
-  for (int i = 0; i < g; ++i) s += unit_tiles(A, b, i, n_q);
+  for (int i = 0; i < g; ++i) s += unit_tiles(A, len, i, n_q);
   return s;
 }
 
 // The units of this pair in turn.  Positions count tiles from the start of the pair's range: the unit
 // begins at `rel` (below zero if an earlier pair began it) and the range ends at `len`.
 struct Walk {
-  int b, g, q0, n_q, nvis, rel, len;
+  int b, g, q0, n_q, nvis, rel, len, seq_len;
   __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
     b = sm.b;
     g = sm.g;
     rel = sm.rel;
     len = sm.len;
+    q0 = sm.q0;
+    n_q = sm.n_q;
+    seq_len = sm.seq_len;
     if (on()) unit(A);
   }
   __device__ __forceinline__ bool on() const { return rel < len; }
@@ -308,17 +314,19 @@ struct Walk {
     return A.part_out != nullptr ? min(tiles(), len - rel) : tiles();
   }
   __device__ __forceinline__ void unit(const PairArgs& A) {
-    q0 = __ldg(A.D.qsl + b);
-    n_q = __ldg(A.D.qsl + b + 1) - q0;
-    nvis = static_cast<int>(visible(A.D, b, g * A.group + ntok(A) - 1, n_q));
+    nvis = static_cast<int>(visible(A.D, seq_len, g * A.group + ntok(A) - 1, n_q));
   }
   __device__ __forceinline__ void next(const PairArgs& A) {
     rel += A.part_out != nullptr ? tiles() : 1;
     if (!on()) return;
     if (++g * A.group >= n_q) {
       g = 0;
-      do ++b;
-      while (__ldg(A.D.qsl + b + 1) == __ldg(A.D.qsl + b));
+      q0 += n_q;
+      int end;
+      do end = __ldg(A.D.qsl + ++b + 1);
+      while (end == q0);
+      n_q = end - q0;
+      seq_len = __ldg(A.D.seq_lens + b);
     }
     unit(A);
   }
@@ -546,65 +554,105 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
 }
 
-// The pair's range of work: every thread takes sequences, a scan over the CTA finds the total and the
-// unit in which the range begins.
-__device__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
+// The pair's range of work.  Threads take the sequences in turn and a scan over the CTA finds the total and
+// the sequence in which the range begins (again from the start if there are more sequences than
+// threads); the first warp then looks for the unit.
+__device__ __forceinline__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
   int64_t* warp_sum = reinterpret_cast<int64_t*>(sm.red);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int batch = A.D.batch;
-  const int64_t most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
-  int64_t total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t carry = 0;
-    const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / kMinTiles : total));
-    const int64_t x0 = pair < P ? pair * total / P : total, x1 = pair < P ? (pair + 1) * total / P : total;
-    if (pass == 1 && threadIdx.x == 0) {
-      sm.x0 = x0;
-      sm.len = static_cast<int>(x1 - x0);
-      if (x0 >= x1) sm.rel = 0;
-      sm.pairs = static_cast<int>(P);
-      sm.total = total;
+  int64_t total = -1, x0 = 0, x1 = 0, carry = 0;
+#pragma unroll 1
+  for (int c0 = 0;;) {
+    const int b = c0 + threadIdx.x;
+    int64_t mine = 0;
+    int q0 = 0, n_q = 0, len = 0;
+    if (b < batch) {
+      q0 = __ldg(A.D.qsl + b);
+      n_q = __ldg(A.D.qsl + b + 1) - q0;
+      len = __ldg(A.D.seq_lens + b);
+      if (n_q > 0) mine = work_before(A, len, (n_q + A.group - 1) / A.group, n_q);
+      if (blockIdx.x == 0 && n_q > 0 && len > static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size)
+        latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
     }
-    for (int c0 = 0; c0 < batch; c0 += kThreads) {
-      const int b = c0 + threadIdx.x;
-      int64_t mine = 0;
-      int n_q = 0, units = 0;
-      if (b < batch) {
-        n_q = __ldg(A.D.qsl + b + 1) - __ldg(A.D.qsl + b);
-        units = (n_q + A.group - 1) / A.group;
-        if (n_q > 0) mine = work_before(A, b, units, n_q);
-        if (pass == 0 && blockIdx.x == 0 && n_q > 0 && __ldg(A.D.seq_lens + b) > most)
-          latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
+    int64_t incl = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t lo = carry + incl - mine;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) lo += warp_sum[w];
+      carry += warp_sum[w];
+    }
+    c0 += kThreads;
+    if (total < 0 && c0 >= batch) {  // the total is known: the pair's range, and the first sequences again if need be
+      total = carry;
+      const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / kMinTiles : total));
+      x0 = pair < P ? pair * total / P : total;
+      x1 = pair < P ? (pair + 1) * total / P : total;
+      if (threadIdx.x == 0) {
+        sm.x0 = x0;
+        sm.len = static_cast<int>(x1 - x0);
+        sm.total = total;
+        sm.pairs = static_cast<int>(P);
+        sm.rel = 0;
       }
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+      if (batch > kThreads) {
+        c0 = 0;
+        carry = 0;
+        continue;
       }
-      __syncthreads();
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int64_t before = carry, all = carry;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-      }
-      const int64_t lo = before + incl - mine;
-      if (pass == 1 && mine > 0 && x0 < x1 && lo <= x0 && x0 < lo + mine) {
-        int ga = 0, gb = units - 1;  // the last unit that begins at or before x0
-        while (ga < gb) {
-          const int gm = (ga + gb + 1) / 2;
-          if (lo + work_before(A, b, gm, n_q) <= x0) ga = gm;
-          else gb = gm - 1;
-        }
+    }
+    if (total >= 0) {
+      if (x0 < x1 && mine > 0 && lo <= x0 && x0 < lo + mine) {
         sm.b = b;
-        sm.g = ga;
-        sm.rel = static_cast<int>(lo + work_before(A, b, ga, n_q) - x0);
+        sm.seq_at = lo;
+        sm.q0 = q0;
+        sm.n_q = n_q;
+        sm.seq_len = len;
       }
-      carry = all;
+      if (c0 >= batch) break;
     }
-    total = carry;
+  }
+  __syncthreads();
+  if (warp == 0 && x0 < x1) {
+    const int n_q = sm.n_q, len = sm.seq_len;
+    const int64_t at = x0 - sm.seq_at;
+    int ga = 0, gb = (n_q + A.group - 1) / A.group - 1;  // the last unit that begins at or before the range is in [ga, gb]
+#pragma unroll 1
+    while (ga < gb) {
+      const int step = (gb - ga + 31) / 32, g = ga + (lane + 1) * step;
+      const int past = __popc(__ballot_sync(0xffffffffu, g <= gb && work_before(A, len, g, n_q) <= at));
+      ga += past * step;
+      gb = min(gb, ga + step - 1);
+    }
+    if (lane == 0) {
+      sm.g = ga;
+      sm.rel = -static_cast<int>(at - work_before(A, len, ga, n_q));
+    }
+  }
+}
+
+// A lane's part of a query row: 16 latent and 2 rope dims, as nine pairs.
+__device__ __forceinline__ void load_query(const PairArgs& A, int64_t row, int lane, uint32_t (&v)[9]) {
+  const __nv_bfloat16* src = A.D.q + row * kDL + 16 * lane;
+  const __nv_bfloat16* pe = A.D.q_pe + row * kDR + 2 * lane;
+  if (A.q_vec) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    v[8] = __ldg(reinterpret_cast<const uint32_t*>(pe));
+  } else {
+    const uint16_t* u = reinterpret_cast<const uint16_t*>(src);
+    const uint16_t* w = reinterpret_cast<const uint16_t*>(pe);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = u[2 * x] | (static_cast<uint32_t>(u[2 * x + 1]) << 16);
+    v[8] = w[0] | (static_cast<uint32_t>(w[1]) << 16);
   }
 }
 
@@ -638,6 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  cudaTriggerProgrammaticLaunchCompletion();  // the merge may be launched; it waits for this grid's end
   plan(A, sm, pair, n_pairs);
   tc_fence_before();
   __syncthreads();
@@ -723,13 +772,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       // Requests this CTA's keys into L2 a few tiles before the K warps load them.
       TileWalk tw;
       tw.start(A, sm);
-      const uint64_t t0 = globaltimer_ns();
-      uint64_t last = t0;
+      uint64_t last = globaltimer_ns();
       uint32_t seen = 0;
       for (uint32_t kk = 0; tw.on(); ++kk) {
         for (;;) {
           const uint32_t done = *static_cast<volatile uint32_t*>(&sm.k_loaded);
-          if (kk < done + kPrefetchAhead) break;
+          if (kk + 1 < done + kPrefetchAhead && done > 0) break;  // not before the first tile and the queries are asked for
           const uint64_t now = globaltimer_ns();
           if (done != seen) last = now;
           seen = done;
@@ -909,52 +957,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is
     // scaled by a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's
     // eight bits exactly down to 2^-23 of that element.
+    // (Short code matters here as much as loads in flight: it runs once a unit, from a cold instruction
+    // cache.)
     const auto load_q = [&](const Walk& w, int slot) {
       const int rows = w.ntok(A) * H - kCtaRows * static_cast<int>(cta);
       const int64_t first = static_cast<int64_t>(w.tok0(A)) * H + kCtaRows * cta;
+      uint32_t v[4][9];
+      const auto ask = [&](int i, int r) {
+#pragma unroll
+        for (int x = 0; x < 9; ++x) v[i][x] = 0;
+        if (r < rows) load_query(A, first + r, lane, v[i]);
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ask(i, 8 * warp + i);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint4 a[4], b[4];
-        uint32_t e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * warp + 4 * half + i;
-          a[i] = b[i] = make_uint4(0, 0, 0, 0);
-          e[i] = 0;
-          if (r < rows) {
-            const __nv_bfloat16* src = A.D.q + (first + r) * kDL + 16 * lane;
-            const __nv_bfloat16* pe = A.D.q_pe + (first + r) * kDR + 2 * lane;
-            if (A.q_vec) {
-              a[i] = __ldg(reinterpret_cast<const uint4*>(src));
-              b[i] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-              e[i] = __ldg(reinterpret_cast<const uint32_t*>(pe));
-            } else {
-              const uint16_t* u = reinterpret_cast<const uint16_t*>(src);
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(pe);
-              uint32_t t[8];
+          uint32_t top2 = 0;  // the largest magnitude (bf16 bits of non-negative values order as integers)
 #pragma unroll
-              for (int x = 0; x < 8; ++x) t[x] = u[2 * x] | (static_cast<uint32_t>(u[2 * x + 1]) << 16);
-              a[i] = make_uint4(t[0], t[1], t[2], t[3]);
-              b[i] = make_uint4(t[4], t[5], t[6], t[7]);
-              e[i] = v[0] | (static_cast<uint32_t>(v[1]) << 16);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * warp + 4 * half + i;
-          const uint32_t w9[9] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w, e[i]};
-          uint32_t top = 0;  // the largest magnitude's bits (fp32 bits of non-negative values order as integers)
-#pragma unroll
-          for (int x = 0; x < 9; ++x) top = max(top, max((w9[x] << 16) & 0x7FFFFFFFu, w9[x] & 0x7FFF0000u));
-          top = __reduce_max_sync(0xffffffffu, top);
-          const int ex = static_cast<int>(top >> 23);  // biased exponent
+          for (int x = 0; x < 9; ++x) top2 = __vmaxu2(top2, v[i][x] & 0x7FFF7FFFu);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+          const int ex = static_cast<int>(top >> 7);  // biased exponent
           const int up = (ex == 0 || ex == 255) ? 0 : min(126, 127 + 8 - ex);  // zeros, infinities and NaN as they are
           const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23) * A.sign;
           uint32_t o[9];
 #pragma unroll
           for (int x = 0; x < 9; ++x)
-            o[x] = pack_half2(__uint_as_float(w9[x] << 16) * f, __uint_as_float(w9[x] & 0xFFFF0000u) * f);
+            o[x] = pack_half2(__uint_as_float(v[i][x] << 16) * f, __uint_as_float(v[i][x] & 0xFFFF0000u) * f);
+          if (half == 0) ask(i, r + 4);
           const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
           const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
           *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]) = odd ? o1 : o0;
@@ -977,8 +1009,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     bool failed = false;
     while (w.on() && !failed) {
       const int grow = kCtaRows * static_cast<int>(cta) + row;  // row of the unit
-      const bool real = grow < w.ntok(A) * H;
-      const int vis = real ? static_cast<int>(visible(A.D, w.b, w.g * A.group + grow / H, w.n_q)) : 0;
+      const int real_rows = w.ntok(A) * H;
+      const bool real = grow < real_rows;
+      const int vis = real ? static_cast<int>(visible(A.D, w.seq_len, w.g * A.group + grow / H, w.n_q)) : 0;
       const int ta = w.ta(A), tb = w.tb(A);
       // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
       const float f = fmaxf(sm.row_f[n & 1][row], 1.2e-38f);
@@ -1086,27 +1119,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (partial) A.part_lse[slot * kRows + grow] = lse;
         else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
       }
+      // A lane holds 128 dims of its row.  Sixteen at a time, the lanes of a group of four exchange them so
+      // that lane i of the group stores four dims of each of the group's rows and the group 64 (bf16: 32)
+      // consecutive bytes (a lane that stores its own row's dims touches 32 rows in every store).
+      const int i4 = lane & 3;
 #pragma unroll 1
-      for (int x = 0; x < 4; ++x) {
-        uint32_t o[32];
+      for (int x = 0; x < 8; ++x) {
+        uint32_t o[16];
         __syncwarp();
-        tmem_ld32(tmem_o + lane_base + 128 * wg + 32 * x, o);
+        tmem_ld16(tmem_o + lane_base + 128 * wg + 16 * x, o);
         tmem_ld_wait(o);
-        if (real && partial) {
-          float4* dst = reinterpret_cast<float4*>(A.part_out + (slot * kRows + grow) * kDL + d0 + 32 * x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-        } else if (real) {
-          uint4* dst = reinterpret_cast<uint4*>(A.D.out + orow * kDL + d0 + 32 * x);
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        // o[4 j + i]: dims 4 j + i of the own row -> dims 4 i4 + i of row j of the group
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
+        for (int st = 1; st <= 2; st <<= 1) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              h[y] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
-            dst[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          for (int j = 0; j < 4; ++j) {
+            if ((j & st) == 0) {
+              const bool hi = (i4 & st) != 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
+                if (hi) o[4 * j + i] = got;
+                else o[4 * (j | st) + i] = got;
+              }
+            }
+          }
+        }
+        const int d = d0 + 16 * x + 4 * i4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int gr = grow - i4 + j;
+          if (gr < real_rows) {
+            if (partial)
+              *reinterpret_cast<uint4*>(A.part_out + (slot * kRows + gr) * kDL + d) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            else
+              *reinterpret_cast<uint2*>(A.D.out + (orow - i4 + j) * kDL + d) =
+                  make_uint2(pack_bf16x2(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1])),
+                             pack_bf16x2(__uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3])));
           }
         }
       }
@@ -1129,87 +1180,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 }
 
 // Joins the parts of units that ran on several pairs: lse = ln sum e^lse_i, out = sum e^(lse_i - lse) out_i
-// in fp32.  One block per row at a time, a thread per four dims; the parts' loads go out eight at a time.
-constexpr int kMergeThreads = 128;
+// in fp32.  A warp takes a row (a lane 16 dims) where a few parts are to be joined; where there are many, as
+// for one long sequence, the block's four warps share it (a lane 4 dims, eight parts' loads in flight).
+constexpr int kMergeThreads = 128, kFewParts = 4;
+template <int kStep>
+__device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, int row, int quarter0, int quarters,
+                                          const float* part_lse, const float* part_out, int n_heads, __nv_bfloat16* out, float* lse) {
+  const int lane = threadIdx.x & 31;
+  const auto slot = [&](int i) -> int64_t { return i == 0 ? 2 * p + 1 : 2 * (p + i); };
+  float v[kMaxPairs / 32], mx = -INFINITY, z = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxPairs / 32; ++i) {
+    v[i] = 32 * i + lane < parts ? __ldg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
+    mx = fmaxf(mx, v[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+  for (int i = 0; i < kMaxPairs / 32; ++i) {
+    v[i] = expf(v[i] - base);  // NaN stays NaN
+    z += v[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  const int64_t orow = static_cast<int64_t>(M.tok0) * n_heads + row;
+#pragma unroll 1
+  for (int q = quarter0; q < quarter0 + quarters; q += kStep == 2 ? 4 : 1) {
+    constexpr int kQ = kStep == 2 ? 4 : 1;  // quarters at once
+    float4 acc[kQ];
+#pragma unroll
+    for (int y = 0; y < kQ; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += kStep) {
+      float4 a[kStep][kQ];
+      float f[kStep];
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const int part = min(i0 + i, parts - 1);
+        const float w = part < 32 ? v[0] : part < 64 ? v[1] : part < 96 ? v[2] : v[3];
+        f[i] = __shfl_sync(0xffffffffu, w, part & 31) * inv;
+        if (i0 + i >= parts) f[i] = 0.f;
+#pragma unroll
+        for (int y = 0; y < kQ; ++y)
+          a[i][y] = __ldg(reinterpret_cast<const float4*>(part_out + (slot(part) * kRows + row) * kDL + 128 * (q + y)) + lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+#pragma unroll
+        for (int y = 0; y < kQ; ++y) {
+          acc[y].x += f[i] * a[i][y].x;
+          acc[y].y += f[i] * a[i][y].y;
+          acc[y].z += f[i] * a[i][y].z;
+          acc[y].w += f[i] * a[i][y].w;
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < kQ; ++y)
+      reinterpret_cast<uint2*>(out + orow * kDL + 128 * (q + y))[lane] =
+          make_uint2(pack_bf16x2(acc[y].x, acc[y].y), pack_bf16x2(acc[y].z, acc[y].w));
+  }
+  if (quarter0 == 0 && lane == 0 && lse != nullptr) lse[orow] = z == 0.f ? -INFINITY : mx + logf(z);
+}
+
 __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMeta* __restrict__ meta,
                                                                     const float* __restrict__ part_lse,
                                                                     const float* __restrict__ part_out, int n_pairs,
                                                                     int n_heads, __nv_bfloat16* __restrict__ out,
                                                                     float* __restrict__ lse) {
   __shared__ int cum[kMaxPairs + 1];  // rows to join of the pairs before p
-  __shared__ float weight[kMaxPairs];
   static_assert(kMergeThreads == kMaxPairs, "a thread per pair");
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  cudaGridDependencySynchronize();
   cum[tid + 1] = tid < n_pairs ? meta[tid].ntok * n_heads : 0;
   if (tid == 0) cum[0] = 0;
   __syncthreads();
+#pragma unroll 1
   for (int o = 1; o < kMaxPairs; o <<= 1) {
     const int v = tid + 1 > o ? cum[tid + 1 - o] : 0;
     __syncthreads();
     cum[tid + 1] += v;
     __syncthreads();
   }
-  for (int item = blockIdx.x; item < cum[kMaxPairs]; item += gridDim.x) {
+  const int total = cum[kMaxPairs];
+  const auto join = [&](int item, bool few) {
     int p = 0, hi = n_pairs - 1;
     while (p < hi) {
       const int mid = (p + hi + 1) / 2;
       if (cum[mid] <= item) p = mid;
       else hi = mid - 1;
     }
-    const int row = item - cum[p];
     const PairMeta M = meta[p];
-    // pairs p + 1 .. p + more carry the rest
-    int more = 0;
-    while (p + more + 1 < M.pairs && (p + more + 1) * M.total / M.pairs < M.end) ++more;
-    const int parts = more + 1;
-    const auto slot = [&](int i) -> int64_t { return i == 0 ? 2 * p + 1 : 2 * (p + i); };
-    float z = 0.f, mx = -INFINITY;
-    if (tid < 32) {
-      float v[kMaxPairs / 32];
-#pragma unroll
-      for (int i = 0; i < kMaxPairs / 32; ++i) {
-        v[i] = 32 * i + lane < parts ? __ldg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
-        mx = fmaxf(mx, v[i]);
-        if (v[i] != v[i]) mx = v[i];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-      for (int i = 0; i < kMaxPairs / 32; ++i) {
-        v[i] = expf(v[i] - base);
-        z += v[i];
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      const float inv = z == 0.f ? 0.f : 1.f / z;
-#pragma unroll
-      for (int i = 0; i < kMaxPairs / 32; ++i)
-        if (32 * i + lane < parts) weight[32 * i + lane] = v[i] * inv;
-    }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i0 + i < parts) v[i] = __ldg(reinterpret_cast<const float4*>(part_out + (slot(i0 + i) * kRows + row) * kDL) + tid);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i0 + i < parts) {
-          const float f = weight[i0 + i];
-          acc.x += f * v[i].x;
-          acc.y += f * v[i].y;
-          acc.z += f * v[i].z;
-          acc.w += f * v[i].w;
-        }
-      }
-    }
-    const int64_t orow = static_cast<int64_t>(M.tok0) * n_heads + row;
-    reinterpret_cast<uint2*>(out + orow * kDL)[tid] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    if (tid == 0 && lse != nullptr) lse[orow] = z == 0.f ? -INFINITY : mx + logf(z);
-    __syncthreads();  // weight is read
-  }
+    // pairs p + 1 .. carry the rest: range r begins at floor(r total / pairs), before the unit's end for
+    // r < end pairs / total
+    const int n = static_cast<int>(min((M.end * M.pairs + M.total - 1) / M.total, static_cast<int64_t>(M.pairs))) - p;
+    if (few && n <= kFewParts) merge_row<2>(M, p, n, item - cum[p], 0, 4, part_lse, part_out, n_heads, out, lse);
+    if (!few && n > kFewParts) merge_row<8>(M, p, n, item - cum[p], warp, 1, part_lse, part_out, n_heads, out, lse);
+  };
+#pragma unroll 1
+  for (int item = 4 * blockIdx.x + warp; item < total; item += 4 * gridDim.x) join(item, true);
+#pragma unroll 1
+  for (int item = blockIdx.x; item < total; item += gridDim.x) join(item, false);
 }
 
 // Layouts of the full latent shape.
@@ -1279,8 +1352,19 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   else dense_pair_kernel<false><<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   if (split) {
-    dense_merge_kernel<<<8 * device_sm_count(), kMergeThreads, 0, s>>>(A.meta, A.part_lse, A.part_out, pairs, D.n_heads, D.out, D.lse);
-    if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+    // launched while the pairs still work (its blocks wait for their results before they read)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(6 * device_sm_count());
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, dense_merge_kernel, static_cast<const PairMeta*>(A.meta), static_cast<const float*>(A.part_lse),
+                           static_cast<const float*>(A.part_out), pairs, D.n_heads, D.out, D.lse) != cudaSuccess)
+      return SMLA_ERR_CUDA;
   }
   return SMLA_OK;
 }
