@@ -800,29 +800,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     }
   } else if (warp >= kFirstV) {
     // ------------------------------ V: the other CTA's 64 keys x this CTA's 256 latent dims ------------------------------
-    // Warp vw takes 8 of the keys.  A lane loads eight codes of a key, which become one 16-byte slot of a
-    // chunk: a key's 256 codes are one coalesced load, and a quarter-warp stores the eight slots of a
-    // key's chunk, which lie in different banks.  (Loads of 64 bytes from each of eight keys need no
-    // shuffles, but took 24 passes of the load pipe each instead of three; the pipe was 82% busy.)
-    // Lane 2 i + x keeps scale x of key i.
+    // Warp vw takes 8 of the keys, two at a time.  A lane loads 16 codes of a key, which become two 16-byte
+    // slots of a chunk: a key's 256 codes are read together, and a quarter-warp's stores go to eight
+    // different slots (lanes of odd chunks store their second slot first).  (Loads of 64 bytes from each of
+    // eight keys need no shuffles, but took 24 passes of the load pipe each; eight codes a lane need
+    // no swap, but twice the loads and shuffles.)  Lane 2 i + x keeps scale x of key i.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kVRegs));
     constexpr int kN = kKeysPerV;
     const int vw = warp - kFirstV, other = 1 - static_cast<int>(cta);
     const int key0 = kCtaKeys * other + kN * vw;
-    const int code_off = 256 * static_cast<int>(cta) + 8 * lane, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
-    const uint32_t dst = (4 * other + (lane >> 3)) * kCtaKeys * 128 + sw128_off(kN * vw, lane & 7);
+    const int sub = lane & 15, odd = (sub >> 2) & 1;
+    const int code_off = 256 * static_cast<int>(cta) + 16 * sub, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
+    // row & 7 of key 2 i + (lane >> 4) is that of key lane >> 4 xor 2 i
+    const uint32_t dst = (4 * other + (sub >> 2)) * kCtaKeys * 128 + sw128_off(kN * vw + (lane >> 4), 2 * (sub & 3) + odd);
     const uint32_t full[2] = {map_cta(smem_u32(&sm.v_full[0]), 0), map_cta(smem_u32(&sm.v_full[1]), 0)};
-    uint2 codes[kN];
+    uint4 codes[kN / 2];
     float sc;
     Records<kRuns, kN> rec;
-    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + code_off)); };
+    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(2 * i + (lane >> 4)) + code_off)); };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get((lane >> 1) & (kN - 1)) + scale_off)); };
     // Stores a tile and asks for the next: a key's registers take their next codes as soon as they are stored.
     const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * i + (lane >> 4));
-        *reinterpret_cast<uint4*>(tile + ((dst ^ ((i & 7) << 4)) + 128 * i)) = dequant8<slow()>(codes[i], s);
+      for (int i = 0; i < kN / 2; ++i) {
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * (2 * i + (lane >> 4)) + (sub >> 3));
+        const uint4 c = codes[i];
+        uint8_t* to = tile + 256 * i;
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
         load(i);
       }
     };
@@ -832,15 +837,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     rec.find(A, tw, key0, lane);
     int n = rec.take(A);  // visible records among the loaded ones
 #pragma unroll
-    for (int i = 0; i < kN; ++i) load(i);
+    for (int i = 0; i < kN / 2; ++i) load(i);
     load_scale();
     tw.next(A);
     rec.find(A, tw, key0, lane);
     for (uint32_t kk = 0; on; ++kk) {
       if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (i >= n) codes[i] = make_uint2(0, 0);
+        for (int i = 0; i < kN / 2; ++i)
+          if (2 * i + (lane >> 4) >= n) codes[i] = make_uint4(0, 0, 0, 0);
         if (((lane >> 1) & (kN - 1)) >= n) sc = 0.f;
       }
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
@@ -860,29 +865,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
-    // Warp kw takes keys 8 kw .. + 7, as for V: a key's codes are two loads, the rope of four keys another.
+    // Warp kw takes keys 8 kw .. + 7, as for V: a key's codes are one load, the rope of four keys another.
     // Lane 4 i + x keeps scale x of key i.
     static_assert(kKRegs == kLaunchRegs, "no change of registers");
     constexpr int kN = kKeysPerK;
     const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
-    const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
+    const int odd = (lane >> 2) & 1;
+    const uint32_t dst = (lane >> 2) * kCtaKeys * 128 + sw128_off(kN * kw, 2 * (lane & 3) + odd);
     const uint32_t full[2] = {map_cta(smem_u32(&sm.k_full[0]), 0), map_cta(smem_u32(&sm.k_full[1]), 0)};
-    uint2 codes[2][kN];
+    uint4 codes[kN];
     uint4 rope[2];
     float sc;
     Records<kRuns, kN> rec;
-    const auto load = [&](int h, int i) { codes[h][i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + 256 * h + 8 * lane)); };
+    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(i)) + lane); };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3))); };
     const auto load_rope = [&](int i) {
       rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
     const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
 #pragma unroll
-      for (int u = 0; u < 2 * kN; ++u) {
-        const int h = u / kN, i = u % kN;
-        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h + (lane >> 4));
-        *reinterpret_cast<uint4*>(tile + ((dst ^ (i << 4)) + 128 * i + 4 * kCtaKeys * 128 * h)) = dequant8<slow()>(codes[h][i], s);
-        load(h, i);
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+        const uint4 c = codes[i];
+        uint8_t* to = tile + 128 * i;
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 4))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 4) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
+        load(i);
       }
     };
     TileWalk tw;
@@ -891,10 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     rec.find(A, tw, key0, lane);
     int n = rec.take(A);  // visible records among the loaded ones
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      load(0, i);
-      load(1, i);
-    }
+    for (int i = 0; i < kN; ++i) load(i);
     load_scale();
     load_rope(0);
     load_rope(1);
@@ -904,7 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       if (n < kN) {  // the end of a context
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          if (i >= n) codes[0][i] = codes[1][i] = make_uint2(0, 0);
+          if (i >= n) codes[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
