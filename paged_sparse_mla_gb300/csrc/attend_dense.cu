@@ -774,7 +774,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       tw.start(A, sm);
       uint64_t last = globaltimer_ns();
       uint32_t seen = 0;
-      for (uint32_t kk = 0; tw.on(); ++kk) {
+      for (uint32_t kk = 0; tw.on(); ++kk, tw.next(A)) {
+        if (kk < *static_cast<volatile uint32_t*>(&sm.k_loaded)) continue;  // too late for this tile
         for (;;) {
           const uint32_t done = *static_cast<volatile uint32_t*>(&sm.k_loaded);
           if (kk + 1 < done + kPrefetchAhead && done > 0) break;  // not before the first tile and the queries are asked for
@@ -795,7 +796,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
               prefetch_l2_bulk(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + (j - pg * A.D.L.block_size) * kRec, kRec);
           }
         }
-        tw.next(A);
       }
     }
   } else if (warp >= kFirstV) {
@@ -819,7 +819,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     Records<kRuns, kN> rec;
     const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(2 * i + (lane >> 4)) + code_off)); };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get((lane >> 1) & (kN - 1)) + scale_off)); };
-    // Stores a tile and asks for the next: a key's registers take their next codes as soon as they are stored.
     const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
 #pragma unroll
       for (int i = 0; i < kN / 2; ++i) {
@@ -828,19 +827,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         uint8_t* to = tile + 256 * i;
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
-        load(i);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on();
     rec.find(A, tw, key0, lane);
-    int n = rec.take(A);  // visible records among the loaded ones
+    int n = 0;  // visible records among the loaded ones
+    const auto load_tile = [&]() {
+      n = rec.take(A);
+      load_scale();
 #pragma unroll
-    for (int i = 0; i < kN / 2; ++i) load(i);
-    load_scale();
-    tw.next(A);
-    rec.find(A, tw, key0, lane);
+      for (int i = 0; i < kN / 2; ++i) load(i);
+      tw.next(A);
+      rec.find(A, tw, key0, lane);
+    };
+    load_tile();
     for (uint32_t kk = 0; on; ++kk) {
       if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
 #pragma unroll
@@ -850,9 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       }
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
-      n = rec.take(A);
       on = tw.on();
-      load_scale();
       // the tile's scores are formed: the chunks that V does not need are free
       if (!__all_sync(0xffffffffu, pair_wait(&sm.s_full[kk & 1], (kk >> 1) & 1, err, &sm.abort))) break;
       if (slow) store(std::true_type{}, mine, sm.kv[kk & 1][0]);
@@ -860,8 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full[kk & 1]);
-      tw.next(A);
-      rec.find(A, tw, key0, lane);
+      load_tile();  // after the fence, which would wait for loads in flight
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
@@ -890,21 +889,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         uint8_t* to = tile + 128 * i;
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 4))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 4) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
-        load(i);
       }
     };
     TileWalk tw;
     tw.start(A, sm);
     bool on = tw.on(), bad = false;
     rec.find(A, tw, key0, lane);
-    int n = rec.take(A);  // visible records among the loaded ones
+    int n = 0;  // visible records among the loaded ones
+    const auto load_tile = [&]() {
+      n = rec.take(A);
+      load_scale();
 #pragma unroll
-    for (int i = 0; i < kN; ++i) load(i);
-    load_scale();
-    load_rope(0);
-    load_rope(1);
-    tw.next(A);
-    rec.find(A, tw, key0, lane);
+      for (int i = 0; i < kN; ++i) load(i);
+      load_rope(0);
+      load_rope(1);
+      tw.next(A);
+      rec.find(A, tw, key0, lane);
+    };
+    load_tile();
     for (uint32_t kk = 0; on; ++kk) {
       if (n < kN) {  // the end of a context
 #pragma unroll
@@ -918,9 +920,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       bad |= !(sc <= kMaxScale);
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
-      n = rec.take(A);
       on = tw.on();
-      load_scale();
       if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
       uint8_t* tile = sm.kv[kk & 1][0];
       if (slow) store(std::true_type{}, mine, tile);
@@ -937,13 +937,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         }
         bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
         *reinterpret_cast<uint4*>(tile + 8 * kCtaKeys * 128 + sw128_off(kN * kw + 4 * i + (lane >> 3), lane & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-        load_rope(i);
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full[kk & 1]);
-      tw.next(A);
-      rec.find(A, tw, key0, lane);
+      load_tile();  // after the fence, which would wait for loads in flight
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
     if (bad) latch_error(err, SMLA_ERR_RANGE);
