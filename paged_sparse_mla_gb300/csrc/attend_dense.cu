@@ -215,7 +215,7 @@ struct __align__(1024) PairSmem {
   uint8_t p1[kCtaRows * 128];              // P for keys 64-127 of a tile (keys 0-63: the tile's rope chunk): [64 rows][64 keys]
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
-  uint64_t k_full[2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive
+  uint64_t k_full[2][2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive (K: by halves)
   uint64_t s_full[2], kv_free[2];                            // completed by the MMAs in both CTAs
   uint64_t final_bar;
   int64_t x0, total, seq_at;           // start of the pair's range of work; all work, over `pairs` pairs; (plan)
@@ -670,7 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     mbar_init(&sm.q_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.final_bar, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], 2 * kKWarps);
+      mbar_init(&sm.k_full[i][0], 2 * kKWarps);
+      mbar_init(&sm.k_full[i][1], 2 * kKWarps);
       mbar_init(&sm.v_full[i], 2 * kVWarps);
       mbar_init(&sm.kv_free[i], 1);
       mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
@@ -711,16 +712,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_test(bar, parity));
       };
-      // S = Q . K^T of tile k1 into score buffer k1 % 2
-      const auto mma1 = [&]() {
+      // S = Q . K^T of tile k1 into score buffer k1 % 2: its dims 0-255, then the others
+      const auto mma1 = [&](int part) {
         const uint32_t buf = k1 & 1;
+        const int end = part == 0 ? 4 : kChunks;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c)
+        for (int c = 4 * part; c < end; ++c)
           unrolled<4>([&](auto x) {
             mma2_f16<x() * 32, x() * 32>(tmem_s + buf * 64, dq_lo + c * (kChunk >> 4), dk_hi,
                                          dk_lo + (buf * kTileBytes + c * kChunk) / 16, dk_hi, idesc1, (c | x()) != 0, elected);
           });
+        if (part == 0) return;
         commit2(&sm.s_full[buf], elected);
         ++k1;
       };
@@ -748,12 +751,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         // Whichever is ready: P . V of the oldest tile with written probabilities (it frees the tile
         // buffer), else the next tile's scores (so that they are formed while the softmax works).
         uint64_t t0 = 0;
+        int half = 0;  // of tile k1's scores
         for (uint32_t idle = 0; ok && k2 < end;) {
           if (k2 < k1 && ready(&sm.p_full, k2 & 1) && ready(&sm.v_full[k2 & 1], (k2 >> 1) & 1)) {
             mma2(k2 == begin);
             idle = 0;
-          } else if (k1 < end && ready(&sm.k_full[k1 & 1], (k1 >> 1) & 1) && ready(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1)) {
-            mma1();
+          } else if (k1 < end && ready(&sm.k_full[k1 & 1][half], (k1 >> 1) & 1) &&
+                     (half == 1 || ready(&sm.s_free[k1 & 1], ((k1 >> 1) & 1) ^ 1))) {
+            mma1(half);
+            half ^= 1;
             idle = 0;
           } else if ((++idle & 63u) == 0) {  // as pair_wait: give up after kWaitLimitNs
             const uint64_t t = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
@@ -864,31 +870,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
-    // Warp kw takes keys 8 kw .. + 7, as for V: a key's codes are one load, the rope of four keys another.
+    // Warp kw takes keys 8 kw .. + 7.  A lane loads eight codes of a key at a time, so that dims 0-255 of all
+    // keys are handed over while the others are still converted.
     // Lane 4 i + x keeps scale x of key i.
     static_assert(kKRegs == kLaunchRegs, "no change of registers");
     constexpr int kN = kKeysPerK;
     const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
-    const int odd = (lane >> 2) & 1;
-    const uint32_t dst = (lane >> 2) * kCtaKeys * 128 + sw128_off(kN * kw, 2 * (lane & 3) + odd);
-    const uint32_t full[2] = {map_cta(smem_u32(&sm.k_full[0]), 0), map_cta(smem_u32(&sm.k_full[1]), 0)};
-    uint4 codes[kN];
+    const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
+    const uint32_t full = map_cta(smem_u32(&sm.k_full[0][0]), 0);
+    uint2 codes[2][kN];
     uint4 rope[2];
     float sc;
     Records<kRuns, kN> rec;
-    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(i)) + lane); };
+    const auto load = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) codes[h][i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + 256 * h) + lane);
+    };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3))); };
     const auto load_rope = [&](int i) {
       rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
-    const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
+    const auto store = [&](auto slow, auto h, uint32_t mine, uint8_t* tile) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
-        const uint4 c = codes[i];
-        uint8_t* to = tile + 128 * i;
-        *reinterpret_cast<uint4*>(to + (dst ^ (i << 4))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
-        *reinterpret_cast<uint4*>(to + (dst ^ (i << 4) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h() + (lane >> 4));
+        *reinterpret_cast<uint4*>(tile + 128 * i + 4 * kCtaKeys * 128 * h() + (dst ^ (i << 4))) = dequant8<slow()>(codes[h()][i], s);
       }
     };
     TileWalk tw;
@@ -911,7 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       if (n < kN) {  // the end of a context
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          if (i >= n) codes[i] = make_uint4(0, 0, 0, 0);
+          if (i >= n) codes[0][i] = codes[1][i] = make_uint2(0, 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
@@ -923,8 +929,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       on = tw.on();
       if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
       uint8_t* tile = sm.kv[kk & 1][0];
-      if (slow) store(std::true_type{}, mine, tile);
-      else store(std::false_type{}, mine, tile);
+      if (slow) store(std::true_type{}, std::integral_constant<int, 0>{}, mine, tile);
+      else store(std::false_type{}, std::integral_constant<int, 0>{}, mine, tile);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(full + 16 * (kk & 1));
+      if (slow) store(std::true_type{}, std::integral_constant<int, 1>{}, mine, tile);
+      else store(std::false_type{}, std::integral_constant<int, 1>{}, mine, tile);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
@@ -940,7 +951,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive_cluster(full[kk & 1]);
+      if (lane == 0) arrive_cluster(full + 16 * (kk & 1) + 8);
       load_tile();  // after the fence, which would wait for loads in flight
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
