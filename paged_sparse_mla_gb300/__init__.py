@@ -429,53 +429,86 @@ def make_rope(cos_sin, interleaved, idx_interleaved=False, idx_rope=True) -> Rop
     return rope
 
 
-def _need_rope(layout, rope, positions, n):
-    """The rotation's table fits the layout and lies with the other tensors; a position per token."""
+# The calls below take a few microseconds of GPU time for a decode step, so their checks are kept lean: what a
+# tensor must hold is checked argument by argument (_take), where it lies is checked once for the whole call
+# (_on_device).
+
+_BF16, _F32, _U8, _I32, _I64T = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.int64
+
+
+def _take(t, dtype, name, n):
+    """Address of a contiguous tensor of `dtype` with at least n elements; None passes."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: needs at least {n} elements, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libsmla takes contiguous tensors only")
+    return t.data_ptr()
+
+
+def _take_rows(t, name, shape):
+    """(address, element strides of the leading axes) of a bf16 tensor of exactly `shape` whose last axis is
+    contiguous; its leading axes may have any stride.  None passes."""
+    if t is None:
+        return None, (0,) * (len(shape) - 1)
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: its last axis has to be contiguous, got strides {strides}")
+    return t.data_ptr(), strides[:-1]
+
+
+def _on_device(tensors, stream):
+    """The stream's handle, after checking that every tensor lies on the current device."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("libsmla takes CUDA tensors only")
+            if dev < 0:
+                dev = torch.cuda.current_device()
+            if d != dev:
+                raise ValueError(f"tensor on cuda:{d}, but the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rope_args(layout, rope, positions, n):
+    """(descriptor, address of the positions) of an optional rotation whose table fits the layout."""
     if rope is None:
-        return
+        return None, None
     if rope.table.shape[1] != layout.d_rope:
         raise ValueError(f"cos_sin: rows of d_rope = {layout.d_rope} expected, got shape {tuple(rope.table.shape)}")
     if positions is None:
         raise ValueError("positions: needed with a rotation")
-    _need(positions, torch.int64, "positions", n)
-    _ptr(rope.table)
-
-
-def _rows(t, dtype, name, shape):
-    """(pointer, element strides of the leading axes) of a tensor whose last axis is contiguous and whose
-    shape is exactly `shape`; its leading axes may have any stride.  None passes as (None, zeros)."""
-    if t is None:
-        return None, (0,) * (len(shape) - 1)
-    _expect(t, dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: its last axis has to be contiguous, got strides {t.stride()}")
-    if not t.is_cuda:
-        raise ValueError("libsmla takes CUDA tensors only")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return t.data_ptr(), t.stride()[:-1]
+    return ctypes.byref(rope), _take(positions, _I64T, "positions", n)
 
 
 def kvpack_append(layout, pool, layer, latent, rope_key, idx_k, rope, positions, slot_mapping, latent_norm=None,
                   idx_norm=None, idx_bias=None, eps=1e-6, stream=None):
     """Norm, rotate, quantise and store new tokens.  latent [n, d_latent], rope_key [n, d_rope] and idx_k
     [n, d_index] (or None) are bf16 with contiguous rows any distance apart; rope is a Rope or None."""
-    _expect(slot_mapping, torch.int64, "slot_mapping")
     n = slot_mapping.numel()
-    _need(pool, torch.uint8, "pool", layout.pool_bytes)
-    _need(latent_norm, torch.float32, "latent_norm", layout.d_latent)
-    _need(idx_norm, torch.float32, "idx_norm", layout.d_index)
-    _need(idx_bias, torch.float32, "idx_bias", layout.d_index)
-    _need_rope(layout, rope, positions, n)
-    lat, (lat_s,) = _rows(latent, torch.bfloat16, "latent", (n, layout.d_latent))
-    rk, (rk_s,) = _rows(rope_key if layout.d_rope else None, torch.bfloat16, "rope_key", (n, layout.d_rope))
-    ik, (ik_s,) = _rows(idx_k, torch.bfloat16, "idx_k", (n, layout.d_index))
-    _check(lib().kvpack_append(ctypes.byref(layout), _ptr(pool), layer, lat, lat_s, rk, rk_s, ik, ik_s,
-                               _ptr(latent_norm), _ptr(idx_norm), _ptr(idx_bias), eps,
-                               None if rope is None else ctypes.byref(rope), _ptr(positions), _ptr(slot_mapping), n,
-                               _stream(stream)), "kvpack_append")
+    d_latent, d_rope, d_index = layout.d_latent, layout.d_rope, layout.d_index
+    slots = _take(slot_mapping, _I64T, "slot_mapping", n)
+    pl = _take(pool, _U8, "pool", layout.pool_bytes)
+    ln = _take(latent_norm, _F32, "latent_norm", d_latent)
+    kn = _take(idx_norm, _F32, "idx_norm", d_index)
+    kb = _take(idx_bias, _F32, "idx_bias", d_index)
+    rp, pos = _rope_args(layout, rope, positions, n)
+    lat, (lat_s,) = _take_rows(latent, "latent", (n, d_latent))
+    rk, (rk_s,) = _take_rows(rope_key if d_rope else None, "rope_key", (n, d_rope))
+    ik, (ik_s,) = _take_rows(idx_k, "idx_k", (n, d_index))
+    st = _on_device((pool, latent, rope_key if d_rope else None, idx_k, slot_mapping, latent_norm, idx_norm, idx_bias,
+                     None if rp is None else rope.table, None if rp is None else positions), stream)
+    _check((_LIB or lib()).kvpack_append(ctypes.byref(layout), pl, layer, lat, lat_s, rk, rk_s, ik, ik_s, ln, kn, kb,
+                                         eps, rp, pos, slots, n, st), "kvpack_append")
 
 
 def smla_query_prep(layout, params, rope, positions, q_pe=None, q_pe_out=None, q_idx=None, w=None, w_scale=1.0,
@@ -485,25 +518,26 @@ def smla_query_prep(layout, params, rope, positions, q_pe=None, q_pe_out=None, q
     if q_pe is None and q_idx is None:
         raise ValueError("smla_query_prep: needs q_pe or q_idx")
     n = (q_idx if q_pe is None else q_pe).shape[0]
-    H, HI = params.n_heads, params.n_idx_heads
-    _need_rope(layout, rope, positions, n)
-    pe, (pe_t, pe_h) = _rows(q_pe, torch.bfloat16, "q_pe", (n, H, layout.d_rope))
-    ix, (ix_t, ix_h) = _rows(q_idx, torch.bfloat16, "q_idx", (n, HI, layout.d_index))
+    H, HI, d_rope, d_index = params.n_heads, params.n_idx_heads, layout.d_rope, layout.d_index
+    rp, pos = _rope_args(layout, rope, positions, n)
+    pe, (pe_t, pe_h) = _take_rows(q_pe, "q_pe", (n, H, d_rope))
+    ix, (ix_t, ix_h) = _take_rows(q_idx, "q_idx", (n, HI, d_index))
+    po = wp = co = wo = None
     if q_pe is not None:
         if q_pe_out is None:
             raise ValueError("q_pe_out: needed with q_pe")
-        _need(q_pe_out, torch.bfloat16, "q_pe_out", n * H * layout.d_rope)
+        po = _take(q_pe_out, _BF16, "q_pe_out", n * H * d_rope)
     if q_idx is not None:
         if w is None or q_idx_out is None or w_out is None:
             raise ValueError("w, q_idx_out and w_out: needed with q_idx")
-        _need(w, torch.float32, "w", n * HI)
-        _need(q_idx_out, torch.uint8, "q_idx_out", n * HI * layout.d_index)
-        _need(w_out, torch.float32, "w_out", n * HI)
-    _need(idx_norm, torch.float32, "idx_norm", layout.d_index)
-    _check(lib().smla_query_prep(ctypes.byref(layout), ctypes.byref(params),
-                                 None if rope is None else ctypes.byref(rope), _ptr(positions), pe, pe_t, pe_h,
-                                 _ptr(q_pe_out), ix, ix_t, ix_h, _ptr(idx_norm), eps, _ptr(w), w_scale,
-                                 _ptr(q_idx_out), _ptr(w_out), n, _stream(stream)), "smla_query_prep")
+        wp = _take(w, _F32, "w", n * HI)
+        co = _take(q_idx_out, _U8, "q_idx_out", n * HI * d_index)
+        wo = _take(w_out, _F32, "w_out", n * HI)
+    kn = _take(idx_norm, _F32, "idx_norm", d_index)
+    st = _on_device((q_pe, q_idx, q_pe_out, q_idx_out, w, w_out, idx_norm, None if rp is None else rope.table,
+                     None if rp is None else positions), stream)
+    _check((_LIB or lib()).smla_query_prep(ctypes.byref(layout), ctypes.byref(params), rp, pos, pe, pe_t, pe_h, po, ix,
+                                           ix_t, ix_h, kn, eps, wp, w_scale, co, wo, n, st), "smla_query_prep")
 
 
 def attend_dense_workspace_size(layout, params, n_tokens) -> int:
@@ -514,19 +548,24 @@ def smla_attend_dense(layout, params, pool, layer, q, q_pe, block_table, seq_len
                       workspace=None, stream=None):
     """Latent attention over the whole visible context.  `lse` is optional; `workspace` (uint8 device tensor
     of at least attend_dense_workspace_size(...) bytes, optional) lets long contexts split over the SMs."""
-    T, H = q.shape[0], params.n_heads
-    _need(pool, torch.uint8, "pool", layout.pool_bytes)
-    _need(q, torch.bfloat16, "q", T * H * layout.d_latent)
-    _need(q_pe, torch.bfloat16, "q_pe", T * H * layout.d_rope)
-    _need_geometry(block_table, seq_lens, query_start_loc, seq_lens.numel())
-    _need(out, torch.bfloat16, "out", T * H * layout.d_latent)
-    _need(lse, torch.float32, "lse", T * H)
-    _need(workspace, torch.uint8, "workspace")
-    _check(lib().smla_attend_dense(ctypes.byref(layout), ctypes.byref(params), _ptr(pool), layer, _ptr(q), _ptr(q_pe),
-                                   _ptr(block_table), block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc),
-                                   seq_lens.numel(), T, _ptr(out), _ptr(lse), _ptr(workspace),
-                                   0 if workspace is None else workspace.numel(), _stream(stream)),
-           "smla_attend_dense")
+    T = q.shape[0]
+    rows = T * params.n_heads
+    batch = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
+        raise ValueError(f"block_table: needs a row per sequence ({batch}), got shape {tuple(block_table.shape)}")
+    pl = _take(pool, _U8, "pool", layout.pool_bytes)
+    qa = _take(q, _BF16, "q", rows * layout.d_latent)
+    pe = _take(q_pe, _BF16, "q_pe", rows * layout.d_rope)
+    bt = _take(block_table, _I32, "block_table", 0)
+    sl = _take(seq_lens, _I32, "seq_lens", batch)
+    qs = _take(query_start_loc, _I32, "query_start_loc", batch + 1)
+    oa = _take(out, _BF16, "out", rows * layout.d_latent)
+    la = _take(lse, _F32, "lse", rows)
+    ws = _take(workspace, _U8, "workspace", 0)
+    st = _on_device((q, pool, q_pe, block_table, seq_lens, query_start_loc, out, lse, workspace), stream)
+    _check((_LIB or lib()).smla_attend_dense(ctypes.byref(layout), ctypes.byref(params), pl, layer, qa, pe, bt,
+                                             block_table.shape[1], sl, qs, batch, T, oa, la, ws,
+                                             0 if workspace is None else workspace.numel(), st), "smla_attend_dense")
 
 
 def smla_selftest_wait(limit_ns, stream=None):
