@@ -68,12 +68,14 @@ __device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, bool vec, floa
   for (int i = 0; i < N; ++i) x[i] = __bfloat162float(p[i]);
 }
 
-// amax -> (scale, its reciprocal) for codes of largest magnitude `top`.
-__device__ __forceinline__ void quant_scale(float amax, float top, float& scale, float& inv) {
+// amax -> (scale, its reciprocal) for codes of largest magnitude `top` = 1 / rtop.  Each is within two units of
+// the last place of the quotient; a scale that is a little small saturates.
+__device__ __forceinline__ void quant_scale(float amax, float rtop, float& scale, float& inv) {
   const bool tiny = amax < kTinyAmax;
-  scale = tiny ? 1.0f : amax / top;
-  inv = tiny ? 1.0f : top / amax;
+  scale = tiny ? 1.0f : amax * rtop;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
 }
+constexpr float kRE4M3 = 1.0f / 448.0f, kRE2M1 = 1.0f / 6.0f;
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -193,11 +195,18 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
   const int lanes_per_tile = L.quant_tile / E;
   for (int m = 1; m < lanes_per_tile; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
   float scale, inv;
-  quant_scale(amax, 448.0f, scale, inv);
+  quant_scale(amax, kRE4M3, scale, inv);
+  // the record is 16-byte aligned: a lane's codes leave as one store
+  if constexpr (E == 2) {
+    reinterpret_cast<uint16_t*>(rec)[lane] = static_cast<uint16_t>(e4m3x2(x[0] * inv, x[1] * inv));
+  } else {
+    uint32_t w[E / 4];
 #pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    const uint32_t w = e4m3x2(x[i] * inv, x[i + 1] * inv);
-    reinterpret_cast<uint16_t*>(rec + lane * E)[i / 2] = static_cast<uint16_t>(w);
+    for (int i = 0; i < E / 4; ++i)
+      w[i] = e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+    if constexpr (E == 16) reinterpret_cast<uint4*>(rec)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (E == 8) reinterpret_cast<uint2*>(rec)[lane] = make_uint2(w[0], w[1]);
+    else reinterpret_cast<uint32_t*>(rec)[lane] = w[0];
   }
   if ((lane * E) % L.quant_tile == 0) reinterpret_cast<float*>(rec + L.d_latent)[(lane * E) / L.quant_tile] = scale;
 
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
   for (int i = 0; i < EK; ++i) kmax = fmaxf(kmax, fabsf(z[i]));
   float kscale, kinv;
   const bool fp4 = L.key_format == SMLA_KEY_E2M1;
-  quant_scale(warp_max(kmax), fp4 ? 6.0f : 448.0f, kscale, kinv);
+  quant_scale(warp_max(kmax), fp4 ? kRE2M1 : kRE4M3, kscale, kinv);
   uint8_t* kdst = base + L.idx_key_off + static_cast<int64_t>(off) * L.key_bytes;
   if (fp4) {
     if constexpr (EK == 1) {
@@ -244,6 +253,11 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
         kdst[(lane * EK + i) / 2] =
             __nv_cvt_float2_to_fp4x2(make_float2(z[i] * kinv, z[i + 1] * kinv), __NV_E2M1, cudaRoundNearest);
     }
+  } else if constexpr (EK >= 4) {
+#pragma unroll
+    for (int i = 0; i < EK; i += 4)
+      *reinterpret_cast<uint32_t*>(kdst + lane * EK + i) =
+          e4m3x2(z[i] * kinv, z[i + 1] * kinv) | e4m3x2(z[i + 2] * kinv, z[i + 3] * kinv) << 16;
   } else {
 #pragma unroll
     for (int i = 0; i < EK; ++i)
@@ -318,11 +332,308 @@ __global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryArgs A) {
 #pragma unroll
   for (int i = 0; i < EK; ++i) amax = fmaxf(amax, fabsf(z[i]));
   float scale, inv;
-  quant_scale(warp_max(amax), 448.0f, scale, inv);
+  quant_scale(warp_max(amax), kRE4M3, scale, inv);
   uint8_t* dst = A.codes + (t * A.n_idx_heads + h) * A.d_index + lane * EK;
 #pragma unroll
   for (int i = 0; i < EK; ++i) dst[i] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(z[i] * inv, __NV_SATFINITE, __NV_E4M3));
   if (lane == 0) A.w_out[t * A.n_idx_heads + h] = __ldg(A.w + t * A.n_idx_heads + h) * A.w_scale * scale;
+}
+
+// Cosines and sines for the eight consecutive elements that start at element 8 s of a vector whose first 64
+// elements rotate: interleaved, those of pairs 4 s .. + 3 (in the first four); halves, those of pairs
+// 8 (s % 4) .. + 7 with the sine's sign as the element's place in its pair wants it.  Past the rotated
+// elements (s >= 8) the angle is zero.
+__device__ __forceinline__ void load_angles(const float* cs, int s, bool interleaved, float (&c)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = 1.f;
+    sn[i] = 0.f;
+  }
+  if (s >= 8) return;
+  const float4* p = reinterpret_cast<const float4*>(cs + (interleaved ? 4 * s : 8 * (s & 3)));
+  const float4 a = __ldg(p), b = __ldg(p + 8);
+  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+  sn[0] = b.x, sn[1] = b.y, sn[2] = b.z, sn[3] = b.w;
+  if (interleaved) return;
+  const float4 d = __ldg(p + 1), e = __ldg(p + 9);
+  c[4] = d.x, c[5] = d.y, c[6] = d.z, c[7] = d.w;
+  sn[4] = e.x, sn[5] = e.y, sn[6] = e.z, sn[7] = e.w;
+  if (s < 4) {  // first elements: a c - b s, second: b c + a s
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+  }
+}
+
+// Rotates a lane's eight consecutive elements; halves pair with the lane four away.
+__device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[8], const float (&sn)[8], bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * c[i] - b * sn[i];
+      x[2 * i + 1] = a * sn[i] + b * c[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + __shfl_xor_sync(0xffffffffu, x[i], 4) * sn[i];
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(ws[i] << 16);
+    x[2 * i + 1] = __uint_as_float(ws[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
+  return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16,
+                    e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16);
+}
+// sum and maximum over the half-warp
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float half_max8(const float (&x)[8]) {
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v = fmaxf(v, fabsf(x[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// kvpack_append for the full shape (512 latent dims in tiles of 128, 64 rope and 128 indexer dims), 16-byte
+// aligned rows: two warps per token, since a token's two parts do not meet and a few tokens are a matter of
+// latency.  Warp 0: the latent, a lane dims 8 l .. + 7 and 256 + 8 l .. + 7, so that rows, norm weights and
+// codes are coalesced and a quantisation tile is a half-warp.  Warp 1: the indexer key (eight dims a lane of
+// the first half-warp) and the rope key (eight lanes of the second).
+constexpr int kAppendTokens = 4;  // of a CTA
+template <bool kFp4>
+__global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const AppendArgs A) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kAppendTokens + (warp >> 1);
+  if (t >= A.n_tokens) return;
+  const KernelLayout& L = A.L;
+  const int64_t slot = __ldg(A.slots + t);
+  const int64_t pos = A.rope.cos_sin ? __ldg(A.rope.positions + t) : 0;
+  const int sub = lane & 15, s8 = lane & 7;
+  const bool key_part = (warp & 1) != 0, is_key = lane < 16;
+  uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+  if (!key_part) {
+    const uint4* src = reinterpret_cast<const uint4*>(A.latent + t * A.latent_stride);
+    v0 = __ldg(src + lane);
+    v1 = __ldg(src + 32 + lane);
+  } else if (is_key) {
+    if (A.idx_k) v0 = __ldg(reinterpret_cast<const uint4*>(A.idx_k + t * A.idx_stride) + sub);
+  } else {
+    v0 = __ldg(reinterpret_cast<const uint4*>(A.rope_key + t * A.rope_stride) + s8);  // lanes 24-31 as 16-23
+  }
+  if (slot < 0) return;
+  if (slot >= L.num_blocks * L.block_size || (A.rope.cos_sin && (pos < 0 || pos >= A.rope.n_positions))) {
+    if (lane == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
+    return;
+  }
+  const int64_t blk = slot / L.block_size;
+  const int off = static_cast<int>(slot - blk * L.block_size);
+  uint8_t* base = A.pool + blk * L.block_stride + static_cast<int64_t>(A.layer) * L.layer_stride;
+  uint8_t* rec = base + L.rec_off + static_cast<int64_t>(off) * L.rec_stride;
+  float x[8], w[8];
+  unpack8(v0, x);
+  if (!key_part) {
+    float y[8];
+    unpack8(v1, y);
+    if (A.latent_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
+      const float rstd = rsqrtf(warp_sum(ss) / 512.0f + A.eps);
+      load8(A.latent_norm + 8 * lane, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * w[i];
+      load8(A.latent_norm + 256 + 8 * lane, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * rstd * w[i];
+    }
+    float sx, ix, sy, iy;
+    quant_scale(half_max8(x), kRE4M3, sx, ix);
+    quant_scale(half_max8(y), kRE4M3, sy, iy);
+    reinterpret_cast<uint2*>(rec)[lane] = codes8(x, ix);
+    reinterpret_cast<uint2*>(rec)[32 + lane] = codes8(y, iy);
+    if (sub == 0) {
+      float* sc = reinterpret_cast<float*>(rec + 512) + (lane >> 4);
+      sc[0] = sx;
+      sc[2] = sy;
+    }
+    return;
+  }
+  const float* cs = A.rope.cos_sin ? A.rope.cos_sin + pos * 64 : nullptr;
+  // the norm of the key, in the first half-warp (the sums of the second are not used)
+  if (A.idx_k && A.idx_norm) {
+    const float mean = A.idx_bias ? half_sum(((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]))) / 128.0f : 0.f;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += (x[i] - mean) * (x[i] - mean);
+    const float rstd = rsqrtf(half_sum(ss) / 128.0f + A.eps);
+    if (is_key) {
+      load8(A.idx_norm + 8 * sub, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = (x[i] - mean) * rstd * w[i];
+      if (A.idx_bias) {
+        load8(A.idx_bias + 8 * sub, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] += w[i];
+      }
+    }
+  }
+  // Key and rope may pair their elements differently: the halves' exchange is done for both and taken where
+  // it belongs.
+  if (cs) {
+    const bool inter = is_key ? A.rope.idx_interleaved : A.rope.interleaved;
+    const int s = is_key ? (A.rope.idx_rope ? sub : 8) : s8;
+    float c[8], sn[8];
+    load_angles(cs, s, inter, c, sn);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __shfl_xor_sync(0xffffffffu, x[i], 4);
+    if (inter) {
+      rotate8(x, c, sn, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + w[i] * sn[i];
+    }
+  }
+  const float amax = half_max8(x);
+  if (!is_key) {
+    if (lane < 24)
+      reinterpret_cast<uint4*>(rec + 528)[s8] =
+          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    return;
+  }
+  if (!A.idx_k) return;
+  float scale, inv;
+  quant_scale(amax, kFp4 ? kRE2M1 : kRE4M3, scale, inv);
+  uint8_t* kdst = base + L.idx_key_off + static_cast<int64_t>(off) * L.key_bytes;
+  if constexpr (kFp4) {
+    uint32_t q = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_E2M1, cudaRoundNearest)) << (8 * i);
+    reinterpret_cast<uint32_t*>(kdst)[sub] = q;
+  } else {
+    reinterpret_cast<uint2*>(kdst)[sub] = codes8(x, inv);
+  }
+  if (sub == 0) reinterpret_cast<float*>(base + L.idx_scale_off)[off] = scale;
+}
+
+// smla_query_prep for 128 indexer dims and 64 rope dims, everything 16-byte aligned: one CTA per token.  Sixteen
+// lanes hold an indexer head (eight dims each), eight lanes a q_pe head, so that a row is one coalesced
+// 16-byte load a lane, its sums and maxima four shuffles, and the angles, loaded once a token, stay in
+// registers for all heads.  Bound by memory: 8,192 tokens of 64 + 64 heads, 342 MB, QUERY_FIGURE (the kernel above, a
+// warp per row with rotations through shared memory and byte stores: 254 us).
+constexpr int kQWarps = 8;
+__global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArgs A) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x;
+  const int sub = lane & 15, hi = lane >> 4, s8 = lane & 7;
+  const float* cs = nullptr;
+  int64_t pos = 0;
+  if (A.rope.cos_sin) pos = __ldg(A.rope.positions + t);
+  // the first rows are asked for before the position is known to be good
+  constexpr int kIt = 4;
+  uint4 v[kIt];
+  float wv[kIt];
+  uint8_t* codes = A.codes + t * A.n_idx_heads * 128;
+  const int idx_pairs = A.q_idx ? (A.n_idx_heads + 1) / 2 : 0;
+  const auto ask = [&](int i, int it) {
+    const int h = 2 * it + hi;
+    v[i] = make_uint4(0, 0, 0, 0);
+    wv[i] = 0.f;
+    if (it < idx_pairs && h < A.n_idx_heads) {
+      v[i] = __ldg(reinterpret_cast<const uint4*>(A.q_idx + t * A.idx_token + h * A.idx_head) + sub);
+      wv[i] = __ldg(A.w + t * A.n_idx_heads + h);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) ask(i, warp + kQWarps * i);
+  const int pe_quads = A.q_pe ? (A.n_heads + 3) / 4 : 0;
+  constexpr int kPe = 2;
+  uint4 pv[kPe];
+  const auto ask_pe = [&](int it) -> uint4 {
+    const int h = 4 * it + (lane >> 3);
+    if (it < pe_quads && h < A.n_heads)
+      return __ldg(reinterpret_cast<const uint4*>(A.q_pe + t * A.pe_token + h * A.pe_head) + s8);
+    return make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < kPe; ++i) pv[i] = ask_pe(warp + kQWarps * i);
+  float c[8], sn[8], norm[8];
+  if (A.rope.cos_sin) {
+    if (pos < 0 || pos >= A.rope.n_positions) {
+      if (threadIdx.x == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
+      return;
+    }
+    cs = A.rope.cos_sin + pos * 64;
+  }
+  // ---- indexer heads ----
+  const bool turn = cs != nullptr && A.rope.idx_rope;
+  if (idx_pairs > 0) {
+    if (turn) load_angles(cs, sub, A.rope.idx_interleaved, c, sn);
+    if (A.idx_norm) load8(A.idx_norm + 8 * sub, norm);
+  }
+  for (int it0 = warp; it0 < idx_pairs; it0 += kQWarps * kIt) {
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) {
+      const int it = it0 + kQWarps * i, h = 2 * it + hi;
+      if (it >= idx_pairs) break;
+      float x[8];
+      unpack8(v[i], x);
+      if (A.idx_norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+        const float rstd = rsqrtf(half_sum(ss) / 128.0f + A.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * norm[e];
+      }
+      if (turn) rotate8(x, c, sn, A.rope.idx_interleaved);
+      float scale, inv;
+      quant_scale(half_max8(x), kRE4M3, scale, inv);
+      if (h < A.n_idx_heads) {
+        reinterpret_cast<uint2*>(codes + h * 128)[sub] = codes8(x, inv);
+        if (sub == 0) A.w_out[t * A.n_idx_heads + h] = wv[i] * A.w_scale * scale;
+      }
+    }
+    if (it0 + kQWarps * kIt < idx_pairs) {
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) ask(i, it0 + kQWarps * (kIt + i));
+    }
+  }
+  // ---- q_pe ----
+  if (pe_quads > 0 && cs != nullptr) load_angles(cs, s8, A.rope.interleaved, c, sn);
+  for (int it0 = warp; it0 < pe_quads; it0 += kQWarps * kPe) {
+#pragma unroll
+    for (int i = 0; i < kPe; ++i) {
+      const int it = it0 + kQWarps * i, h = 4 * it + (lane >> 3);
+      if (it >= pe_quads) break;
+      float x[8];
+      unpack8(pv[i], x);
+      if (cs != nullptr) rotate8(x, c, sn, A.rope.interleaved);
+      if (h < A.n_heads)
+        reinterpret_cast<uint4*>(A.q_pe_out + (t * A.n_heads + h) * 64)[s8] =
+            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    if (it0 + kQWarps * kPe < pe_quads) {
+#pragma unroll
+      for (int i = 0; i < kPe; ++i) pv[i] = ask_pe(it0 + kQWarps * (kPe + i));
+    }
+  }
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -405,6 +716,15 @@ extern "C" smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, 
   A.vec_latent = aligned(latent, 16) && latent_stride % 8 == 0;
   A.vec_idx = aligned(idx_k, 16) && idx_k_stride % 8 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The full shape with rows that load as 16-byte pieces takes the kernel built for it.
+  if (L.d_latent == 512 && L.quant_tile == 128 && L.d_rope == 64 && L.d_index == 128 && A.vec_latent &&
+      aligned(rope_key, 16) && rope_stride % 8 == 0 && (!idx || A.vec_idx) && aligned(latent_norm, 16) &&
+      aligned(idx_norm, 16) && aligned(idx_bias, 16) && aligned(A.rope.cos_sin, 16)) {
+    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kAppendTokens - 1) / kAppendTokens);
+    if (L.key_format == SMLA_KEY_E2M1) append_full_kernel<true><<<blocks, 64 * kAppendTokens, 0, s>>>(A);
+    else append_full_kernel<false><<<blocks, 64 * kAppendTokens, 0, s>>>(A);
+    return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  }
   switch (L.d_latent / 32) {
     case 2: launch_append<2>(A, L.d_index, s); break;
     case 4: launch_append<4>(A, L.d_index, s); break;
@@ -455,10 +775,18 @@ extern "C" smla_status_t smla_query_prep(const smla_layout_t* layout, const smla
   A.d_index = layout->d_index;
   A.rope = rope_args(rope, positions, layout->d_rope);
   A.vec_idx = aligned(q_idx, 16) && q_idx_token_stride % 8 == 0 && q_idx_head_stride % 8 == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Rows that load as 16-byte pieces take the kernel built for them.
+  if ((!idx || (layout->d_index == 128 && A.vec_idx && aligned(q_idx_out, 8) && aligned(idx_norm, 16))) &&
+      (layout->d_rope == 64 || (!pe && !(A.rope.cos_sin && A.rope.idx_rope))) &&
+      (!pe || (aligned(q_pe, 16) && q_pe_token_stride % 8 == 0 && q_pe_head_stride % 8 == 0 && aligned(q_pe_out, 16))) &&
+      aligned(A.rope.cos_sin, 16)) {
+    query_full_kernel<<<n_tokens, 32 * kQWarps, 0, s>>>(A);
+    return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  }
   const int64_t rows = static_cast<int64_t>(n_tokens) * ((pe ? A.n_heads : 0) + (idx ? A.n_idx_heads : 0));
   if ((rows + kWarps - 1) / kWarps > 0x7fffffff) return SMLA_ERR_UNSUPPORTED;
   const unsigned blocks = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (idx ? layout->d_index : 32) {
     case 32: query_kernel<1><<<blocks, 32 * kWarps, 0, s>>>(A); break;
     case 64: query_kernel<2><<<blocks, 32 * kWarps, 0, s>>>(A); break;
