@@ -339,61 +339,63 @@ __global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryArgs A) {
   if (lane == 0) A.w_out[t * A.n_idx_heads + h] = __ldg(A.w + t * A.n_idx_heads + h) * A.w_scale * scale;
 }
 
-// Cosines and sines for the eight consecutive elements that start at element 8 s of a vector whose first 64
-// elements rotate: interleaved, those of pairs 4 s .. + 3 (in the first four); halves, those of pairs
-// 8 (s % 4) .. + 7 with the sine's sign as the element's place in its pair wants it.  Past the rotated
-// elements (s >= 8) the angle is zero.
-__device__ __forceinline__ void load_angles(const float* cs, int s, bool interleaved, float (&c)[8], float (&sn)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.f;
-    sn[i] = 0.f;
-  }
-  if (s >= 8) return;
-  const float4* p = reinterpret_cast<const float4*>(cs + (interleaved ? 4 * s : 8 * (s & 3)));
-  const float4 a = __ldg(p), b = __ldg(p + 8);
-  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-  sn[0] = b.x, sn[1] = b.y, sn[2] = b.z, sn[3] = b.w;
-  if (interleaved) return;
-  const float4 d = __ldg(p + 1), e = __ldg(p + 9);
-  c[4] = d.x, c[5] = d.y, c[6] = d.z, c[7] = d.w;
-  sn[4] = e.x, sn[5] = e.y, sn[6] = e.z, sn[7] = e.w;
-  if (s < 4) {  // first elements: a c - b s, second: b c + a s
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+// Eight lanes hold 64 dims, lane j dims 4 j .. + 3 and 32 + 4 j .. + 3: every rotation pair lies in one lane,
+// whether it is (i, i + 32) or (2 i, 2 i + 1), and rows load and store in whole sectors.
+// Cosines and sines of the lane's four pairs: halves, pairs 4 j .. + 3; interleaved, 2 j, 2 j + 1, 16 + 2 j, 17 + 2 j.
+__device__ __forceinline__ void load_angles(const float* cs, int j, bool interleaved, float (&c)[4], float (&sn)[4]) {
+  if (interleaved) {
+    const float2 a = __ldg(reinterpret_cast<const float2*>(cs) + j), b = __ldg(reinterpret_cast<const float2*>(cs) + 8 + j);
+    const float2 d = __ldg(reinterpret_cast<const float2*>(cs) + 16 + j), e = __ldg(reinterpret_cast<const float2*>(cs) + 24 + j);
+    c[0] = a.x, c[1] = a.y, c[2] = b.x, c[3] = b.y;
+    sn[0] = d.x, sn[1] = d.y, sn[2] = e.x, sn[3] = e.y;
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(cs) + j), d = __ldg(reinterpret_cast<const float4*>(cs) + 8 + j);
+    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+    sn[0] = d.x, sn[1] = d.y, sn[2] = d.z, sn[3] = d.w;
   }
 }
 
-// Rotates a lane's eight consecutive elements; halves pair with the lane four away.
-__device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[8], const float (&sn)[8], bool interleaved) {
-  if (interleaved) {
+__device__ __forceinline__ void rotate8(float (&x)[8], const float (&c)[4], const float (&sn)[4], bool interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    if (interleaved) {
       const float a = x[2 * i], b = x[2 * i + 1];
       x[2 * i] = a * c[i] - b * sn[i];
       x[2 * i + 1] = a * sn[i] + b * c[i];
+    } else {
+      const float a = x[i], b = x[i + 4];
+      x[i] = a * c[i] - b * sn[i];
+      x[i + 4] = a * sn[i] + b * c[i];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + __shfl_xor_sync(0xffffffffu, x[i], 4) * sn[i];
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+// The lane's eight bf16 of a row (p: the row's 64 dims) and its eight fp32 of a weight vector.
+struct Raw8 {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ Raw8 load_raw8(const __nv_bfloat16* p, int j) {
+  return {__ldg(reinterpret_cast<const uint2*>(p) + j), __ldg(reinterpret_cast<const uint2*>(p) + 8 + j)};
+}
+__device__ __forceinline__ void unpack8(const Raw8& w, float (&x)[8]) {
+  const uint32_t ws[4] = {w.lo.x, w.lo.y, w.hi.x, w.hi.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(ws[i] << 16);
     x[2 * i + 1] = __uint_as_float(ws[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+__device__ __forceinline__ void load8(const float* p, int j, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p) + j), b = __ldg(reinterpret_cast<const float4*>(p) + 8 + j);
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
-  return make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16,
-                    e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16);
+__device__ __forceinline__ void store_codes8(uint8_t* p, int j, const float (&x)[8], float inv) {
+  reinterpret_cast<uint32_t*>(p)[j] = e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16;
+  reinterpret_cast<uint32_t*>(p)[8 + j] = e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16;
+}
+__device__ __forceinline__ void store_bf16x8(__nv_bfloat16* p, int j, const float (&x)[8]) {
+  reinterpret_cast<uint2*>(p)[j] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  reinterpret_cast<uint2*>(p)[8 + j] = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 // sum and maximum over the half-warp
 __device__ __forceinline__ float half_sum(float v) {
@@ -412,9 +414,9 @@ __device__ __forceinline__ float half_max8(const float (&x)[8]) {
 
 // kvpack_append for the full shape (512 latent dims in tiles of 128, 64 rope and 128 indexer dims), 16-byte
 // aligned rows: two warps per token, since a token's two parts do not meet and a few tokens are a matter of
-// latency.  Warp 0: the latent, a lane dims 8 l .. + 7 and 256 + 8 l .. + 7, so that rows, norm weights and
-// codes are coalesced and a quantisation tile is a half-warp.  Warp 1: the indexer key (eight dims a lane of
-// the first half-warp) and the rope key (eight lanes of the second).
+// latency.  Warp 0: the latent, 64 dims to eight lanes twice (dims 0-255, then the others), so that a
+// quantisation tile is a half-warp.  Warp 1: the indexer key in its first half-warp and the rope key in eight
+// lanes of the second.
 constexpr int kAppendTokens = 4;  // of a CTA
 template <bool kFp4>
 __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const AppendArgs A) {
@@ -424,17 +426,17 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
   const KernelLayout& L = A.L;
   const int64_t slot = __ldg(A.slots + t);
   const int64_t pos = A.rope.cos_sin ? __ldg(A.rope.positions + t) : 0;
-  const int sub = lane & 15, s8 = lane & 7;
+  const int j = lane & 7, g = lane >> 3;  // the lane's place in its 64 dims, and which 64 dims
   const bool key_part = (warp & 1) != 0, is_key = lane < 16;
-  uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+  Raw8 v0 = {}, v1 = {};
   if (!key_part) {
-    const uint4* src = reinterpret_cast<const uint4*>(A.latent + t * A.latent_stride);
-    v0 = __ldg(src + lane);
-    v1 = __ldg(src + 32 + lane);
+    const __nv_bfloat16* src = A.latent + t * A.latent_stride + 64 * g;
+    v0 = load_raw8(src, j);
+    v1 = load_raw8(src + 256, j);
   } else if (is_key) {
-    if (A.idx_k) v0 = __ldg(reinterpret_cast<const uint4*>(A.idx_k + t * A.idx_stride) + sub);
+    if (A.idx_k) v0 = load_raw8(A.idx_k + t * A.idx_stride + 64 * g, j);
   } else {
-    v0 = __ldg(reinterpret_cast<const uint4*>(A.rope_key + t * A.rope_stride) + s8);  // lanes 24-31 as 16-23
+    v0 = load_raw8(A.rope_key + t * A.rope_stride, j);  // lanes 24-31 as 16-23
   }
   if (slot < 0) return;
   if (slot >= L.num_blocks * L.block_size || (A.rope.cos_sin && (pos < 0 || pos >= A.rope.n_positions))) {
@@ -455,19 +457,19 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
       const float rstd = rsqrtf(warp_sum(ss) / 512.0f + A.eps);
-      load8(A.latent_norm + 8 * lane, w);
+      load8(A.latent_norm + 64 * g, j, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = x[i] * rstd * w[i];
-      load8(A.latent_norm + 256 + 8 * lane, w);
+      load8(A.latent_norm + 256 + 64 * g, j, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = y[i] * rstd * w[i];
     }
     float sx, ix, sy, iy;
     quant_scale(half_max8(x), kRE4M3, sx, ix);
     quant_scale(half_max8(y), kRE4M3, sy, iy);
-    reinterpret_cast<uint2*>(rec)[lane] = codes8(x, ix);
-    reinterpret_cast<uint2*>(rec)[32 + lane] = codes8(y, iy);
-    if (sub == 0) {
+    store_codes8(rec + 64 * g, j, x, ix);
+    store_codes8(rec + 256 + 64 * g, j, y, iy);
+    if ((lane & 15) == 0) {
       float* sc = reinterpret_cast<float*>(rec + 512) + (lane >> 4);
       sc[0] = sx;
       sc[2] = sy;
@@ -483,37 +485,26 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
     for (int i = 0; i < 8; ++i) ss += (x[i] - mean) * (x[i] - mean);
     const float rstd = rsqrtf(half_sum(ss) / 128.0f + A.eps);
     if (is_key) {
-      load8(A.idx_norm + 8 * sub, w);
+      load8(A.idx_norm + 64 * g, j, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = (x[i] - mean) * rstd * w[i];
       if (A.idx_bias) {
-        load8(A.idx_bias + 8 * sub, w);
+        load8(A.idx_bias + 64 * g, j, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] += w[i];
       }
     }
   }
-  // Key and rope may pair their elements differently: the halves' exchange is done for both and taken where
-  // it belongs.
-  if (cs) {
-    const bool inter = is_key ? A.rope.idx_interleaved : A.rope.interleaved;
-    const int s = is_key ? (A.rope.idx_rope ? sub : 8) : s8;
-    float c[8], sn[8];
-    load_angles(cs, s, inter, c, sn);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __shfl_xor_sync(0xffffffffu, x[i], 4);
-    if (inter) {
-      rotate8(x, c, sn, true);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + w[i] * sn[i];
-    }
+  if (cs && (is_key ? g == 0 && A.rope.idx_rope : true)) {
+    float c[4], sn[4];
+    const bool interleaved = is_key ? A.rope.idx_interleaved : A.rope.interleaved;
+    load_angles(cs, j, interleaved, c, sn);
+    rotate8(x, c, sn, interleaved);
   }
+  __syncwarp();
   const float amax = half_max8(x);
   if (!is_key) {
-    if (lane < 24)
-      reinterpret_cast<uint4*>(rec + 528)[s8] =
-          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    if (lane < 24) store_bf16x8(reinterpret_cast<__nv_bfloat16*>(rec + 528), j, x);
     return;
   }
   if (!A.idx_k) return;
@@ -521,42 +512,44 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
   quant_scale(amax, kFp4 ? kRE2M1 : kRE4M3, scale, inv);
   uint8_t* kdst = base + L.idx_key_off + static_cast<int64_t>(off) * L.key_bytes;
   if constexpr (kFp4) {
-    uint32_t q = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_E2M1, cudaRoundNearest)) << (8 * i);
-    reinterpret_cast<uint32_t*>(kdst)[sub] = q;
+    const auto four = [&](int i) -> uint16_t {  // elements i .. i + 3
+      return static_cast<uint16_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[i] * inv, x[i + 1] * inv), __NV_E2M1, cudaRoundNearest) |
+                                   __nv_cvt_float2_to_fp4x2(make_float2(x[i + 2] * inv, x[i + 3] * inv), __NV_E2M1, cudaRoundNearest) << 8);
+    };
+    uint16_t* q = reinterpret_cast<uint16_t*>(kdst + 32 * g);
+    q[j] = four(0);
+    q[8 + j] = four(4);
   } else {
-    reinterpret_cast<uint2*>(kdst)[sub] = codes8(x, inv);
+    store_codes8(kdst + 64 * g, j, x, inv);
   }
-  if (sub == 0) reinterpret_cast<float*>(base + L.idx_scale_off)[off] = scale;
+  if (lane == 0) reinterpret_cast<float*>(base + L.idx_scale_off)[off] = scale;
 }
 
 // smla_query_prep for 128 indexer dims and 64 rope dims, everything 16-byte aligned: one CTA per token.  Sixteen
-// lanes hold an indexer head (eight dims each), eight lanes a q_pe head, so that a row is one coalesced
-// 16-byte load a lane, its sums and maxima four shuffles, and the angles, loaded once a token, stay in
-// registers for all heads.  Bound by memory: 8,192 tokens of 64 + 64 heads, 342 MB, QUERY_FIGURE (the kernel above, a
+// lanes hold an indexer head, eight lanes a q_pe head (the lanes' dims: above), so that a row's sums and
+// maxima are four shuffles, its rotation none, and the angles, loaded once a token, stay in registers for
+// all heads.  Bound by memory: 8,192 tokens of 64 + 64 heads, 342 MB, QUERY_FIGURE (the kernel above, a
 // warp per row with rotations through shared memory and byte stores: 254 us).
 constexpr int kQWarps = 8;
 __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArgs A) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = blockIdx.x;
-  const int sub = lane & 15, hi = lane >> 4, s8 = lane & 7;
+  const int hi = lane >> 4, j = lane & 7, g = (lane >> 3) & 1;
   const float* cs = nullptr;
   int64_t pos = 0;
   if (A.rope.cos_sin) pos = __ldg(A.rope.positions + t);
   // the first rows are asked for before the position is known to be good
   constexpr int kIt = 4;
-  uint4 v[kIt];
+  Raw8 v[kIt];
   float wv[kIt];
   uint8_t* codes = A.codes + t * A.n_idx_heads * 128;
   const int idx_pairs = A.q_idx ? (A.n_idx_heads + 1) / 2 : 0;
   const auto ask = [&](int i, int it) {
     const int h = 2 * it + hi;
-    v[i] = make_uint4(0, 0, 0, 0);
+    v[i] = Raw8{};
     wv[i] = 0.f;
     if (it < idx_pairs && h < A.n_idx_heads) {
-      v[i] = __ldg(reinterpret_cast<const uint4*>(A.q_idx + t * A.idx_token + h * A.idx_head) + sub);
+      v[i] = load_raw8(A.q_idx + t * A.idx_token + h * A.idx_head + 64 * g, j);
       wv[i] = __ldg(A.w + t * A.n_idx_heads + h);
     }
   };
@@ -564,16 +557,16 @@ __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArg
   for (int i = 0; i < kIt; ++i) ask(i, warp + kQWarps * i);
   const int pe_quads = A.q_pe ? (A.n_heads + 3) / 4 : 0;
   constexpr int kPe = 2;
-  uint4 pv[kPe];
-  const auto ask_pe = [&](int it) -> uint4 {
+  Raw8 pv[kPe];
+  const auto ask_pe = [&](int it) -> Raw8 {
     const int h = 4 * it + (lane >> 3);
     if (it < pe_quads && h < A.n_heads)
-      return __ldg(reinterpret_cast<const uint4*>(A.q_pe + t * A.pe_token + h * A.pe_head) + s8);
-    return make_uint4(0, 0, 0, 0);
+      return load_raw8(A.q_pe + t * A.pe_token + h * A.pe_head, j);
+    return Raw8{};
   };
 #pragma unroll
   for (int i = 0; i < kPe; ++i) pv[i] = ask_pe(warp + kQWarps * i);
-  float c[8], sn[8], norm[8];
+  float c[4], sn[4], norm[8];
   if (A.rope.cos_sin) {
     if (pos < 0 || pos >= A.rope.n_positions) {
       if (threadIdx.x == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
@@ -584,8 +577,15 @@ __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArg
   // ---- indexer heads ----
   const bool turn = cs != nullptr && A.rope.idx_rope;
   if (idx_pairs > 0) {
-    if (turn) load_angles(cs, sub, A.rope.idx_interleaved, c, sn);
-    if (A.idx_norm) load8(A.idx_norm + 8 * sub, norm);
+    if (turn) load_angles(cs, j, A.rope.idx_interleaved, c, sn);
+    if (A.idx_norm) load8(A.idx_norm + 64 * g, j, norm);
+    if (g == 1) {  // dims 64-127 do not rotate
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = 1.f;
+        sn[i] = 0.f;
+      }
+    }
   }
   for (int it0 = warp; it0 < idx_pairs; it0 += kQWarps * kIt) {
 #pragma unroll
@@ -606,8 +606,8 @@ __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArg
       float scale, inv;
       quant_scale(half_max8(x), kRE4M3, scale, inv);
       if (h < A.n_idx_heads) {
-        reinterpret_cast<uint2*>(codes + h * 128)[sub] = codes8(x, inv);
-        if (sub == 0) A.w_out[t * A.n_idx_heads + h] = wv[i] * A.w_scale * scale;
+        store_codes8(codes + h * 128 + 64 * g, j, x, inv);
+        if ((lane & 15) == 0) A.w_out[t * A.n_idx_heads + h] = wv[i] * A.w_scale * scale;
       }
     }
     if (it0 + kQWarps * kIt < idx_pairs) {
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArg
     }
   }
   // ---- q_pe ----
-  if (pe_quads > 0 && cs != nullptr) load_angles(cs, s8, A.rope.interleaved, c, sn);
+  if (pe_quads > 0 && cs != nullptr) load_angles(cs, j, A.rope.interleaved, c, sn);
   for (int it0 = warp; it0 < pe_quads; it0 += kQWarps * kPe) {
 #pragma unroll
     for (int i = 0; i < kPe; ++i) {
@@ -626,8 +626,7 @@ __global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArg
       unpack8(pv[i], x);
       if (cs != nullptr) rotate8(x, c, sn, A.rope.interleaved);
       if (h < A.n_heads)
-        reinterpret_cast<uint4*>(A.q_pe_out + (t * A.n_heads + h) * 64)[s8] =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        store_bf16x8(A.q_pe_out + (t * A.n_heads + h) * 64, j, x);
     }
     if (it0 + kQWarps * kPe < pe_quads) {
 #pragma unroll
