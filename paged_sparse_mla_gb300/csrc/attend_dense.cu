@@ -216,7 +216,7 @@ struct __align__(1024) PairSmem {
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
   uint64_t k_full[2][2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive (K: by halves)
-  uint64_t s_full[2], kv_free[2];                            // completed by the MMAs in both CTAs
+  uint64_t s_full[2], kv_free[2][2];  // completed by the MMAs in both CTAs (tile buffer: chunks 0-3, then all)
   uint64_t final_bar;
   int64_t x0, total, seq_at;           // start of the pair's range of work; all work, over `pairs` pairs; (plan)
   int pairs, b, g, rel, len, q0, n_q, seq_len;  // the range's first unit, its position (see Walk) and sequence
@@ -673,7 +673,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       mbar_init(&sm.k_full[i][0], 2 * kKWarps);
       mbar_init(&sm.k_full[i][1], 2 * kKWarps);
       mbar_init(&sm.v_full[i], 2 * kVWarps);
-      mbar_init(&sm.kv_free[i], 1);
+      mbar_init(&sm.kv_free[i][0], 1);
+      mbar_init(&sm.kv_free[i][1], 1);
       mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
       mbar_init(&sm.s_full[i], 1);
     }
@@ -739,8 +740,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
             mma2_f16<x * 32, 2 * j * kChunk + x * 2048>(tmem_o + j * 128, p, dk_hi, dv_lo + (buf * kTileBytes + 4 * h * kChunk) / 16,
                                                          dv_hi, idesc2, !(first && (h | x) == 0), elected);
           });
+          commit2(&sm.kv_free[buf][h], elected);
         }
-        commit2(&sm.kv_free[buf], elected);
         ++k2;
       };
       Walk w;
@@ -927,13 +928,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const bool slow = __any_sync(0xffffffffu, small_scale(sc));
       const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
       on = tw.on();
-      if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1][0], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
       uint8_t* tile = sm.kv[kk & 1][0];
       if (slow) store(std::true_type{}, std::integral_constant<int, 0>{}, mine, tile);
       else store(std::false_type{}, std::integral_constant<int, 0>{}, mine, tile);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full + 16 * (kk & 1));
+      if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1][1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
       if (slow) store(std::true_type{}, std::integral_constant<int, 1>{}, mine, tile);
       else store(std::false_type{}, std::integral_constant<int, 1>{}, mine, tile);
 #pragma unroll
@@ -1073,7 +1075,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           m = mn;
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O holds the tiles before this one once their last MMA is done; this tile's waits for p_full
-            ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+            ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -1101,7 +1103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         }
         l += ls.x + ls.y;
         // keys 0-63 go to this tile's rope chunk; p1 is free once the last tile's MMAs have read it
-        if (kh == 1 && kk > 0) ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+        if (kh == 1 && kk > 0) ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
         uint8_t* p = kh == 0 ? sm.kv[buf][8] : sm.p1;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
@@ -1117,7 +1119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       nx.next(A);
       if (nx.on()) load_q(nx, (n + 1) & 1);
       // ---- end of unit ----
-      ok = pair_wait(&sm.kv_free[(kk - 1) & 1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+      ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
       __syncwarp();
       tc_fence_after();
       sm.red[2 * wg + kh][row] = l;

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
 // all heads.  Bound by memory: 8,192 tokens of 64 + 64 heads, 342 MB, QUERY_FIGURE (the kernel above, a
 // warp per row with rotations through shared memory and byte stores: 254 us).
 constexpr int kQWarps = 8;
-__global__ void __launch_bounds__(32 * kQWarps) query_full_kernel(const QueryArgs A) {
+__global__ void __launch_bounds__(32 * kQWarps, 4) query_full_kernel(const QueryArgs A) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = blockIdx.x;
   const int hi = lane >> 4, j = lane & 7, g = (lane >> 3) & 1;
