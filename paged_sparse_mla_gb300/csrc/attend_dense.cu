@@ -215,7 +215,7 @@ struct __align__(1024) PairSmem {
   uint8_t p1[kCtaRows * 128];              // P for keys 64-127 of a tile (keys 0-63: the tile's rope chunk): [64 rows][64 keys]
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
-  uint64_t k_full[2][2], v_full[2], p_full, q_full, s_free[2];  // used in the first CTA; both CTAs arrive (K: by halves)
+  uint64_t k_full[2][2], v_full[2], p_full[2], q_full, s_free[2];  // used in the first CTA; both CTAs arrive (K: by halves)
   uint64_t s_full[2], kv_free[2][2];  // completed by the MMAs in both CTAs (tile buffer: chunks 0-3, then all)
   uint64_t final_bar;
   int64_t x0, total, seq_at;           // start of the pair's range of work; all work, over `pairs` pairs; (plan)
@@ -666,13 +666,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   unsigned* err = A.D.err;
   if (threadIdx.x == 0) {
-    mbar_init(&sm.p_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.q_full, 2 * kSoftmaxWarps);
     mbar_init(&sm.final_bar, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_full[i][0], 2 * kKWarps);
       mbar_init(&sm.k_full[i][1], 2 * kKWarps);
       mbar_init(&sm.v_full[i], 2 * kVWarps);
+      mbar_init(&sm.p_full[i], 2 * kSoftmaxWarps);
       mbar_init(&sm.kv_free[i][0], 1);
       mbar_init(&sm.kv_free[i][1], 1);
       mbar_init(&sm.s_free[i], 2 * kSoftmaxWarps);
@@ -754,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         uint64_t t0 = 0;
         int half = 0;  // of tile k1's scores
         for (uint32_t idle = 0; ok && k2 < end;) {
-          if (k2 < k1 && ready(&sm.p_full, k2 & 1) && ready(&sm.v_full[k2 & 1], (k2 >> 1) & 1)) {
+          if (k2 < k1 && ready(&sm.p_full[k2 & 1], (k2 >> 1) & 1) && ready(&sm.v_full[k2 & 1], (k2 >> 1) & 1)) {
             mma2(k2 == begin);
             idle = 0;
           } else if (k1 < end && ready(&sm.k_full[k1 & 1][half], (k1 >> 1) & 1) &&
@@ -967,7 +967,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     const int sp = warp & 3, wg = warp >> 2;
     const int L = 32 * sp + lane, row = L & 63, kh = L >> 6;
     const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
-    const uint32_t p_full = map_cta(smem_u32(&sm.p_full), 0), q_full = map_cta(smem_u32(&sm.q_full), 0);
+    // (p_full by the tile's parity: one CTA's warps may be a tile ahead of the other's)
+    const uint32_t p_full[2] = {map_cta(smem_u32(&sm.p_full[0]), 0), map_cta(smem_u32(&sm.p_full[1]), 0)}, q_full = map_cta(smem_u32(&sm.q_full), 0);
     const uint32_t s_free[2] = {map_cta(smem_u32(&sm.s_free[0]), 0), map_cta(smem_u32(&sm.s_free[1]), 0)};
     const int H = A.D.n_heads;
     // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is
@@ -1111,7 +1112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(p_full);
+        if (lane == 0) arrive_cluster(p_full[buf]);
       }
       if (failed) break;
       // the next unit's queries while the last MMAs run (the last scores are read: Q is free)

@@ -165,6 +165,22 @@ def test_many_sequences_of_uneven_length():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_repeated_calls_give_the_same_bits():
+    """Units of uneven rows and lengths, so that the two CTAs of a pair run apart: every hand-off between
+    them has to hold whichever is ahead."""
+    rng = np.random.default_rng(2)
+    lens = [int(x) for x in rng.integers(1, 700, 90)]
+    counts = [int(min(n, k)) for n, k in zip(lens, rng.integers(1, 6, 90))]
+    for heads in (64, 16):
+        c = Case(lens, counts, heads, seed=22)
+        want = c.run()
+        c.check(want)
+        for _ in range(40):
+            got = c.run()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ok()
+
+
 def test_long_contexts_split_over_the_sms():
     c = Case([9001, 20000], [2, 1], 64, seed=6)
     split, whole = c.run(True), c.run(False)
