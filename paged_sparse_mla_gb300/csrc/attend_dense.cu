@@ -196,7 +196,7 @@ constexpr int kSoftmaxWarps = 8, kKWarps = 8, kVWarps = 8;
 constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kCtaKeys / kVWarps;  // of a warp, in a tile
 constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
 constexpr int kThreads = 32 * (kIssuer + 4);  // the issuer's warpgroup: one warp issues, three only lend registers
-constexpr int kLaunchRegs = 72, kSoftmaxRegs = 96, kKRegs = 72, kVRegs = 48, kIssuerRegs = 56;
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kKRegs = 72, kVRegs = 48, kIssuerRegs = 56;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * kVRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
@@ -307,6 +307,12 @@ struct Walk {
   __device__ __forceinline__ bool on() const { return rel < len; }
   __device__ __forceinline__ int tok0(const PairArgs& A) const { return q0 + g * A.group; }
   __device__ __forceinline__ int ntok(const PairArgs& A) const { return min(A.group, n_q - g * A.group); }
+  // Rows of this CTA: the first half of the unit's rows, or the others.
+  __device__ __forceinline__ int rows_before(const PairArgs& A, int cta) const { return cta * ((ntok(A) * A.D.n_heads + 1) / 2); }
+  __device__ __forceinline__ int rows(const PairArgs& A, int cta) const {
+    const int all = ntok(A) * A.D.n_heads, first = (all + 1) / 2;
+    return cta == 0 ? first : all - first;
+  }
   __device__ __forceinline__ int tiles() const { return max(1, (nvis + kKeys - 1) / kKeys); }
   // the pair's tiles [ta, tb) of the unit
   __device__ __forceinline__ int ta(const PairArgs& A) const { return A.part_out != nullptr ? max(-rel, 0) : 0; }
@@ -977,8 +983,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     // (Short code matters here as much as loads in flight: it runs once a unit, from a cold instruction
     // cache.)
     const auto load_q = [&](const Walk& w, int slot) {
-      const int rows = w.ntok(A) * H - kCtaRows * static_cast<int>(cta);
-      const int64_t first = static_cast<int64_t>(w.tok0(A)) * H + kCtaRows * cta;
+      const int rows = w.rows(A, cta);
+      const int64_t first = static_cast<int64_t>(w.tok0(A)) * H + w.rows_before(A, cta);
       uint32_t v[4][9];
       const auto ask = [&](int i, int r) {
 #pragma unroll
@@ -1025,9 +1031,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     uint32_t kk = 0, n = 0;
     bool failed = false;
     while (w.on() && !failed) {
-      const int grow = kCtaRows * static_cast<int>(cta) + row;  // row of the unit
-      const int real_rows = w.ntok(A) * H;
-      const bool real = grow < real_rows;
+      const int rows = w.rows(A, cta), grow = w.rows_before(A, cta) + row;  // grow: row of the unit
+      const bool real = row < rows;
+      const bool idle = 32 * (sp & 1) >= rows;  // no row of this warp is one: it only keeps the others company
       const int vis = real ? static_cast<int>(visible(A.D, w.seq_len, w.g * A.group + grow / H, w.n_q)) : 0;
       const int ta = w.ta(A), tb = w.tb(A);
       // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
@@ -1048,7 +1054,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         // visible keys among this thread's 32
         const int vr = vis - (tile * kKeys + 64 * kh + 32 * wg);
         float mx = -INFINITY;
-        if (__all_sync(0xffffffffu, vr >= 32)) {
+        if (idle) {
+        } else if (__all_sync(0xffffffffu, vr >= 32)) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
         } else {
@@ -1091,6 +1098,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
             tmem_st_wait();
           }
           named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read
+        }
+        if (idle) {  // the rows' P is whatever it was; their part of O is not read
+          if (kh == 1 && kk > 0) ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+          __syncwarp();
+          if (lane == 0) arrive_cluster(p_full[buf]);
+          continue;
         }
         const float mu = m == -INFINITY ? 0.f : m;
         uint32_t pw[16];
@@ -1141,7 +1154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       // consecutive bytes (a lane that stores its own row's dims touches 32 rows in every store).
       const int i4 = lane & 3;
 #pragma unroll 1
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < 8 && !idle; ++x) {
         uint32_t o[16];
         __syncwarp();
         tmem_ld16(tmem_o + lane_base + 128 * wg + 16 * x, o);
@@ -1168,7 +1181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int gr = grow - i4 + j;
-          if (gr < real_rows) {
+          if (row - i4 + j < rows) {
             if (partial)
               *reinterpret_cast<uint4*>(A.part_out + (slot * kRows + gr) * kDL + d) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             else
