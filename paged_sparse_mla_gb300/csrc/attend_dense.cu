@@ -239,7 +239,7 @@ struct PairArgs {
   int group;        // query tokens of a unit: as many as fit 128 rows
   float abs_scale;  // |softmax_scale| log2(e)
   float sign;       // of softmax_scale, applied to the queries
-  bool q_vec;       // q is 16-byte and q_pe 4-byte aligned
+  bool q_vec;       // q and q_pe are 16-byte aligned
   float *part_out, *part_lse;  // partial results, slots [2 pairs][128 rows]; nullptr: units are not split
   PairMeta* meta;   // [pairs]
   const uint8_t* records;               // the layer's records in block 0
@@ -799,6 +799,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           __nanosleep(100);
         }
         __syncwarp();
+        if (kk > 0 && tw.tile == tw.w.ta(A) && A.q_vec) {
+          // a unit's first tile: its queries as well (unasked, they cost the softmax warps 4 % of a batch of short units)
+          const int rows = tw.w.rows(A, cta);
+          const int64_t first = static_cast<int64_t>(tw.w.tok0(A)) * A.D.n_heads + tw.w.rows_before(A, cta);
+          for (int r = lane; r < rows; r += 32) {
+            prefetch_l2_bulk(A.D.q + (first + r) * kDL, 2 * kDL);
+            prefetch_l2_bulk(A.D.q_pe + (first + r) * kDR, 2 * kDR);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int j = tw.tile * kKeys + kCtaKeys * static_cast<int>(cta) + 32 * i + lane;
@@ -1149,45 +1158,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (partial) A.part_lse[slot * kRows + grow] = lse;
         else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
       }
-      // A lane holds 128 dims of its row.  Sixteen at a time, the lanes of a group of four exchange them so
-      // that lane i of the group stores four dims of each of the group's rows and the group 64 (bf16: 32)
-      // consecutive bytes (a lane that stores its own row's dims touches 32 rows in every store).
+      // A lane holds 128 dims of its row and reads them 32 at a time (16: 4 % slower where units are short).
+      // The lanes of a group of four exchange sixteen dims so that lane i of the group stores four of
+      // each of the group's rows and the group 64 (bf16: 32) consecutive bytes (a lane that stores its
+      // own row's dims touches 32 rows in every store).
       const int i4 = lane & 3;
 #pragma unroll 1
-      for (int x = 0; x < 8 && !idle; ++x) {
-        uint32_t o[16];
+      for (int x2 = 0; x2 < 4 && !idle; ++x2) {
+        uint32_t both[32];
         __syncwarp();
-        tmem_ld16(tmem_o + lane_base + 128 * wg + 16 * x, o);
-        tmem_ld_wait(o);
+        tmem_ld32(tmem_o + lane_base + 128 * wg + 32 * x2, both);
+        tmem_ld_wait(both);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-        // o[4 j + i]: dims 4 j + i of the own row -> dims 4 i4 + i of row j of the group
+        for (int y = 0; y < 2; ++y) {
+          const int x = 2 * x2 + y;
+          uint32_t o[16];
 #pragma unroll
-        for (int st = 1; st <= 2; st <<= 1) {
+          for (int i = 0; i < 16; ++i) o[i] = both[16 * y + i];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if ((j & st) == 0) {
-              const bool hi = (i4 & st) != 0;
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          // o[4 j + i]: dims 4 j + i of the own row -> dims 4 i4 + i of row j of the group
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
-                if (hi) o[4 * j + i] = got;
-                else o[4 * (j | st) + i] = got;
+          for (int st = 1; st <= 2; st <<= 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((j & st) == 0) {
+                const bool hi = (i4 & st) != 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
+                  if (hi) o[4 * j + i] = got;
+                  else o[4 * (j | st) + i] = got;
+                }
               }
             }
           }
-        }
-        const int d = d0 + 16 * x + 4 * i4;
+          const int d = d0 + 16 * x + 4 * i4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int gr = grow - i4 + j;
-          if (row - i4 + j < rows) {
-            if (partial)
-              *reinterpret_cast<uint4*>(A.part_out + (slot * kRows + gr) * kDL + d) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            else
-              *reinterpret_cast<uint2*>(A.D.out + (orow - i4 + j) * kDL + d) =
-                  make_uint2(pack_bf16x2(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1])),
-                             pack_bf16x2(__uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3])));
+          for (int j = 0; j < 4; ++j) {
+            const int gr = grow - i4 + j;
+            if (row - i4 + j < rows) {
+              if (partial)
+                *reinterpret_cast<uint4*>(A.part_out + (slot * kRows + gr) * kDL + d) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              else
+                *reinterpret_cast<uint2*>(A.D.out + (orow - i4 + j) * kDL + d) =
+                    make_uint2(pack_bf16x2(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1])),
+                               pack_bf16x2(__uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3])));
+            }
           }
         }
       }
@@ -1364,7 +1381,7 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.group = kRows / D.n_heads;
   A.abs_scale = fabsf(softmax_scale) * kLog2e;
   A.sign = softmax_scale < 0.f ? -1.f : 1.f;
-  A.q_vec = (reinterpret_cast<uintptr_t>(D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(D.q_pe) & 3) == 0;
+  A.q_vec = (reinterpret_cast<uintptr_t>(D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(D.q_pe) & 15) == 0;
   A.records = D.pool + static_cast<int64_t>(D.layer) * D.L.layer_stride + D.L.rec_off;
   uint32_t log2 = 0;
   while ((1ull << log2) < static_cast<uint64_t>(D.L.block_size)) ++log2;
