@@ -131,7 +131,8 @@ struct AppendArgs {
   unsigned* err;
 };
 
-// One warp per token: lane l owns latent elements [E l, E l + E) and key elements [EK l, EK l + EK).
+// Any shape and alignment: one warp per token, lane l owns latent elements [E l, E l + E) and key elements
+// [EK l, EK l + EK).
 template <int E, int EK>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A) {
   __shared__ float stage[kWarps][32 * EK];
@@ -280,7 +281,8 @@ struct QueryArgs {
   unsigned* err;
 };
 
-// One warp per row: rows [0, n_idx_heads) of a token are its indexer heads, the next n_heads its q_pe.
+// Any shape and alignment, one warp per row: rows [0, n_idx_heads) of a token are its indexer heads, the next
+// n_heads its q_pe.
 template <int EK>
 __global__ void __launch_bounds__(32 * kWarps) query_kernel(const QueryArgs A) {
   __shared__ float stage[kWarps][32 * EK];
@@ -417,6 +419,9 @@ __device__ __forceinline__ float half_max8(const float (&x)[8]) {
 // latency.  Warp 0: the latent, 64 dims to eight lanes twice (dims 0-255, then the others), so that a
 // quantisation tile is a half-warp.  Warp 1: the indexer key in its first half-warp and the rope key in eight
 // lanes of the second.
+// 8,192 tokens (20 MB with their records) take 8.0 us, 2.5 TB/s, launch included (the kernel above, a warp per
+// token with byte stores for the key: 15.2), one token 2.5 us (3.7): both are the chain slot -> row -> sums ->
+// codes and a launch, not bandwidth.
 constexpr int kAppendTokens = 4;  // of a CTA
 template <bool kFp4>
 __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const AppendArgs A) {
@@ -525,112 +530,202 @@ __global__ void __launch_bounds__(64 * kAppendTokens) append_full_kernel(const A
   if (lane == 0) reinterpret_cast<float*>(base + L.idx_scale_off)[off] = scale;
 }
 
-// smla_query_prep for 128 indexer dims and 64 rope dims, everything 16-byte aligned: one CTA per token.  Sixteen
-// lanes hold an indexer head, eight lanes a q_pe head (the lanes' dims: above), so that a row's sums and
-// maxima are four shuffles, its rotation none, and the angles, loaded once a token, stay in registers for
-// all heads.  Bound by memory: 8,192 tokens of 64 + 64 heads, 342 MB, QUERY_FIGURE (the kernel above, a
-// warp per row with rotations through shared memory and byte stores: 254 us).
-constexpr int kQWarps = 8;
-__global__ void __launch_bounds__(32 * kQWarps, 4) query_full_kernel(const QueryArgs A) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Two floats in a register pair: packed fp32 operations take half the issue slots.
+__device__ __forceinline__ uint64_t pair_of(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return of_pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
+  return of_pair(r);
+}
+
+// The lane's eight values x of 64 dims as pairs (x0, x2), (x1, x3), (x4, x6), (x5, x7): both kinds of
+// rotation pairs then meet in packed operations.
+__device__ __forceinline__ void unpack_pairs(const Raw8& w, float2* x) {
+  x[0] = make_float2(__uint_as_float(w.lo.x << 16), __uint_as_float(w.lo.y << 16));
+  x[1] = make_float2(__uint_as_float(w.lo.x & 0xFFFF0000u), __uint_as_float(w.lo.y & 0xFFFF0000u));
+  x[2] = make_float2(__uint_as_float(w.hi.x << 16), __uint_as_float(w.hi.y << 16));
+  x[3] = make_float2(__uint_as_float(w.hi.x & 0xFFFF0000u), __uint_as_float(w.hi.y & 0xFFFF0000u));
+}
+struct Turn {
+  float2 c[2], s[2], n[2];  // cosines, sines, minus the sines
+};
+__device__ __forceinline__ void load_turn(const float* cs, int j, bool interleaved, Turn& u) {
+  float c[4], s[4];
+  load_angles(cs, j, interleaved, c, s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    u.c[i] = interleaved ? make_float2(c[2 * i], c[2 * i + 1]) : make_float2(c[i], c[i + 2]);
+    u.s[i] = interleaved ? make_float2(s[2 * i], s[2 * i + 1]) : make_float2(s[i], s[i + 2]);
+    u.n[i] = make_float2(-u.s[i].x, -u.s[i].y);
+  }
+}
+__device__ __forceinline__ void turn2(float2& a, float2& b, float2 c, float2 s, float2 n) {
+  const float2 a0 = a;
+  a = fma2(b, n, mul2(a, c));
+  b = fma2(a0, s, mul2(b, c));
+}
+__device__ __forceinline__ void rotate_pairs(float2* x, const Turn& u, bool interleaved) {
+  if (interleaved) {
+    turn2(x[0], x[1], u.c[0], u.s[0], u.n[0]);
+    turn2(x[2], x[3], u.c[1], u.s[1], u.n[1]);
+  } else {
+    turn2(x[0], x[2], u.c[0], u.s[0], u.n[0]);
+    turn2(x[1], x[3], u.c[1], u.s[1], u.n[1]);
+  }
+}
+
+// smla_query_prep for 128 indexer dims and 64 rope dims, everything 16-byte aligned: one CTA per token.  Eight
+// lanes hold a head (the lanes' dims: above; an indexer head's dims 64-127 likewise), so that a row's sum
+// and maximum are three shuffles each, its rotation none, and the angles, loaded once a token, stay in
+// registers for all heads.  A norm's 1 / rms scales the whole row: only the row's scale sees it, its codes
+// are those of the row without it.
+// Bound by memory: 8,192 tokens of 64 + 64 heads move 342 MB in 58.7 us, 5.8 TB/s (a warp per row, with
+// rotations through shared memory and byte stores, the kernel above: 243 us; sixteen lanes a head, unpacked
+// fp32 and every warp at both kinds of heads: 70 us, bound by its instructions).
+// Three warps a token leave the SM eight tokens at a time and most loads in flight; a step of a few tokens
+// is a matter of latency and takes twelve warps, as long as all of its CTAs (two an SM) run at once:
+// 1 token 2.3 us against 3.5 with three warps, 256 tokens 3.1 against 4.1, 512 tokens 5.0 against 4.7,
+// 8,192 tokens 86 against 58.7.
+constexpr int kQWarps = 12;  // of a CTA, at most; a multiple of three
+__global__ void __launch_bounds__(32 * kQWarps, 2) query_full_kernel(const QueryArgs A) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t t = blockIdx.x;
-  const int hi = lane >> 4, j = lane & 7, g = (lane >> 3) & 1;
+  const int sub = lane >> 3, j = lane & 7;  // the lane's head of four, its place in 64 dims
+  const int idx_quads = A.q_idx ? (A.n_idx_heads + 3) / 4 : 0, pe_quads = A.q_pe ? (A.n_heads + 3) / 4 : 0;
+  // a third of the warps takes q_pe (64 dims a head against 128)
+  const int pe_warps = pe_quads == 0 ? 0 : idx_quads == 0 ? warps : warps / 3;
   const float* cs = nullptr;
   int64_t pos = 0;
   if (A.rope.cos_sin) pos = __ldg(A.rope.positions + t);
-  // the first rows are asked for before the position is known to be good
-  constexpr int kIt = 4;
-  Raw8 v[kIt];
+  const auto angles = [&]() -> bool {
+    if (A.rope.cos_sin == nullptr) return true;
+    if (pos < 0 || pos >= A.rope.n_positions) {
+      if (threadIdx.x == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
+      return false;
+    }
+    cs = A.rope.cos_sin + pos * 64;
+    return true;
+  };
+  Turn u;
+  if (warp < pe_warps) {  // ---- q_pe ----
+    constexpr int kIt = 4;
+    Raw8 v[kIt];
+    const auto ask = [&](int i, int it) {
+      const int h = 4 * it + sub;
+      v[i] = Raw8{};
+      if (it < pe_quads && h < A.n_heads) v[i] = load_raw8(A.q_pe + t * A.pe_token + h * A.pe_head, j);
+    };
+    // the first rows are asked for before the position is known to be good
+#pragma unroll
+    for (int i = 0; i < kIt; ++i) ask(i, warp + pe_warps * i);
+    if (!angles()) return;
+    if (cs != nullptr) load_turn(cs, j, A.rope.interleaved, u);
+#pragma unroll 1
+    for (int it0 = warp; it0 < pe_quads; it0 += pe_warps * kIt) {
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const int it = it0 + pe_warps * i, h = 4 * it + sub;
+        if (it >= pe_quads) break;
+        float2 x[4];
+        unpack_pairs(v[i], x);
+        ask(i, it + pe_warps * kIt);
+        if (cs != nullptr) rotate_pairs(x, u, A.rope.interleaved);
+        if (h < A.n_heads) {
+          uint2* dst = reinterpret_cast<uint2*>(A.q_pe_out + (t * A.n_heads + h) * 64) + j;
+          dst[0] = make_uint2(pack_bf16x2(x[0].x, x[1].x), pack_bf16x2(x[0].y, x[1].y));
+          dst[8] = make_uint2(pack_bf16x2(x[2].x, x[3].x), pack_bf16x2(x[2].y, x[3].y));
+        }
+      }
+    }
+    return;
+  }
+  // ---- indexer heads ----
+  const int step = warps - pe_warps;
+  constexpr int kIt = 2;
+  Raw8 v[kIt][2];
   float wv[kIt];
-  uint8_t* codes = A.codes + t * A.n_idx_heads * 128;
-  const int idx_pairs = A.q_idx ? (A.n_idx_heads + 1) / 2 : 0;
   const auto ask = [&](int i, int it) {
-    const int h = 2 * it + hi;
-    v[i] = Raw8{};
+    const int h = 4 * it + sub;
+    v[i][0] = v[i][1] = Raw8{};
     wv[i] = 0.f;
-    if (it < idx_pairs && h < A.n_idx_heads) {
-      v[i] = load_raw8(A.q_idx + t * A.idx_token + h * A.idx_head + 64 * g, j);
+    if (it < idx_quads && h < A.n_idx_heads) {
+      const __nv_bfloat16* src = A.q_idx + t * A.idx_token + h * A.idx_head;
+      v[i][0] = load_raw8(src, j);
+      v[i][1] = load_raw8(src + 64, j);
       wv[i] = __ldg(A.w + t * A.n_idx_heads + h);
     }
   };
 #pragma unroll
-  for (int i = 0; i < kIt; ++i) ask(i, warp + kQWarps * i);
-  const int pe_quads = A.q_pe ? (A.n_heads + 3) / 4 : 0;
-  constexpr int kPe = 2;
-  Raw8 pv[kPe];
-  const auto ask_pe = [&](int it) -> Raw8 {
-    const int h = 4 * it + (lane >> 3);
-    if (it < pe_quads && h < A.n_heads)
-      return load_raw8(A.q_pe + t * A.pe_token + h * A.pe_head, j);
-    return Raw8{};
-  };
-#pragma unroll
-  for (int i = 0; i < kPe; ++i) pv[i] = ask_pe(warp + kQWarps * i);
-  float c[4], sn[4], norm[8];
-  if (A.rope.cos_sin) {
-    if (pos < 0 || pos >= A.rope.n_positions) {
-      if (threadIdx.x == 0) latch_error(A.err, SMLA_ERR_BAD_INDEX);
-      return;
-    }
-    cs = A.rope.cos_sin + pos * 64;
-  }
-  // ---- indexer heads ----
+  for (int i = 0; i < kIt; ++i) ask(i, warp - pe_warps + step * i);
+  if (!angles()) return;
   const bool turn = cs != nullptr && A.rope.idx_rope;
-  if (idx_pairs > 0) {
-    if (turn) load_angles(cs, j, A.rope.idx_interleaved, c, sn);
-    if (A.idx_norm) load8(A.idx_norm + 64 * g, j, norm);
-    if (g == 1) {  // dims 64-127 do not rotate
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = 1.f;
-        sn[i] = 0.f;
-      }
-    }
-  }
-  for (int it0 = warp; it0 < idx_pairs; it0 += kQWarps * kIt) {
+  if (turn) load_turn(cs, j, A.rope.idx_interleaved, u);
+#pragma unroll 1
+  for (int it0 = warp - pe_warps; it0 < idx_quads; it0 += step * kIt) {
 #pragma unroll
     for (int i = 0; i < kIt; ++i) {
-      const int it = it0 + kQWarps * i, h = 2 * it + hi;
-      if (it >= idx_pairs) break;
-      float x[8];
-      unpack8(v[i], x);
+      const int it = it0 + step * i, h = 4 * it + sub;
+      if (it >= idx_quads) break;
+      float2 x[8];
+      unpack_pairs(v[i][0], x);
+      unpack_pairs(v[i][1], x + 4);
+      const float weight = wv[i];
+      ask(i, it + step * kIt);
+      float rstd = 1.f;
       if (A.idx_norm) {
-        float ss = 0.f;
+        float2 ss = mul2(x[0], x[0]), sr = mul2(x[1], x[1]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-        const float rstd = rsqrtf(half_sum(ss) / 128.0f + A.eps);
+        for (int e = 2; e < 8; e += 2) {
+          ss = fma2(x[e], x[e], ss);
+          sr = fma2(x[e + 1], x[e + 1], sr);
+        }
+        float sum = (ss.x + sr.x) + (ss.y + sr.y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * rstd * norm[e];
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        rstd = rsqrtf(sum / 128.0f + A.eps);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {  // read again for every head: sixteen registers less are a CTA more
+          float4 w;
+          asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                       : "l"(A.idx_norm + 16 * e + 4 * j));
+          x[e] = mul2(x[e], make_float2(w.x, w.z));
+          x[e + 1] = mul2(x[e + 1], make_float2(w.y, w.w));
+        }
       }
-      if (turn) rotate8(x, c, sn, A.rope.idx_interleaved);
+      if (turn) rotate_pairs(x, u, A.rope.idx_interleaved);
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float scale, inv;
-      quant_scale(half_max8(x), kRE4M3, scale, inv);
+      quant_scale(amax * rstd, kRE4M3, scale, inv);
+      inv *= rstd;
       if (h < A.n_idx_heads) {
-        store_codes8(codes + h * 128 + 64 * g, j, x, inv);
-        if ((lane & 15) == 0) A.w_out[t * A.n_idx_heads + h] = wv[i] * A.w_scale * scale;
+        const int64_t row = t * A.n_idx_heads + h;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(A.codes + row * 128) + j;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], make_float2(inv, inv));
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)  // x0 .. x3 and x4 .. x7 of either half
+          dst[8 * (e >> 1)] = e4m3x2(x[e].x, x[e + 1].x) | e4m3x2(x[e].y, x[e + 1].y) << 16;
+        if (j == 0) A.w_out[row] = weight * A.w_scale * scale;
       }
-    }
-    if (it0 + kQWarps * kIt < idx_pairs) {
-#pragma unroll
-      for (int i = 0; i < kIt; ++i) ask(i, it0 + kQWarps * (kIt + i));
-    }
-  }
-  // ---- q_pe ----
-  if (pe_quads > 0 && cs != nullptr) load_angles(cs, j, A.rope.interleaved, c, sn);
-  for (int it0 = warp; it0 < pe_quads; it0 += kQWarps * kPe) {
-#pragma unroll
-    for (int i = 0; i < kPe; ++i) {
-      const int it = it0 + kQWarps * i, h = 4 * it + (lane >> 3);
-      if (it >= pe_quads) break;
-      float x[8];
-      unpack8(pv[i], x);
-      if (cs != nullptr) rotate8(x, c, sn, A.rope.interleaved);
-      if (h < A.n_heads)
-        store_bf16x8(A.q_pe_out + (t * A.n_heads + h) * 64, j, x);
-    }
-    if (it0 + kQWarps * kPe < pe_quads) {
-#pragma unroll
-      for (int i = 0; i < kPe; ++i) pv[i] = ask_pe(it0 + kQWarps * (kPe + i));
     }
   }
 }
@@ -715,7 +810,8 @@ extern "C" smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, 
   A.vec_latent = aligned(latent, 16) && latent_stride % 8 == 0;
   A.vec_idx = aligned(idx_k, 16) && idx_k_stride % 8 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // The full shape with rows that load as 16-byte pieces takes the kernel built for it.
+  // The full shape with rows that load as 16-byte pieces takes the kernel built for it (half the time at 8,192
+  // tokens, two thirds at one: see there).
   if (L.d_latent == 512 && L.quant_tile == 128 && L.d_rope == 64 && L.d_index == 128 && A.vec_latent &&
       aligned(rope_key, 16) && rope_stride % 8 == 0 && (!idx || A.vec_idx) && aligned(latent_norm, 16) &&
       aligned(idx_norm, 16) && aligned(idx_bias, 16) && aligned(A.rope.cos_sin, 16)) {
@@ -775,12 +871,12 @@ extern "C" smla_status_t smla_query_prep(const smla_layout_t* layout, const smla
   A.rope = rope_args(rope, positions, layout->d_rope);
   A.vec_idx = aligned(q_idx, 16) && q_idx_token_stride % 8 == 0 && q_idx_head_stride % 8 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Rows that load as 16-byte pieces take the kernel built for them.
+  // Rows that load as 16-byte pieces take the kernel built for them (a quarter of the time at 8,192 tokens: see there).
   if ((!idx || (layout->d_index == 128 && A.vec_idx && aligned(q_idx_out, 8) && aligned(idx_norm, 16))) &&
       (layout->d_rope == 64 || (!pe && !(A.rope.cos_sin && A.rope.idx_rope))) &&
       (!pe || (aligned(q_pe, 16) && q_pe_token_stride % 8 == 0 && q_pe_head_stride % 8 == 0 && aligned(q_pe_out, 16))) &&
       aligned(A.rope.cos_sin, 16)) {
-    query_full_kernel<<<n_tokens, 32 * kQWarps, 0, s>>>(A);
+    query_full_kernel<<<n_tokens, 32 * (n_tokens <= 2 * device_sm_count() ? kQWarps : 3), 0, s>>>(A);
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
   }
   const int64_t rows = static_cast<int64_t>(n_tokens) * ((pe ? A.n_heads : 0) + (idx ? A.n_idx_heads : 0));
