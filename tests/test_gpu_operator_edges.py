@@ -157,6 +157,31 @@ def test_broadcast_inputs():
     ok()
 
 
+@pytest.mark.parametrize("heads,idx_heads,norm,interleaved", [(64, 64, True, False), (5, 7, True, True), (130, 0, False, True),
+                                                              (0, 33, False, False), (1, 1, True, True)])
+def test_many_queries_equal_a_few_at_a_time(heads, idx_heads, norm, interleaved):
+    """A chunk's queries (three warps a token) have the bits of the same queries in small calls (twelve)."""
+    g = torch.Generator(device="cuda").manual_seed(42)
+    lay, prm = smla.layout_init(16, 1, 512, 64, 128, 128, 4), smla.make_params(max(heads, 1), max(idx_heads, 1), 16, 1.0)
+    rope = smla.make_rope(torch.from_numpy(table(5000, 64)).cuda(), interleaved=interleaved, idx_interleaved=not interleaved)
+    n = 1201
+    pos = torch.randint(0, 5000, (n,), generator=g, device="cuda")
+    pe, ix = torch.randn(n, heads, 64, generator=g, device="cuda").bfloat16(), torch.randn(n, idx_heads, 128, generator=g, device="cuda").bfloat16()
+    w, kn = torch.randn(n, idx_heads, generator=g, device="cuda"), torch.rand(128, generator=g, device="cuda") if norm else None
+    got = []
+    for step in (n, 100):
+        po = torch.full((n, heads, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        co, wo = torch.full((n, idx_heads, 128), 9, dtype=torch.uint8, device="cuda"), torch.full((n, idx_heads), 5.0, device="cuda")
+        for a in range(0, n, step):
+            b = slice(a, min(n, a + step))
+            smla.smla_query_prep(lay, prm, rope, pos[b], q_pe=pe[b] if heads else None, q_pe_out=po[b] if heads else None,
+                                 q_idx=ix[b] if idx_heads else None, w=w[b], q_idx_out=co[b], w_out=wo[b], idx_norm=kn)
+        got.append((po, co, wo))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    ok()
+
+
 def test_calls_without_tokens():
     lay, prm = smla.layout_init(64, 1, 512, 64, 128, 128, 2), smla.make_params(8, 4, 16, 1.0)
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
