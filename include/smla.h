@@ -439,8 +439,8 @@ typedef struct smla_rope {
  *   positions    int64 [n_tokens]
  *   slot_mapping int64 [n_tokens], as kvpack_store: -1 = skip, a slot beyond the pool is
  *                skipped and latched; a token whose position is outside the table is too
- * Two tokens of one call must not share a slot.  Inputs must be finite.  The
- * pool is 16-byte aligned, the inputs aligned to their element.  Built for the
+ * Two tokens of one call must not share a slot.  Inputs must be finite, a normed row's
+ * squares and their sum too.  The pool is 16-byte aligned, the inputs aligned to their element.  Built for the
  * latents that kvpack_store takes (64, 128, 256 or 512), d_rope <= 64 and d_index
  * of 32, 64, 128 or 256.
  */
@@ -498,16 +498,19 @@ smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* 
  *   workspace  optional (NULL and 0): with smla_attend_dense_workspace_size() bytes,
  *              16-byte aligned, long contexts are split evenly over the SMs and the parts
  *              merged by their lse, without it each group of query tokens stays on one pair
- *              of SMs.  Its contents need not be kept; calls that may overlap need one each.
+ *              of SMs (as with fewer bytes).  Its contents need not be kept; calls that may
+ *              overlap need one each, captured ones among them.
  * seq_lens, query_start_loc and block_table are read on the device: block ids outside the
  * pool read as zeros and positions past the block-table row are not visited (both latch
  * SMLA_ERR_BAD_INDEX).  query_start_loc is trusted to increase from 0 to at most n_tokens.
- * Memory past a sequence's length is never used, whatever it holds.
+ * Memory past a sequence's length is never used, whatever it holds; cached values within it must be
+ * finite: on the tensor cores a NaN at a position that only some query tokens see reaches the others too.
  * Latents of 512 dims in tiles of 128 with 64 rope dims run on the tensor cores with
- * fp16 operands (fp32 accumulation): a latent scale above 65504 / 448 or a rope value
- * beyond fp16's range latches SMLA_ERR_RANGE, and the outputs that read it are not
- * valid; cached values below 2^-14 are held to 2^-25 absolutely.  Other shapes kvpack_store takes (d_rope <= 64) run in fp32 on the CUDA cores.
- * The pool is 16-byte aligned.
+ * fp16 operands (fp32 accumulation): a latent scale above 65504 / 448, a rope value
+ * beyond fp16's range or such a NaN latches SMLA_ERR_RANGE, and the outputs of its
+ * sequence are not valid; cached values below 2^-14 are held to 2^-25 absolutely.  Other shapes kvpack_store
+ * takes (d_rope <= 64) run in fp32 on the CUDA cores.
+ * The pool is 16-byte aligned.  The same call gives the same bits every time.
  */
 smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t* params, const void* pool, int layer,
                                 const void* q, const void* q_pe, const int32_t* block_table, int bt_stride,

@@ -3,6 +3,11 @@
 // [AgentX "Kimi K3"], [GLM-5.3 "What is new"]: MLA keeps one latent KV shared by all query heads, so
 // attention is MQA over the latent; V is the latent.  [GLM-5.3 "How to try"]: a prompt that fits the
 // top-k attends over all of its positions; here that holds at any length.
+//
+//   s_j = softmax_scale (q . K_j + q_pe . kpe_j),  m = max_j s_j,  l = sum_j e^(s_j - m)
+//   out = sum_j e^(s_j - m) K_j / l,  lse = m + ln l            over the positions j that the token sees
+// in one pass over the keys: m and l are running values, and what is summed so far is multiplied by
+// e^(m_old - m_new) when m moves.  Exponentials are powers of two (the scale carries log2 e).
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -41,7 +46,9 @@ __device__ __forceinline__ int64_t visible(const DenseArgs& A, int len, int i, i
 // ---------------------------------------------------------------------------
 // Shapes without a tensor-core kernel: fp32 throughout.  One CTA per (query token, 8 heads); keys in
 // tiles of 32, dequantised into shared memory; warp h scores head h (a lane per key), then every
-// thread accumulates its dims for the 8 heads.
+// thread accumulates its dims for the 8 heads.  Bound by shared-memory reads, one per multiply-add: on the
+// full shape, which has its own kernel, it took 33.6 ms where that takes 0.20 (32 tokens, 64 heads,
+// 8,192 to 32,768 positions each).
 // ---------------------------------------------------------------------------
 constexpr int kSHeads = 8, kSKeys = 32, kSThreads = 256;
 
@@ -188,6 +195,27 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // dims; in the second, chunks 4-7 are keys 64-127 of dims 256-511 and chunks 0-3 are refilled with
 // keys 0-63 of those.  The rope chunk, free then too, takes the first half of P.  That leaves shared
 // memory for two tile buffers beside the queries.
+//
+// Operands are fp16, not bf16: an E4M3 code is exact in it, so that a key carries the rounding of its scale
+// and of the product (2^-11 each; bf16 2^-8), P that of 2^-11.  What fp16 lacks in range is met by a
+// power of two per query row and checked for keys (SMLA_ERR_RANGE).  Sums, maxima and O are fp32.
+//
+// Warps: eight take the softmax of the CTA's rows, its queries and results; eight turn the CTA's keys into K,
+// eight the other CTA's into V; one lane of one warp issues all MMAs of the pair, another warp asks for
+// keys and queries to come into L2, a third looks for NaN where it would spread.  The grid is one pair per two SMs.  All work, counted in key tiles, is
+// cut into as many equal ranges: a pair walks over the units (sequence, group of query tokens) of its
+// range, and a unit that crosses ranges leaves partial results, which dense_merge_kernel joins by their lse.
+//
+// Bound by the shared-memory and L1 data path.  A tile moves, per SM, 240 KB of MMA operands, 120 KB of
+// stores of converted keys and 59 KB of record loads through it (2.0 us with records from L2), against
+// 1.2 us of MMA at full rate.  With loads that always hit L1 (a wrong answer) the cases below took 11 to
+// 20 % less, the largest share of any one part.  More rows per pair would read each operand
+// for more rows, but O fills half of tensor memory and the scores a quarter.  Measured, 64 heads:
+//   2,048 query tokens at 20,480 positions   4.13 ms, 1.20 PFLOP/s (tensor pipe active half of the time)
+//   32 decode tokens, 8,192 to 32,768        199 us, 2.2 TB/s (half of a pair's rows are empty, and
+//                                            DRAM's latency adds a fifth)
+//   64 x 4 drafted tokens, 4,096 to 32,768   669 us, 0.98 PFLOP/s
+//   one token at one position                18.4 us, the chain plan -> queries -> tile -> results -> merge
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128, kKeys = 128;      // of a pair
 constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
@@ -195,24 +223,27 @@ constexpr int kDL = 512, kDR = 64, kChunks = 9;  // 64-dim chunks: 8 latent, 1 r
 constexpr int kSoftmaxWarps = 8, kKWarps = 8, kVWarps = 8;
 constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kCtaKeys / kVWarps;  // of a warp, in a tile
 constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
-constexpr int kThreads = 32 * (kIssuer + 4);  // the issuer's warpgroup: one warp issues, three only lend registers
+constexpr int kThreads = 32 * (kIssuer + 4);  // the last four: issuer, L2 requests, check for NaN, none
 constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kKRegs = 72, kVRegs = 48, kIssuerRegs = 56;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * kVRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
-constexpr float kRescale = 8.0f;       // the running maximum moves when a score passes it by 2^8
+// The running maximum moves when a score passes it by 2^8: few tiles rescale O, and P stays far below fp16's end
+// (2^12 was no faster).
+constexpr float kRescale = 8.0f;
 constexpr float kMaxScale = 65504.0f / 448.0f;
 constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
 constexpr float kSmallScale = 1.220703125e-4f;  // 2^-13: below it a scale loses bits in fp16
 constexpr int kMaxPairs = 128;
 constexpr int kRec = kDL + 16 + 2 * kDR;  // bytes of a record: codes, four scales, rope
-constexpr int kMinTiles = 2;           // key tiles a pair takes at least
-constexpr int kPrefetchAhead = 4;      // tiles requested into L2 ahead of the loads
+constexpr int kMinTiles = 2;  // key tiles a pair takes at least (1 to 4: the same)
+// Tiles requested into L2 ahead of the loads (1 to 16: the same; none: decode steps 2 % slower, a chunk 1 %).
+constexpr int kPrefetchAhead = 4;
 
 struct __align__(1024) PairSmem {
   uint8_t kv[2][kChunks][kCtaKeys * 128];  // tile buffer, chunk: [64 keys][64 dims] fp16, 128-byte swizzle; see above
   uint8_t q[kChunks][kCtaRows * 128];
-  uint8_t p1[kCtaRows * 128];              // P for keys 64-127 of a tile (keys 0-63: the tile's rope chunk): [64 rows][64 keys]
+  uint8_t p1[kCtaRows * 128];              // P [64 rows][64 keys], keys 64-127 of a tile (keys 0-63: its rope chunk)
   float red[4][kCtaRows];
   float row_f[2][kCtaRows];            // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
   uint64_t k_full[2][2], v_full[2], p_full[2], q_full, s_free[2];  // used in the first CTA; both CTAs arrive (K: by halves)
@@ -509,7 +540,8 @@ __device__ __forceinline__ int page_of(const PairArgs& A, int j) {
 // The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
 // of 16, so that they lie one after another in a block and every lane knows them all from the first
 // (`n` of them hold visible positions; what follows in the block is read too and zeroed by the caller).
-// Otherwise lane i looks up the i-th and the lanes pass the addresses around, two shuffles a record.
+// Otherwise lane i looks up the i-th and the lanes pass the addresses around, two shuffles a record: on blocks of
+// 64 that takes 3 % longer in decode steps (205 us against 199) and 5 % in a chunk (4.36 ms against 4.12).
 // find() asks for the block id, take() turns it into the address: a tile later, so that nothing waits for
 // the block table.
 template <bool kRuns, int kN>
@@ -819,6 +851,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           }
         }
       }
+    } else if (warp == kIssuer + 2) {
+      // A NaN (code 0x7F of either sign) at a position that only some of a unit's tokens see reaches the others
+      // too: their zeros times it.  So those few positions are looked at.  (In the K warps, which hold
+      // the codes anyway, the same check cost 5 % of the whole call.)
+      bool bad = false;
+      Walk w;
+      for (w.start(A, sm); w.on(); w.next(A)) {
+        const int end = min(w.nvis, w.tb(A) * kKeys);
+#pragma unroll 1
+        for (int j = max(w.nvis - w.ntok(A) + 1, w.ta(A) * kKeys) + static_cast<int>(cta); j < end; j += 2) {
+          const int pg = page_of(A, j);
+          const int blk = __ldg(A.D.block_table + static_cast<int64_t>(w.b) * A.D.bt_stride + pg);
+          if (blk < 0 || blk >= A.D.L.num_blocks) continue;
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride +
+                                                               (j - pg * A.D.L.block_size) * kRec) + lane);
+          const auto is = [](uint32_t x) { return (x & 0x7F7F7F7Fu) + 0x01010101u; };
+          bad |= ((is(c.x) | is(c.y) | is(c.z) | is(c.w)) & 0x80808080u) != 0;
+        }
+      }
+      if (bad) latch_error(err, SMLA_ERR_RANGE);
     }
   } else if (warp >= kFirstV) {
     // ------------------------------ V: the other CTA's 64 keys x this CTA's 256 latent dims ------------------------------
@@ -1158,7 +1210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (partial) A.part_lse[slot * kRows + grow] = lse;
         else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
       }
-      // A lane holds 128 dims of its row and reads them 32 at a time (16: 4 % slower where units are short).
+      // A lane holds 128 dims of its row and reads them 32 at a time (16: 4 % slower on batches of short units).
       // The lanes of a group of four exchange sixteen dims so that lane i of the group stores four of
       // each of the group's rows and the group 64 (bf16: 32) consecutive bytes (a lane that stores its
       // own row's dims touches 32 rows in every store).
@@ -1229,6 +1281,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 // Joins the parts of units that ran on several pairs: lse = ln sum e^lse_i, out = sum e^(lse_i - lse) out_i
 // in fp32.  A warp takes a row (a lane 16 dims) where a few parts are to be joined; where there are many, as
 // for one long sequence, the block's four warps share it (a lane 4 dims, eight parts' loads in flight).
+// With the whole call's time: one sequence of 262,143 positions 98 us (119 with a warp per row), 64 sequences of
+// four tokens 669 us (680 with a block per row).
 constexpr int kMergeThreads = 128, kFewParts = 4;
 template <int kStep>
 __device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, int row, int quarter0, int quarters,
@@ -1388,6 +1442,9 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.bs_mul = static_cast<uint32_t>((((1ull << log2) - D.L.block_size) << 32) / D.L.block_size + 1);
   A.bs_shift1 = log2 > 0 ? 1 : 0;
   A.bs_shift2 = log2 > 0 ? log2 - 1 : 0;
+  // Splitting pays wherever units are fewer or more uneven than pairs, and costs nothing measurable elsewhere:
+  // 32 decode tokens 199 us (622 without), one long sequence 98 us (4.8 ms), a chunk of 1,024 units 4.12 ms
+  // (4.36).  Without a workspace units stay whole.
   const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
   if (split) {
     uint8_t* w = static_cast<uint8_t*>(workspace);

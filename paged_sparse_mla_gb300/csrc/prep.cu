@@ -7,7 +7,7 @@
 // Norm, position rotation, quantisation and the scatter (or the head weight) are one pass: a row is
 // read once as bf16, kept in fp32 registers (in shared memory only where a rotation pairs elements of
 // different lanes) and leaves as codes.  The normalised values are not rounded to bf16 before they are
-// quantised: that rounding (2^-9) would only add to the code's (2^-4).
+// quantised: that rounding (2^-8) would only add to the code's (2^-4).
 #include <cuda_fp4.h>
 
 #include "smla_internal.h"

@@ -59,6 +59,25 @@ def test_softmax_scales(sigma):
     ok()
 
 
+@pytest.mark.parametrize("value", [0x7F, 0xFF])
+def test_nan_in_the_cache(value):
+    """At a position that every token sees it is theirs; where only the last token sees it, the others' zero
+    weights would carry it too: latched.  Past the sequence it is never read."""
+    for lens, pos, latched in (([300], 100, False), ([300], 299, True), ([256], 255, True), ([300], 300, False)):
+        c = Case(lens, [2], 64, seed=43)
+        rec = c.pool.view(-1, c.lay.block_stride)[int(c.table[0, pos // 64]), :64 * 656].view(64, 656)
+        rec[pos % 64, 7] = value
+        out, _ = c.run()
+        assert smla.smla_get_last_error() == (7 if latched else 0)
+        nan = torch.isnan(out)
+        if pos == 100:
+            assert nan[..., 7].all()
+        elif pos == 300:
+            assert not nan.any()
+        else:
+            assert nan[1, :, 7].all()
+
+
 def test_a_workspace_that_is_too_small_is_not_used():
     c = Case([900], [1], 64, seed=35)
     want, _ = c.run(workspace=False)
