@@ -694,6 +694,25 @@ __device__ __forceinline__ void load_query(const PairArgs& A, int64_t row, int l
   }
 }
 
+// Lane i of a group of four holds four items of four words; afterwards item j is what lane j held as item i.
+__device__ __forceinline__ void transpose4(uint32_t (&o)[16], bool hi1, bool hi2) {
+#pragma unroll
+  for (int st = 1; st <= 2; st <<= 1) {
+    const bool hi = st == 1 ? hi1 : hi2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if ((j & st) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
+          if (hi) o[4 * j + i] = got;
+          else o[4 * (j | st) + i] = got;
+        }
+      }
+    }
+  }
+}
+
 template <bool kRuns>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_pair_kernel(const PairArgs A) {
   extern __shared__ uint8_t smem_raw[];
@@ -1210,54 +1229,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (partial) A.part_lse[slot * kRows + grow] = lse;
         else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
       }
-      // A lane holds 128 dims of its row and reads them 32 at a time (16: 4 % slower on batches of short units).
-      // The lanes of a group of four exchange sixteen dims so that lane i of the group stores four of
-      // each of the group's rows and the group 64 (bf16: 32) consecutive bytes (a lane that stores its
-      // own row's dims touches 32 rows in every store).
+      // A lane holds 128 dims of its row and reads them 32 at a time.  The lanes of a group of four exchange them
+      // (as bf16 pairs; partial results in fp32, in two halves), so that the group stores 64 consecutive
+      // bytes of each of its rows: a lane that stores its own row's dims touches 32 rows in every store, and
+      // exchanges in fp32 throughout made a batch of short units 6 % slower.
       const int i4 = lane & 3;
+      const bool hi1 = (i4 & 1) != 0, hi2 = (i4 & 2) != 0;
+      const uint32_t t_o = tmem_o + lane_base + 128 * wg;
 #pragma unroll 1
-      for (int x2 = 0; x2 < 4 && !idle; ++x2) {
-        uint32_t both[32];
+      for (int x = 0; x < 4 && !idle; ++x) {
+        uint32_t o[32];
         __syncwarp();
-        tmem_ld32(tmem_o + lane_base + 128 * wg + 32 * x2, both);
-        tmem_ld_wait(both);
+        tmem_ld32(t_o + 32 * x, o);
+        tmem_ld_wait(o);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int x = 2 * x2 + y;
-          uint32_t o[16];
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        uint32_t h[16];
+        if (partial) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = both[16 * y + i];
+          for (int y = 0; y < 2; ++y) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-          // o[4 j + i]: dims 4 j + i of the own row -> dims 4 i4 + i of row j of the group
+            for (int i = 0; i < 16; ++i) h[i] = o[16 * y + i];
+            transpose4(h, hi1, hi2);
+            float* to = A.part_out + (slot * kRows + grow - i4) * kDL + d0 + 32 * x + 16 * y + 4 * i4;
 #pragma unroll
-          for (int st = 1; st <= 2; st <<= 1) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((j & st) == 0) {
-                const bool hi = (i4 & st) != 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
-                  if (hi) o[4 * j + i] = got;
-                  else o[4 * (j | st) + i] = got;
-                }
-              }
-            }
+            for (int j = 0; j < 4; ++j)
+              if (row - i4 + j < rows)
+                *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
           }
-          const int d = d0 + 16 * x + 4 * i4;
+        } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int gr = grow - i4 + j;
-            if (row - i4 + j < rows) {
-              if (partial)
-                *reinterpret_cast<uint4*>(A.part_out + (slot * kRows + gr) * kDL + d) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-              else
-                *reinterpret_cast<uint2*>(A.D.out + (orow - i4 + j) * kDL + d) =
-                    make_uint2(pack_bf16x2(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1])),
-                               pack_bf16x2(__uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3])));
-            }
-          }
+          for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          transpose4(h, hi1, hi2);
+          __nv_bfloat16* to = A.D.out + (orow - i4) * kDL + d0 + 32 * x + 8 * i4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row - i4 + j < rows)
+              *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
         }
       }
       tc_fence_before();
