@@ -233,7 +233,11 @@ static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * 
 constexpr float kRescale = 8.0f;
 constexpr float kMaxScale = 65504.0f / 448.0f;
 constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
-constexpr float kSmallScale = 1.220703125e-4f;  // 2^-13: below it a scale loses bits in fp16
+// Below 2^-13 a scale would lose bits in fp16 (from 2^-14 on).  Such a scale is taken times 2^19, which keeps its
+// products (at most 448 x 2^6) in range, and what was stored is multiplied by 2^-19 in a second pass: exact down to
+// fp16's smallest normal value, within half its step (2^-25) below.  A second pass over the few tiles that need
+// it and not a second form of the loop: the loop's code shares the instruction cache with the other warps'.
+constexpr float kSmallScale = 1.220703125e-4f, kSmallUp = 524288.f;
 constexpr int kMaxPairs = 128;
 constexpr int kRec = kDL + 16 + 2 * kDR;  // bytes of a record: codes, four scales, rope
 constexpr int kMinTiles = 2;  // key tiles a pair takes at least (1 to 4: the same)
@@ -505,26 +509,28 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Eight E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale rounds to 11 bits and
-// the product once more (2 x 2^-11 in all).  kSlow: the scale may be so small that fp16 would hold it with
-// fewer bits, so the products are formed in fp32.  `sc`: the scale, as two halves or in fp32.
-template <bool kSlow>
+// Eight E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale (two halves) rounds to 11
+// bits and the product once more (2 x 2^-11 in all).
 __device__ __forceinline__ uint4 dequant8(const uint2& codes, uint32_t sc) {
   uint32_t o[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const uint32_t w = x < 2 ? codes.x : codes.y;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (x & 1))), __NV_E4M3);
-    const __half2 c = *reinterpret_cast<const __half2*>(&h);
-    if constexpr (!kSlow) {
-      const __half2 y = __hmul2(c, *reinterpret_cast<const __half2*>(&sc));
-      o[x] = *reinterpret_cast<const uint32_t*>(&y);
-    } else {
-      const float2 f = __half22float2(c);
-      o[x] = pack_half2(f.x * __uint_as_float(sc), f.y * __uint_as_float(sc));
-    }
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&sc));
+    o[x] = *reinterpret_cast<const uint32_t*>(&y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Eight stored values of a key with a small scale, times 2^-19 (see kSmallScale).
+__device__ __forceinline__ void shrink8(uint8_t* p) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(p);
+  const uint32_t k = 0x00200020u;  // 2^-19 twice
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(w + x), *reinterpret_cast<const __half2*>(&k));
+    w[x] = *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 __device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale && s != 0.f; }
 
@@ -912,19 +918,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     Records<kRuns, kN> rec;
     const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(2 * i + (lane >> 4)) + code_off)); };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get((lane >> 1) & (kN - 1)) + scale_off)); };
-    const auto store = [&](auto slow, uint32_t mine, uint8_t* tile) {
+    const auto store = [&](uint32_t mine, unsigned small, uint8_t* tile) {
 #pragma unroll
       for (int i = 0; i < kN / 2; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * (2 * i + (lane >> 4)) + (sub >> 3));
         const uint4 c = codes[i];
         uint8_t* to = tile + 256 * i;
-        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant8<slow()>(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
-        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant8<slow()>(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant8(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
+        *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant8(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
+      }
+      if (small != 0) {
+#pragma unroll 1
+        for (int i = 0; i < kN / 2; ++i)
+          if (small >> (2 * (2 * i + (lane >> 4)) + (sub >> 3)) & 1) {
+            shrink8(tile + 256 * i + (dst ^ (i << 5)));
+            shrink8(tile + 256 * i + (dst ^ (i << 5) ^ 16));
+          }
       }
     };
     TileWalk tw;
     tw.start(A, sm);
-    bool on = tw.on();
     rec.find(A, tw, key0, lane);
     int n = 0;  // visible records among the loaded ones
     const auto load_tile = [&]() {
@@ -935,25 +948,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       tw.next(A);
       rec.find(A, tw, key0, lane);
     };
-    load_tile();
-    for (uint32_t kk = 0; on; ++kk) {
+    for (uint32_t kk = 0;; ++kk) {
+      const bool on = tw.on();
+      load_tile();  // after the fence, which would wait for loads in flight
+      if (!on) break;
       if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i)
           if (2 * i + (lane >> 4) >= n) codes[i] = make_uint4(0, 0, 0, 0);
         if (((lane >> 1) & (kN - 1)) >= n) sc = 0.f;
       }
-      const bool slow = __any_sync(0xffffffffu, small_scale(sc));
-      const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
-      on = tw.on();
+      const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
+      const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
+      const uint32_t mine = pack_half2(scaled, scaled);
       // the tile's scores are formed: the chunks that V does not need are free
       if (!__all_sync(0xffffffffu, pair_wait(&sm.s_full[kk & 1], (kk >> 1) & 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{}, mine, sm.kv[kk & 1][0]);
-      else store(std::false_type{}, mine, sm.kv[kk & 1][0]);
+      store(mine, small, sm.kv[kk & 1][0]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full[kk & 1]);
-      load_tile();  // after the fence, which would wait for loads in flight
     }
   } else if (warp >= kFirstK) {
     // ------------------------------ K: this CTA's 64 keys x 576 dims ------------------------------
@@ -977,16 +990,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     const auto load_rope = [&](int i) {
       rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
     };
-    const auto store = [&](auto slow, auto h, uint32_t mine, uint8_t* tile) {
+    const auto store = [&](auto h, uint32_t mine, unsigned small, uint8_t* tile) {
+      uint8_t* to = tile + 4 * kCtaKeys * 128 * h();
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h() + (lane >> 4));
-        *reinterpret_cast<uint4*>(tile + 128 * i + 4 * kCtaKeys * 128 * h() + (dst ^ (i << 4))) = dequant8<slow()>(codes[h()][i], s);
+        *reinterpret_cast<uint4*>(to + 128 * i + (dst ^ (i << 4))) = dequant8(codes[h()][i], s);
+      }
+      if (small != 0) {
+#pragma unroll 1
+        for (int i = 0; i < kN; ++i)
+          if (small >> (4 * i + 2 * h() + (lane >> 4)) & 1) shrink8(to + 128 * i + (dst ^ (i << 4)));
       }
     };
     TileWalk tw;
     tw.start(A, sm);
-    bool on = tw.on(), bad = false;
+    bool bad = false;
     rec.find(A, tw, key0, lane);
     int n = 0;  // visible records among the loaded ones
     const auto load_tile = [&]() {
@@ -999,8 +1018,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       tw.next(A);
       rec.find(A, tw, key0, lane);
     };
-    load_tile();
-    for (uint32_t kk = 0; on; ++kk) {
+    for (uint32_t kk = 0;; ++kk) {
+      const bool on = tw.on();
+      load_tile();  // after the fence, which would wait for loads in flight
+      if (!on) break;
+      if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 1;
       if (n < kN) {  // the end of a context
 #pragma unroll
         for (int i = 0; i < kN; ++i)
@@ -1011,19 +1033,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if ((lane >> 2) >= n) sc = 0.f;
       }
       bad |= !(sc <= kMaxScale);
-      const bool slow = __any_sync(0xffffffffu, small_scale(sc));
-      const uint32_t mine = slow ? __float_as_uint(sc) : pack_half2(sc, sc);
-      on = tw.on();
+      const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
+      const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
+      const uint32_t mine = pack_half2(scaled, scaled);
       if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1][0], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
       uint8_t* tile = sm.kv[kk & 1][0];
-      if (slow) store(std::true_type{}, std::integral_constant<int, 0>{}, mine, tile);
-      else store(std::false_type{}, std::integral_constant<int, 0>{}, mine, tile);
+      store(std::integral_constant<int, 0>{}, mine, small, tile);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full + 16 * (kk & 1));
       if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1][1], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
-      if (slow) store(std::true_type{}, std::integral_constant<int, 1>{}, mine, tile);
-      else store(std::false_type{}, std::integral_constant<int, 1>{}, mine, tile);
+      store(std::integral_constant<int, 1>{}, mine, small, tile);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
@@ -1040,8 +1060,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_cluster(full + 16 * (kk & 1) + 8);
-      load_tile();  // after the fence, which would wait for loads in flight
-      if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 2;
     }
     if (bad) latch_error(err, SMLA_ERR_RANGE);
   } else {
@@ -1074,10 +1092,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 #pragma unroll
       for (int i = 0; i < 4; ++i) ask(i, 8 * warp + i);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+      for (int r0 = 8 * warp; r0 < 8 * warp + 8; r0 += 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * warp + 4 * half + i;
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + i;
           uint32_t top2 = 0;  // the largest magnitude (bf16 bits of non-negative values order as integers)
 #pragma unroll
           for (int x = 0; x < 9; ++x) top2 = __vmaxu2(top2, v[i][x] & 0x7FFF7FFFu);
@@ -1089,13 +1107,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 #pragma unroll
           for (int x = 0; x < 9; ++x)
             o[x] = pack_half2(__uint_as_float(v[i][x] << 16) * f, __uint_as_float(v[i][x] & 0xFFFF0000u) * f);
-          if (half == 0) ask(i, r + 4);
+#pragma unroll
+          for (int x = 0; x < 9; ++x) v[i][x] = v[i + 2][x];
           const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
           const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
           *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]) = odd ? o1 : o0;
           *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + 1 - odd)]) = odd ? o0 : o1;
           *reinterpret_cast<uint32_t*>(&sm.q[8][sw128_off(r, lane >> 2) + 4 * (lane & 3)]) = o[8];
           if (lane == 0) sm.row_f[slot][r] = A.abs_scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+        if (r0 < 8 * warp + 4) {
+          ask(2, r0 + 4);
+          ask(3, r0 + 5);
         }
       }
       fence_proxy_async();
@@ -1106,11 +1129,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     Walk w;
     w.start(A, sm);
     if (A.meta != nullptr && cta == 0 && threadIdx.x == 0) A.meta[pair].ntok = 0;
-    if (w.on()) load_q(w, 0);
-    named_bar_sync(1, 32 * kSoftmaxWarps);  // row_f
+    Walk nx = w;  // the unit whose queries come next
     uint32_t kk = 0, n = 0;
-    bool failed = false;
-    while (w.on() && !failed) {
+    float m = 0.f, l = 0.f;
+    bool ok = true;
+    // Each turn: the next unit's queries (while the last MMAs run: the last scores are read, Q is free), the
+    // results of the unit before, then the unit's tiles.  In this order the loop holds one copy of each
+    // part, which matters where its code is met for the first time.
+    for (;; ++n) {
+      if (nx.on()) load_q(nx, n & 1);
+      if (n > 0) {
+        // ---- end of unit ----
+        const int rows = w.rows(A, cta), grow = w.rows_before(A, cta) + row;  // grow: row of the unit
+        const bool real = row < rows, idle = 32 * (sp & 1) >= rows;
+        const int ta = w.ta(A), tb = w.tb(A);
+        ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
+        __syncwarp();
+        tc_fence_after();
+        sm.red[2 * wg + kh][row] = l;
+        if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) break;
+        const float lt = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;  // no visible key: zeros
+        const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
+        const bool partial = ta > 0 || tb < w.tiles();
+        const int64_t slot = 2 * pair + (ta > 0 ? 0 : 1);
+        const int64_t orow = static_cast<int64_t>(w.tok0(A)) * H + grow;
+        const int d0 = 256 * kh + 128 * wg;
+        if (kh == 0 && wg == 0 && real) {
+          if (partial) A.part_lse[slot * kRows + grow] = lse;
+          else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
+        }
+        // A lane holds 128 dims of its row and reads them 32 at a time.  The lanes of a group of four exchange them
+        // (as bf16 pairs; partial results in fp32, in two halves), so that the group stores 64 consecutive
+        // bytes of each of its rows: a lane that stores its own row's dims touches 32 rows in every store, and
+        // exchanges in fp32 throughout made a batch of short units 6 % slower.
+        const int i4 = lane & 3;
+        const bool hi1 = (i4 & 1) != 0, hi2 = (i4 & 2) != 0;
+        const uint32_t t_o = tmem_o + lane_base + 128 * wg;
+#pragma unroll 1
+        for (int x = 0; x < 4 && !idle; ++x) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(t_o + 32 * x, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          uint32_t h[16];
+          if (partial) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) h[i] = o[16 * y + i];
+              transpose4(h, hi1, hi2);
+              float* to = A.part_out + (slot * kRows + grow - i4) * kDL + d0 + 32 * x + 16 * y + 4 * i4;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (row - i4 + j < rows)
+                  *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            transpose4(h, hi1, hi2);
+            __nv_bfloat16* to = A.D.out + (orow - i4) * kDL + d0 + 32 * x + 8 * i4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (row - i4 + j < rows)
+                *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+          }
+        }
+        tc_fence_before();
+        // the unit that goes on in the next pair: what the merge has to join
+        if (cta == 0 && threadIdx.x == 0 && ta == 0 && tb < w.tiles())
+          A.meta[pair] = {sm.x0 + w.rel + w.tiles(), sm.total, sm.pairs, w.tok0(A), w.ntok(A)};
+      }
+      named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read, row_f is written
+      w = nx;
+      if (!w.on()) break;
+      nx.next(A);
       const int rows = w.rows(A, cta), grow = w.rows_before(A, cta) + row;  // grow: row of the unit
       const bool real = row < rows;
       const bool idle = 32 * (sp & 1) >= rows;  // no row of this warp is one: it only keeps the others company
@@ -1118,8 +1214,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       const int ta = w.ta(A), tb = w.tb(A);
       // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
       const float f = fmaxf(sm.row_f[n & 1][row], 1.2e-38f);
-      float m = -INFINITY, l = 0.f;
-      bool ok = true;
+      m = -INFINITY;
+      l = 0.f;
+      bool failed = false;
       for (int tile = ta; tile < tb; ++tile, ++kk) {
         const int buf = kk & 1;
         ok = ok && pair_wait(&sm.s_full[buf], (kk >> 1) & 1, err, &sm.abort);
@@ -1134,16 +1231,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         // visible keys among this thread's 32
         const int vr = vis - (tile * kKeys + 64 * kh + 32 * wg);
         float mx = -INFINITY;
-        if (idle) {
-        } else if (__all_sync(0xffffffffu, vr >= 32)) {
+        if (!idle) {
+          if (!__all_sync(0xffffffffu, vr >= 32)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= vr) r[i] = 0xFF800000u;  // -inf
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (i >= vr) r[i] = 0xFF800000u;  // -inf
-            mx = fmaxf(mx, __uint_as_float(r[i]));
-          }
         }
         mx = mx == -INFINITY ? -INFINITY : mx * f;
         // The maximum of a row moves only when a score passes it by 2^8; only then (and on the first
@@ -1208,73 +1303,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (lane == 0) arrive_cluster(p_full[buf]);
       }
       if (failed) break;
-      // the next unit's queries while the last MMAs run (the last scores are read: Q is free)
-      Walk nx = w;
-      nx.next(A);
-      if (nx.on()) load_q(nx, (n + 1) & 1);
-      // ---- end of unit ----
-      ok = pair_wait(&sm.kv_free[(kk - 1) & 1][1], ((kk - 1) >> 1) & 1, err, &sm.abort) && ok;
-      __syncwarp();
-      tc_fence_after();
-      sm.red[2 * wg + kh][row] = l;
-      if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) break;
-      const float lt = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
-      const float inv = lt == 0.f ? 0.f : 1.f / lt;  // no visible key: zeros
-      const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
-      const bool partial = ta > 0 || tb < w.tiles();
-      const int64_t slot = 2 * pair + (ta > 0 ? 0 : 1);
-      const int64_t orow = static_cast<int64_t>(w.tok0(A)) * H + grow;
-      const int d0 = 256 * kh + 128 * wg;
-      if (kh == 0 && wg == 0 && real) {
-        if (partial) A.part_lse[slot * kRows + grow] = lse;
-        else if (A.D.lse != nullptr) A.D.lse[orow] = lse;
-      }
-      // A lane holds 128 dims of its row and reads them 32 at a time.  The lanes of a group of four exchange them
-      // (as bf16 pairs; partial results in fp32, in two halves), so that the group stores 64 consecutive
-      // bytes of each of its rows: a lane that stores its own row's dims touches 32 rows in every store, and
-      // exchanges in fp32 throughout made a batch of short units 6 % slower.
-      const int i4 = lane & 3;
-      const bool hi1 = (i4 & 1) != 0, hi2 = (i4 & 2) != 0;
-      const uint32_t t_o = tmem_o + lane_base + 128 * wg;
-#pragma unroll 1
-      for (int x = 0; x < 4 && !idle; ++x) {
-        uint32_t o[32];
-        __syncwarp();
-        tmem_ld32(t_o + 32 * x, o);
-        tmem_ld_wait(o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-        uint32_t h[16];
-        if (partial) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) h[i] = o[16 * y + i];
-            transpose4(h, hi1, hi2);
-            float* to = A.part_out + (slot * kRows + grow - i4) * kDL + d0 + 32 * x + 16 * y + 4 * i4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (row - i4 + j < rows)
-                *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-          transpose4(h, hi1, hi2);
-          __nv_bfloat16* to = A.D.out + (orow - i4) * kDL + d0 + 32 * x + 8 * i4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row - i4 + j < rows)
-              *reinterpret_cast<uint4*>(to + j * kDL) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-        }
-      }
-      tc_fence_before();
-      named_bar_sync(1, 32 * kSoftmaxWarps);  // red is read, row_f of the next unit is written
-      // the unit that goes on in the next pair: what the merge has to join
-      if (cta == 0 && threadIdx.x == 0 && ta == 0 && tb < w.tiles())
-        A.meta[pair] = {sm.x0 + w.rel + w.tiles(), sm.total, sm.pairs, w.tok0(A), w.ntok(A)};
-      w = nx;
-      ++n;
     }
   }
   tc_fence_before();
