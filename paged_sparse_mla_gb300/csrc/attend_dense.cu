@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t visible(const DenseArgs& A, int len, int i, i
 // Shapes without a tensor-core kernel: fp32 throughout.  One CTA per (query token, 8 heads); keys in
 // tiles of 32, dequantised into shared memory; warp h scores head h (a lane per key), then every
 // thread accumulates its dims for the 8 heads.  Bound by shared-memory reads, one per multiply-add: on the
-// full shape, which has its own kernel, it took 33.6 ms where that takes 0.20 (32 tokens, 64 heads,
+// full shape, which has its own kernel, it took 33.6 ms where that takes 0.19 (32 tokens, 64 heads,
 // 8,192 to 32,768 positions each).
 // ---------------------------------------------------------------------------
 constexpr int kSHeads = 8, kSKeys = 32, kSThreads = 256;
@@ -207,15 +207,15 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // range, and a unit that crosses ranges leaves partial results, which dense_merge_kernel joins by their lse.
 //
 // Bound by the shared-memory and L1 data path.  A tile moves, per SM, 240 KB of MMA operands, 120 KB of
-// stores of converted keys and 59 KB of record loads through it (2.0 us with records from L2), against
-// 1.2 us of MMA at full rate.  With loads that always hit L1 (a wrong answer) the cases below took 11 to
-// 20 % less, the largest share of any one part.  More rows per pair would read each operand
-// for more rows, but O fills half of tensor memory and the scores a quarter.  Measured, 64 heads:
-//   2,048 query tokens at 20,480 positions   4.13 ms, 1.20 PFLOP/s (tensor pipe active half of the time)
-//   32 decode tokens, 8,192 to 32,768        199 us, 2.2 TB/s (half of a pair's rows are empty, and
-//                                            DRAM's latency adds a fifth)
-//   64 x 4 drafted tokens, 4,096 to 32,768   669 us, 0.98 PFLOP/s
-//   one token at one position                18.4 us, the chain plan -> queries -> tile -> results -> merge
+// stores of converted keys and 59 KB of record loads through it (1.9 us with records from L2), against
+// 1.2 us of MMA at full rate.  With loads that always hit L1 (a wrong answer) the cases below took 8 to
+// 18 % less, the largest share of any one part.  The second limit is the instruction cache, which five roles
+// share: one copy of every part of the loops took 5 to 7 % off.  Measured, 64 heads:
+//   2,048 query tokens at 20,480 positions   3.9 ms, 1.27 PFLOP/s (tensor pipe active half of the time)
+//   32 decode tokens, 8,192 to 32,768        187 us, 2.3 TB/s (half of a pair's rows are empty, and
+//                                            DRAM's latency adds a sixth)
+//   64 x 4 drafted tokens, 4,096 to 32,768   640 us, 1.03 PFLOP/s
+//   one token at one position                15 us, the chain plan -> queries -> tile -> results -> merge
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128, kKeys = 128;      // of a pair
 constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
@@ -547,7 +547,7 @@ __device__ __forceinline__ int page_of(const PairArgs& A, int j) {
 // of 16, so that they lie one after another in a block and every lane knows them all from the first
 // (`n` of them hold visible positions; what follows in the block is read too and zeroed by the caller).
 // Otherwise lane i looks up the i-th and the lanes pass the addresses around, two shuffles a record: on blocks of
-// 64 that takes 3 % longer in decode steps (205 us against 199) and 5 % in a chunk (4.36 ms against 4.12).
+// 64 that takes 3 % longer in decode steps (194 us against 188) and 5 % in a chunk (4.11 ms against 3.89).
 // find() asks for the block id, take() turns it into the address: a tile later, so that nothing waits for
 // the block table.
 template <bool kRuns, int kN>
@@ -1317,8 +1317,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 // Joins the parts of units that ran on several pairs: lse = ln sum e^lse_i, out = sum e^(lse_i - lse) out_i
 // in fp32.  A warp takes a row (a lane 16 dims) where a few parts are to be joined; where there are many, as
 // for one long sequence, the block's four warps share it (a lane 4 dims, eight parts' loads in flight).
-// With the whole call's time: one sequence of 262,143 positions 98 us (119 with a warp per row), 64 sequences of
-// four tokens 669 us (680 with a block per row).
+// With the whole call's time: one sequence of 262,143 positions 95 us (117 with a warp per row), 64 sequences of
+// four tokens 645 us (655 with a block per row).
 constexpr int kMergeThreads = 128, kFewParts = 4;
 template <int kStep>
 __device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, int row, int quarter0, int quarters,
@@ -1479,8 +1479,8 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.bs_shift1 = log2 > 0 ? 1 : 0;
   A.bs_shift2 = log2 > 0 ? log2 - 1 : 0;
   // Splitting pays wherever units are fewer or more uneven than pairs, and costs nothing measurable elsewhere:
-  // 32 decode tokens 199 us (622 without), one long sequence 98 us (4.8 ms), a chunk of 1,024 units 4.12 ms
-  // (4.36).  Without a workspace units stay whole.
+  // 32 decode tokens 188 us (598 without), one long sequence 95 us (4.7 ms), a chunk of 1,024 units 3.89 ms
+  // (4.17).  Without a workspace units stay whole.
   const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
   if (split) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
