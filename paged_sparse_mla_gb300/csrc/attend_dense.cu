@@ -202,9 +202,10 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 //
 // Warps: eight take the softmax of the CTA's rows, its queries and results; eight turn the CTA's keys into K,
 // eight the other CTA's into V; one lane of one warp issues all MMAs of the pair, another warp asks for
-// keys and queries to come into L2, a third looks for NaN where it would spread.  The grid is one pair per two SMs.  All work, counted in key tiles, is
-// cut into as many equal ranges: a pair walks over the units (sequence, group of query tokens) of its
-// range, and a unit that crosses ranges leaves partial results, which dense_merge_kernel joins by their lse.
+// keys and queries to come into L2, a third looks for NaN where it would spread.  The grid is one pair
+// per two SMs.  All work, counted in key tiles, is cut into as many equal ranges: a pair walks over the
+// units (sequence, group of query tokens) of its range, and a unit that crosses ranges leaves partial
+// results, which dense_merge_kernel joins by their lse.
 //
 // Bound by the shared-memory and L1 data path.  A tile moves, per SM, 240 KB of MMA operands, 120 KB of
 // stores of converted keys and 59 KB of record loads through it (1.9 us with records from L2), against
@@ -463,7 +464,7 @@ __device__ __forceinline__ void pair_drain(uint64_t* bar, uint32_t parity) {
 // that the operands live in uniform registers (issued from a branch of one lane, each instruction moved
 // them there again and took about 60 cycles whatever its size).  The operands move by constant byte
 // offsets from a descriptor's low word (its address field counts 16 bytes); the loops around are short,
-// since this warp shares the instruction cache with 24 others (all 36 products of a tile unrolled were
+// since this warp shares the instruction cache with 27 others (all 36 products of a tile unrolled were
 // issued at 65 cycles each).
 template <int kAOff, int kBOff>
 __device__ __forceinline__ void mma2_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,

@@ -59,6 +59,17 @@ def test_softmax_scales(sigma):
     ok()
 
 
+def test_scales_of_every_size_side_by_side():
+    """Neighbouring keys and the quant tiles of one key with scales from far below fp16's normal values to large."""
+    rng = np.random.default_rng(44)
+    size = np.array([1e-8, 1e-6, 1e-5, 1e-4, 1e-3, 0.03, 1.0, 10.0])[rng.integers(0, 8, (300, 4))].repeat(128, 1)
+    c = Case([300], [3], 64, seed=44, key_scale=size)
+    c.check(c.run())
+    c = Case([300], [3], 64, 7, seed=44, key_scale=np.minimum(size, 1e-5))
+    c.check(c.run())
+    ok()
+
+
 @pytest.mark.parametrize("value", [0x7F, 0xFF])
 def test_nan_in_the_cache(value):
     """At a position that every token sees it is theirs; where only the last token sees it, the others' zero
