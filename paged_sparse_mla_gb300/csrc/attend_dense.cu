@@ -533,7 +533,7 @@ __device__ __forceinline__ void shrink8(uint8_t* p) {
     w[x] = *reinterpret_cast<const uint32_t*>(&y);
   }
 }
-__device__ __forceinline__ bool small_scale(float s) { return s < kSmallScale && s != 0.f; }
+__device__ __forceinline__ bool small_scale(float s) { return fabsf(s) < kSmallScale && s != 0.f; }
 
 // What unreadable records read as (bad block ids, and nothing left to read): 16 records of zeros.
 __device__ uint4 g_zero_records[16 * 41];
@@ -1033,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
         if ((lane >> 2) >= n) sc = 0.f;
       }
-      bad |= !(sc <= kMaxScale);
+      bad |= !(fabsf(sc) <= kMaxScale);
       const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
       const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
       const uint32_t mine = pack_half2(scaled, scaled);

@@ -70,6 +70,23 @@ def test_scales_of_every_size_side_by_side():
     ok()
 
 
+def test_scales_of_either_sign():
+    """A negative scale (no store writes one) negates its 128 dims, and counts by its size for the range."""
+    c = Case([150], [2], 64, seed=45)
+    lat, rope = c.keys[0][0].copy(), c.keys[0][1]
+    blocks = c.pool.view(-1, c.lay.block_stride)
+    for pos, tile in ((0, 0), (64, 3), (149, 2)):
+        rec = blocks[int(c.table[0, pos // 64]), :64 * 656].view(64, 656)
+        sc = rec[pos % 64, 512 + 4 * tile:516 + 4 * tile]
+        sc.copy_((-sc.clone().view(torch.float32)).view(torch.uint8))
+        lat[pos, 128 * tile:128 * tile + 128] *= -1
+    c.check(c.run(), keys=[(lat, rope)])
+    ok()
+    sc.copy_(torch.tensor([-200.0], device="cuda").view(torch.uint8))
+    c.run()
+    assert smla.smla_get_last_error() == 7
+
+
 @pytest.mark.parametrize("value", [0x7F, 0xFF])
 def test_nan_in_the_cache(value):
     """At a position that every token sees it is theirs; where only the last token sees it, the others' zero
