@@ -232,7 +232,9 @@ static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * 
 // The running maximum moves when a score passes it by 2^8: few tiles rescale O, and P stays far below fp16's end
 // (2^12 was no faster).
 constexpr float kRescale = 8.0f;
-constexpr float kMaxScale = 65504.0f / 448.0f;
+// A scale rounds to fp16 before it multiplies: 146.125 is the last value whose product with code 448 stays finite
+// (65,464; 146.25 gives 65,520, which rounds to infinity), and from half way between them a scale rounds up.
+constexpr float kScaleEnd = 146.1875f;
 constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
 // Below 2^-13 a scale would lose bits in fp16 (from 2^-14 on).  Such a scale is taken times 2^19, which keeps its
 // products (at most 448 x 2^6) in range, and what was stored is multiplied by 2^-19 in a second pass: exact down to
@@ -1033,7 +1035,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
         if ((lane >> 2) >= n) sc = 0.f;
       }
-      bad |= !(fabsf(sc) <= kMaxScale);
+      bad |= !(fabsf(sc) < kScaleEnd);
       const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
       const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
       const uint32_t mine = pack_half2(scaled, scaled);
