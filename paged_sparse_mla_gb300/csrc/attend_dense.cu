@@ -584,13 +584,12 @@ struct Records {
   }
 };
 
-// (a, b) * (c, c) + (d, d) and (a, b) + (c, d) as packed fp32 operations
-__device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
+// (a, b) * (c, c) and (a, b) + (c, d) as packed fp32 operations
+__device__ __forceinline__ float2 mul2(float2 a, float c) {
   uint64_t r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmov.b64 z, {%4, %4};\n\t"
-      "fma.rn.f32x2 %0, x, y, z;\n\t}"
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmul.rn.f32x2 %0, x, y;\n\t}"
       : "=l"(r)
-      : "f"(a.x), "f"(a.y), "f"(c), "f"(d));
+      : "f"(a.x), "f"(a.y), "f"(c));
   return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -1243,20 +1242,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
         }
-        mx = mx == -INFINITY ? -INFINITY : mx * f;
         // The maximum of a row moves only when a score passes it by 2^8; only then (and on the first
-        // tile) the four threads of every row compare notes.
+        // tile) the four threads of every row compare notes.  It is kept as the products' value, before the
+        // scale: a score's difference from it is exact near it, however large both are, while a product
+        // m f would round by many powers of two in probability from 2^28 on.
         const bool first = tile == ta;
-        if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || mx > m + kRescale)) {
+        if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || (mx - m) * f > kRescale)) {
           sm.red[2 * wg + kh][row] = mx;
           if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) {
             failed = true;
             break;
           }
           const float mt = fmaxf(fmaxf(sm.red[0][row], sm.red[1][row]), fmaxf(sm.red[2][row], sm.red[3][row]));
-          const bool move = first || mt > m + kRescale;
+          const bool move = first || (mt - m) * f > kRescale;
           const float mn = move ? fmaxf(m, mt) : m;
-          const float alpha = move && m != -INFINITY ? exp2f(m - mn) : 1.f;
+          const float alpha = move && m != -INFINITY ? exp2f((m - mn) * f) : 1.f;
           l *= alpha;
           m = mn;
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -1288,7 +1288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f, -mu);
+          const float2 x = mul2(add2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(-mu, -mu)), f);
           const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
           ls = add2(ls, p);
           pw[i / 2] = pack_half2(p.x, p.y);
@@ -1306,6 +1306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (lane == 0) arrive_cluster(p_full[buf]);
       }
       if (failed) break;
+      m *= f;  // for the unit's end: in powers of two
     }
   }
   tc_fence_before();

@@ -1,5 +1,5 @@
 """smla_attend_dense at the ends of what its fp16 operands hold: latent scales around the last one whose
-largest code stays finite.  Values are checked with the bounds that tests/test_gpu_dense.py derives."""
+largest code stays finite, and scores of any size.  Values are checked with the bounds that tests/test_gpu_dense.py derives."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +47,30 @@ def test_scales_up_to_the_last_finite_one(scale, latched, pos, sign):
     lat, rope = c.keys[0][0].copy(), c.keys[0][1]
     lat[pos, 384:512] = rec[384:512].view(torch.float8_e4m3fn).double().cpu().numpy() * float(s)
     c.check(got, keys=[(lat, rope)])
+
+
+@pytest.mark.parametrize("q_scale", [1e4, 1e5, 1e6, 1e8, 1e20])
+def test_scores_beyond_fp32s_integers(q_scale):
+    """Scores so large that neighbouring fp32 values are whole powers of two apart in probability: weights come from
+    differences of scores, so that the outputs stay averages of the values."""
+    c = Case([333, 65], [3, 1], 64, seed=10, key_scale=1e3, q_scale=q_scale)
+    for workspace in (True, False):
+        out, lse = c.run(workspace)
+        ok()
+        c.check((out, lse))
+        assert torch.isfinite(lse).all()
+        for row, (lat, _) in zip((0, 3), c.keys):
+            assert out[row].abs().max() <= 1.01 * np.abs(lat).max()
+    # one position whose score is the largest by far more than the keys' roundings takes everything
+    c.q[:], c.q_pe[:] = 0, 0
+    c.q_pe[..., 0] = q_scale
+    slots = [int(c.table[b, j // 64]) for b, j in ((0, 100), (1, 30))]
+    blocks = c.pool.view(-1, c.lay.block_stride)
+    for blk, j in zip(slots, (100, 30)):
+        blocks[blk, (j % 64) * 656 + 528:(j % 64) * 656 + 530] = torch.tensor([1e4], device="cuda").bfloat16().view(torch.uint8)
+    for workspace in (True, False):
+        out, _ = c.run(workspace)
+        ok()
+        for t, (lat, j) in enumerate(((c.keys[0][0], 100),) * 3 + ((c.keys[1][0], 30),)):
+            want = torch.from_numpy(lat[j]).cuda()
+            assert ((out[t].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -11) + 2.0 ** -25).all()
