@@ -507,9 +507,11 @@ smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* 
  * finite: on the tensor cores a NaN at a position that only some query tokens see reaches the others too.
  * Latents of 512 dims in tiles of 128 with 64 rope dims run on the tensor cores with
  * fp16 operands (fp32 accumulation): a latent scale of 146.1875 or more (rounded to fp16, it takes
- * code 448 past fp16's end), a rope value beyond fp16's range or such a NaN latches SMLA_ERR_RANGE, and the outputs of its
- * sequence are not valid; cached values below 2^-14 are held to 2^-25 absolutely.  Other shapes kvpack_store
- * takes (d_rope <= 64) run in fp32 on the CUDA cores.
+ * code 448 past fp16's end), a rope value beyond fp16's range or such a NaN latches
+ * SMLA_ERR_RANGE, and the outputs of its sequence are not valid; cached values below 2^-14 are
+ * held to 2^-25 absolutely, a position's weight to 2^-11 of itself or 2^-32 of the row's largest
+ * weight, whichever is more.  Other shapes kvpack_store takes (d_rope <= 64) run in fp32 on the
+ * CUDA cores.
  * The pool is 16-byte aligned.  The same call gives the same bits every time.
  */
 smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t* params, const void* pool, int layer,

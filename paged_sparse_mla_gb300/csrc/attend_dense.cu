@@ -179,7 +179,7 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // sequence, and on tiles of 128 keys; each CTA owns 64 of the rows and 64 of the keys:
 //   S[128 x 128] = Q[128 x 576] . K^T      two-SM MMAs, M = 128, N = 128: each CTA brings its 64 query
 //                                          rows and its 64 keys
-//   P = 2^(S f - m), row sums in registers  each CTA for its 64 rows and all 128 keys
+//   P = 2^(S f - m + 7), row sums in registers  each CTA for its 64 rows and all 128 keys
 //   O[128 x 512] += P[128 x 128] . V        two-SM MMAs, M = 128, N = 256, twice: each CTA brings its 64
 //                                          rows of P and all 128 keys of its 256 latent dims
 // An M = 128 two-SM accumulator keeps a CTA's 64 rows in 128 lanes: lanes 0-63 hold the first half of
@@ -197,8 +197,9 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // memory for two tile buffers beside the queries.
 //
 // Operands are fp16, not bf16: an E4M3 code is exact in it, so that a key carries the rounding of its scale
-// and of the product (2^-11 each; bf16 2^-8), P that of 2^-11.  What fp16 lacks in range is met by a
-// power of two per query row and checked for keys (SMLA_ERR_RANGE).  Sums, maxima and O are fp32.
+// and of the product (2^-11 each; bf16 2^-8), P that of 2^-11 (see kLift for its smallest values).  What fp16
+// lacks in range is met by a power of two per query row and checked for keys (SMLA_ERR_RANGE).  Sums, maxima
+// and O are fp32.
 //
 // Warps: eight take the softmax of the CTA's rows, its queries and results; eight turn the CTA's keys into K,
 // eight the other CTA's into V; one lane of one warp issues all MMAs of the pair, another warp asks for
@@ -229,9 +230,11 @@ constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kKRegs = 72, kVRegs = 48, kI
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * kVRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
-// The running maximum moves when a score passes it by 2^8: few tiles rescale O, and P stays far below fp16's end
-// (2^12 was no faster).
+// The running maximum moves when a score passes it by 2^8: few tiles rescale O (2^12 was no faster).
 constexpr float kRescale = 8.0f;
+// P is formed 2^7 times as large, 2^15 at most: fp16's last step, 2^-24, is then 2^-31 of a row's largest weight at
+// most.  Without it a long tail 17 nats below one position rounded to zeros in P but not in the sum that divides.
+constexpr float kLift = 7.0f;
 // A scale rounds to fp16 before it multiplies: 146.125 is the last value whose product with code 448 stays finite
 // (65,464; 146.25 gives 65,520, which rounds to infinity), and from half way between them a scale rounds up.
 constexpr float kScaleEnd = 146.1875f;
@@ -584,12 +587,13 @@ struct Records {
   }
 };
 
-// (a, b) * (c, c) and (a, b) + (c, d) as packed fp32 operations
-__device__ __forceinline__ float2 mul2(float2 a, float c) {
+// (a, b) * (c, c) + (d, d) and (a, b) + (c, d) as packed fp32 operations
+__device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
   uint64_t r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmul.rn.f32x2 %0, x, y;\n\t}"
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmov.b64 z, {%4, %4};\n\t"
+      "fma.rn.f32x2 %0, x, y, z;\n\t}"
       : "=l"(r)
-      : "f"(a.x), "f"(a.y), "f"(c));
+      : "f"(a.x), "f"(a.y), "f"(c), "f"(d));
   return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -1288,7 +1292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const float2 x = mul2(add2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(-mu, -mu)), f);
+          const float2 x = fma2(add2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(-mu, -mu)), f, kLift);
           const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
           ls = add2(ls, p);
           pw[i / 2] = pack_half2(p.x, p.y);
@@ -1306,7 +1310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
         if (lane == 0) arrive_cluster(p_full[buf]);
       }
       if (failed) break;
-      m *= f;  // for the unit's end: in powers of two
+      m = m * f - kLift;  // for the unit's end: in powers of two
     }
   }
   tc_fence_before();

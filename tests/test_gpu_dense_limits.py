@@ -1,5 +1,6 @@
 """smla_attend_dense at the ends of what its fp16 operands hold: latent scales around the last one whose
-largest code stays finite, and scores of any size.  Values are checked with the bounds that tests/test_gpu_dense.py derives."""
+largest code stays finite, tails of small weights, and scores of any size.  Values are checked with the
+bounds that tests/test_gpu_dense.py derives."""
 import numpy as np
 import pytest
 import torch
@@ -47,6 +48,80 @@ def test_scales_up_to_the_last_finite_one(scale, latched, pos, sign):
     lat, rope = c.keys[0][0].copy(), c.keys[0][1]
     lat[pos, 384:512] = rec[384:512].view(torch.float8_e4m3fn).double().cpu().numpy() * float(s)
     c.check(got, keys=[(lat, rope)])
+
+
+class Sink:
+    """A long cache made on the GPU: latents of codes around 160 and scales near 1 / 160 (values near one), ropes
+    zero, and one position whose value is zero and whose score stands `gap` above all others': query rows hold a
+    small random latent part and 1 in the first rope dim, which is gap / sigma at that position."""
+
+    def __init__(self, n, gap, at, count, heads=8, seed=53, bs=64):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        blocks = -(-n // bs)
+        self.heads, self.count, self.n, self.sigma = heads, count, n, 1 / 24
+        self.lay = smla.layout_init(bs, 1, 512, 64, 128, 32, blocks)
+        self.pool = torch.zeros(blocks, self.lay.block_stride, dtype=torch.uint8, device="cuda")
+        rec = torch.as_strided(self.pool, (blocks, bs, 656), (self.lay.block_stride, 656, 1))
+        codes = (160 + 40 * torch.randn(blocks, bs, 512, generator=g, device="cuda")).clamp_(-448, 448).to(torch.float8_e4m3fn)
+        scales = (0.8 + 0.4 * torch.rand(blocks, bs, 4, generator=g, device="cuda")) / 160
+        rope = torch.zeros(blocks, bs, 64, dtype=torch.bfloat16, device="cuda")
+        codes.view(torch.uint8)[at // bs, at % bs] = 0
+        rope[at // bs, at % bs, 0] = gap / self.sigma
+        rec[..., :512], rec[..., 512:528], rec[..., 528:] = codes.view(torch.uint8), scales.view(torch.uint8), rope.view(torch.uint8)
+        self.lat = (codes.double().unflatten(-1, (4, 128)) * scales.double()[..., None]).view(-1, 512)[:n]
+        self.rope = rope.double().view(-1, 64)[:n]
+        self.pool = self.pool.view(-1)
+        self.table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None].contiguous()
+        self.q = (0.01 * torch.randn(count, heads, 512, generator=g, device="cuda")).bfloat16()
+        self.q_pe = torch.zeros(count, heads, 64, dtype=torch.bfloat16, device="cuda")
+        self.q_pe[..., 0] = 1
+        self.prm = smla.make_params(heads, 1, 1, self.sigma)
+
+    def run(self, workspace):
+        out = torch.empty(self.count, self.heads, 512, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(self.count, self.heads, device="cuda")
+        ws = torch.empty(smla.attend_dense_workspace_size(self.lay, self.prm, self.count), dtype=torch.uint8, device="cuda")
+        smla.smla_attend_dense(self.lay, self.prm, self.pool, 0, self.q, self.q_pe, self.table,
+                               torch.tensor([self.n], dtype=torch.int32, device="cuda"),
+                               torch.tensor([0, self.count], dtype=torch.int32, device="cuda"), out, lse, workspace=ws if workspace else None)
+        ok()
+        return out, lse
+
+    def check(self, got, tokens):
+        """The bounds of tests/test_gpu_dense.py without their allowance for small probabilities, which here is
+        n 2^-32 max |K|: a probability is held as a multiple of 2^-24 (off by 2^-25) where the largest is at least
+        2^7 (2^15 at most, 2^8 below it at least), so n of them lose n 2^-25 / 2^7 of the sum's weight at most.  The fp32 sums
+        (blocks of 128 products, then one addition a tile, 2^-24 each at most) stay below n / 128 2^-24 |out|."""
+        out, lse = got
+        for t in tokens:
+            v = self.n - self.count + t + 1
+            q, lat = self.q[t].double(), self.lat[:v]
+            s = self.sigma * (q @ lat.T + self.q_pe[t].double() @ self.rope[:v].T)
+            p = torch.softmax(s, -1)
+            want, size = p @ lat, p @ lat.abs()
+            ds = self.sigma * (2.0 ** -10 * (q.abs() @ lat.abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))[:, None]
+            bound = 2.0 ** -8 * want.abs() + size * (2.0 ** -10 + 2.0 ** -11 + 2 * ds + v / 128 * 2.0 ** -24) + 2.0 ** -25 + v * 2.0 ** -32 * lat.abs().max()
+            e = (out[t].double() - want).abs()
+            assert (e <= bound).all(), f"token {t}: off by {(e / bound).max():.1f} times the bound, {(e / want.abs()).max():.3f} of the value"
+            wl = torch.logsumexp(s, -1)
+            assert ((lse[t].double() - wl).abs() <= ds[:, 0] + 1e-5 * (1 + wl.abs())).all()
+
+
+@pytest.mark.parametrize("at", [0, 131_000])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 17.5, 18.5])
+def test_a_dominant_position_leaves_the_tail_its_weight(gap, at):
+    """An attention sink: one position of zero value far above 262,143 others, whose sum still makes the output."""
+    c = Sink(262_144, gap, at, 1)
+    c.check(c.run(False), [0])
+    c.check(c.run(True), [0])
+
+
+@pytest.mark.parametrize("gap", [12.0, 17.5])
+def test_a_dominant_position_before_a_chunk(gap):
+    """The same for a chunk, whose units each see the whole prefix on one pair of SMs or two."""
+    c = Sink(200_000, gap, 3, 1300)
+    for workspace in (True, False):
+        c.check(c.run(workspace), [0, 1, 500, 1024, 1299])
 
 
 @pytest.mark.parametrize("q_scale", [1e4, 1e5, 1e6, 1e8, 1e20])
