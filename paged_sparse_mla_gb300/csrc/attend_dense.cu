@@ -549,6 +549,11 @@ __device__ __forceinline__ int page_of(const PairArgs& A, int j) {
   return static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
 }
 
+// Record of a page's token `off`, in 64 bits: a page may hold more than 2^31 bytes of records.
+__device__ __forceinline__ const uint8_t* record(const PairArgs& A, int blk, int off) {
+  return A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec;
+}
+
 // The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
 // of 16, so that they lie one after another in a block and every lane knows them all from the first
 // (`n` of them hold visible positions; what follows in the block is read too and zeroed by the caller).
@@ -559,14 +564,14 @@ __device__ __forceinline__ int page_of(const PairArgs& A, int j) {
 template <bool kRuns, int kN>
 struct Records {
   const uint8_t* at;
-  int blk, off, n;  // blk = INT_MIN: past the visible positions
+  int blk, off, n;  // blk = INT_MIN: past the visible positions; off: token of the page
   __device__ __forceinline__ void find(const PairArgs& A, const TileWalk& tw, int key0, int lane) {
     blk = INT_MIN;
     if (!tw.on()) return;
     const int j = tw.tile * kKeys + key0 + (kRuns ? 0 : lane & (kN - 1));
     if (j >= tw.w.nvis) return;
     const int pg = page_of(A, j);
-    off = (j - pg * A.D.L.block_size) * kRec;
+    off = j - pg * A.D.L.block_size;
     n = kRuns ? min(tw.w.nvis - j, kN) : kN;
     blk = max(__ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg), -1);
   }
@@ -578,7 +583,7 @@ struct Records {
       latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
       return kN;
     }
-    at = A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + off;
+    at = record(A, blk, off);
     return n;
   }
   __device__ __forceinline__ const uint8_t* get(int i) const {
@@ -878,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
             const int pg = page_of(A, j);
             const int blk = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg);
             if (blk >= 0 && blk < A.D.L.num_blocks)
-              prefetch_l2_bulk(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + (j - pg * A.D.L.block_size) * kRec, kRec);
+              prefetch_l2_bulk(record(A, blk, j - pg * A.D.L.block_size), kRec);
           }
         }
       }
@@ -895,8 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           const int pg = page_of(A, j);
           const int blk = __ldg(A.D.block_table + static_cast<int64_t>(w.b) * A.D.bt_stride + pg);
           if (blk < 0 || blk >= A.D.L.num_blocks) continue;
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride +
-                                                               (j - pg * A.D.L.block_size) * kRec) + lane);
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(record(A, blk, j - pg * A.D.L.block_size)) + lane);
           const auto is = [](uint32_t x) { return (x & 0x7F7F7F7Fu) + 0x01010101u; };
           bad |= ((is(c.x) | is(c.y) | is(c.z) | is(c.w)) & 0x80808080u) != 0;
         }

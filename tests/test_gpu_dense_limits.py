@@ -149,3 +149,43 @@ def test_scores_beyond_fp32s_integers(q_scale):
         for t, (lat, j) in enumerate(((c.keys[0][0], 100),) * 3 + ((c.keys[1][0], 30),)):
             want = torch.from_numpy(lat[j]).cuda()
             assert ((out[t].double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -11) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("bs", [3_300_000, 3_300_001])
+def test_records_beyond_2_gib_of_one_page(bs):
+    """A sequence in one page whose last records lie more than 2^31 bytes into it: all zeros but for its first 100
+    and last 300 positions (a page size of either kind: multiples of 16, and others)."""
+    g = torch.Generator(device="cuda").manual_seed(56)
+    n, heads, sigma = bs - 7, 4, 1 / 24
+    lay = smla.layout_init(bs, 1, 512, 64, 128, 32, 1)
+    pool = torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda")
+    rec = pool[:bs * 656].view(bs, 656)
+    at = torch.cat([torch.arange(100), torch.arange(n - 300, n)]).cuda()
+    assert int(at[-1]) * 656 > 2 ** 31
+    codes = (100 * torch.randn(400, 512, generator=g, device="cuda")).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    scales = (0.8 + 0.4 * torch.rand(400, 4, generator=g, device="cuda")) / 100
+    rope = torch.zeros(400, 64, dtype=torch.bfloat16, device="cuda")
+    rope[:, 0] = 8 / sigma
+    rec[at] = torch.cat([codes.view(torch.uint8), scales.view(torch.uint8), rope.view(torch.uint8)], 1)
+    rec[n:] = 255                                             # NaN behind the sequence
+    lat = (codes.double().unflatten(-1, (4, 128)) * scales.double()[..., None]).view(400, 512)
+    q = (0.1 * torch.randn(2, heads, 512, generator=g, device="cuda")).bfloat16()
+    q_pe = torch.zeros(2, heads, 64, dtype=torch.bfloat16, device="cuda")
+    q_pe[..., 0] = 1
+    prm = smla.make_params(heads, 1, 1, sigma)
+    ws = torch.empty(smla.attend_dense_workspace_size(lay, prm, 2), dtype=torch.uint8, device="cuda")
+    table, lens, qsl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0]], [n], [0, 2]))
+    for workspace in (ws, None):
+        out, lse = torch.empty(2, heads, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(2, heads, device="cuda")
+        smla.smla_attend_dense(lay, prm, pool, 0, q, q_pe, table, lens, qsl, out, lse, workspace=workspace)
+        ok()
+        for t in range(2):
+            seen = 399 + t
+            s = sigma * (q[t].double() @ lat[:seen].T) + sigma * float(rope[0, 0])
+            total = s.exp().sum(-1, keepdim=True) + (n - 400)
+            want, size = s.exp() @ lat[:seen] / total, s.exp() @ lat[:seen].abs() / total
+            ds = sigma * (2.0 ** -10 * (q[t].double().abs() @ lat.abs().T).amax(-1) + 2.0 ** -25 * q[t].double().abs().sum(-1))[:, None]
+            bound = 2.0 ** -8 * want.abs() + size * (2.0 ** -10 + 2.0 ** -11 + 2 * ds + n / 128 * 2.0 ** -24) + 2.0 ** -25 + 400 * 2.0 ** -32 * lat.abs().max()
+            assert ((out[t].double() - want).abs() <= bound).all()
+            wl = total.log()[:, 0]
+            assert ((lse[t].double() - wl).abs() <= ds[:, 0] + n / 128 * 2.0 ** -24 + 1e-5 * (1 + wl.abs())).all()
