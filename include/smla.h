@@ -501,8 +501,8 @@ smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* 
  *              of SMs (as with fewer bytes).  Its contents need not be kept; calls that may
  *              overlap need one each, captured ones among them.
  * seq_lens, query_start_loc and block_table are read on the device: block ids outside the
- * pool read as zeros and positions past the block-table row are not visited (both latch
- * SMLA_ERR_BAD_INDEX).  query_start_loc is trusted to increase from 0 to at most n_tokens.
+ * pool read as zeros, and positions past the block-table row or from 2^31 - 1024 on are not
+ * visited (both latch SMLA_ERR_BAD_INDEX).  query_start_loc is trusted to increase from 0 to at most n_tokens.
  * Memory past a sequence's length is never used, whatever it holds; cached values within it must be
  * finite: on the tensor cores a NaN at a position that only some query tokens see reaches the others too.
  * Latents of 512 dims in tiles of 128 with 64 rope dims run on the tensor cores with

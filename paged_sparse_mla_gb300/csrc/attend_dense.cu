@@ -8,6 +8,7 @@
 //   out = sum_j e^(s_j - m) K_j / l,  lse = m + ln l            over the positions j that the token sees
 // in one pass over the keys: m and l are running values, and what is summed so far is multiplied by
 // e^(m_old - m_new) when m moves.  Exponentials are powers of two (the scale carries log2 e).
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -21,6 +22,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxHeads = 128;
+constexpr int kMaxContext = INT_MAX - 1023;  // a tile's rounding up and a range's start stay below 2^31 from there
 
 struct DenseArgs {
   KernelLayout L;
@@ -30,17 +32,17 @@ struct DenseArgs {
   const __nv_bfloat16 *q, *q_pe;
   const int32_t *block_table, *seq_lens, *qsl;
   int bt_stride, batch, n_tokens;
+  int most;  // positions of a sequence that are visited at most: those of its block-table row, kMaxContext at most
   __nv_bfloat16* out;
   float* lse;  // or nullptr
   unsigned* err;
 };
 
 // Positions that the i-th of n_q query tokens of a sequence of len positions sees: len - n_q + i + 1, at least
-// none and at most what the block-table row holds.
+// none and at most A.most.
 __device__ __forceinline__ int64_t visible(const DenseArgs& A, int len, int i, int n_q) {
   const int64_t n = static_cast<int64_t>(len) - n_q + i + 1;
-  const int64_t most = static_cast<int64_t>(A.bt_stride) * A.L.block_size;
-  return n < 0 ? 0 : n < most ? n : most;
+  return n < 0 ? 0 : n < A.most ? n : A.most;
 }
 
 // ---------------------------------------------------------------------------
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kSThreads) dense_fp32_kernel(const DenseArgs A
   const int b = seq_of_token(A.qsl, A.batch, t);
   const int q0 = __ldg(A.qsl + b), n_q = __ldg(A.qsl + b + 1) - q0;
   const int64_t n = visible(A, __ldg(A.seq_lens + b), t - q0, n_q);
-  if (threadIdx.x == 0 && __ldg(A.seq_lens + b) > static_cast<int64_t>(A.bt_stride) * L.block_size)
+  if (threadIdx.x == 0 && __ldg(A.seq_lens + b) > A.most)
     latch_error(A.err, SMLA_ERR_BAD_INDEX);
   for (int u = threadIdx.x; u < kSHeads * D; u += kSThreads) {
     const int h = h0 + u / D, d = u % D;
@@ -317,10 +319,9 @@ __device__ __forceinline__ int unit_tiles(const PairArgs& A, int len, int g, int
 // number where units are not split.
 __device__ int64_t work_before(const PairArgs& A, int len, int g, int n_q) {
   if (A.part_out == nullptr) return g;
-  const int64_t most = static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size;
   const int units = (n_q + A.group - 1) / A.group;
   if (units == 1) return g == 0 ? 0 : unit_tiles(A, len, 0, n_q);
-  if (len >= n_q && len <= most) {
+  if (len >= n_q && len <= A.D.most) {
     const int whole = min(g, units - 1);
     int64_t s = floor_sum(whole, kKeys, A.group, len - n_q + A.group + kKeys - 1);
     if (g == units) s += (len + kKeys - 1) / kKeys;
@@ -627,7 +628,7 @@ __device__ __forceinline__ void plan(const PairArgs& A, PairSmem& sm, int pair, 
       n_q = __ldg(A.D.qsl + b + 1) - q0;
       len = __ldg(A.D.seq_lens + b);
       if (n_q > 0) mine = work_before(A, len, (n_q + A.group - 1) / A.group, n_q);
-      if (blockIdx.x == 0 && n_q > 0 && len > static_cast<int64_t>(A.D.bt_stride) * A.D.L.block_size)
+      if (blockIdx.x == 0 && n_q > 0 && len > A.D.most)
         latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
     }
     int64_t incl = mine;
@@ -1559,6 +1560,7 @@ extern "C" smla_status_t smla_attend_dense(const smla_layout_t* layout, const sm
   A.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
   A.block_table = block_table;
   A.bt_stride = bt_stride;
+  A.most = static_cast<int>(std::min(static_cast<int64_t>(bt_stride) * L.block_size, static_cast<int64_t>(kMaxContext)));
   A.seq_lens = seq_lens;
   A.qsl = query_start_loc;
   A.batch = batch;

@@ -189,3 +189,35 @@ def test_records_beyond_2_gib_of_one_page(bs):
             assert ((out[t].double() - want).abs() <= bound).all()
             wl = total.log()[:, 0]
             assert ((lse[t].double() - wl).abs() <= ds[:, 0] + n / 128 * 2.0 ** -24 + 1e-5 * (1 + wl.abs())).all()
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("count", [1, 9])
+def test_the_longest_length_on_a_short_table(count, workspace):
+    """Every token sees what the row holds, four blocks of 64."""
+    c = Case([256], [count], 64, seed=57)
+    c.seq_lens[0] = 2 ** 31 - 1
+    out, lse = c.run(workspace)
+    assert smla.smla_get_last_error() == 4
+    q, q_pe, c.counts = c.q, c.q_pe, [1]
+    for t in range(count):
+        c.q, c.q_pe = q[t:t + 1], q_pe[t:t + 1]
+        wo, wl, bo, bl = c.want()
+        assert ((out[t:t + 1].double() - wo).abs() <= bo).all() and ((lse[t:t + 1].double() - wl).abs() <= bl).all()
+
+
+def test_positions_up_to_the_last_that_is_visited():
+    """A row of 513 pages of 2^22 tokens, all one page of zeros, and the longest length: 2^31 - 1024 positions count."""
+    bs = 1 << 22
+    lay = smla.layout_init(bs, 1, 512, 64, 128, 32, 1)
+    pool = torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(1, 513, dtype=torch.int32, device="cuda")
+    prm = smla.make_params(2, 1, 1, 1 / 24)
+    q, q_pe = torch.ones(1, 2, 512, dtype=torch.bfloat16, device="cuda"), torch.ones(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(smla.attend_dense_workspace_size(lay, prm, 1), dtype=torch.uint8, device="cuda")
+    lens, qsl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([2 ** 31 - 1], [0, 1]))
+    out, lse = torch.full_like(q, 7), torch.empty(1, 2, device="cuda")
+    smla.smla_attend_dense(lay, prm, pool, 0, q, q_pe, table, lens, qsl, out, lse, workspace=ws)
+    assert smla.smla_get_last_error() == 4
+    want = np.log(2.0 ** 31 - 1024)
+    assert (out == 0).all() and ((lse - want).abs() <= 1e-5 * (1 + want)).all()
