@@ -1341,7 +1341,7 @@ __device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, i
   float v[kMaxPairs / 32], mx = -INFINITY, z = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxPairs / 32; ++i) {
-    v[i] = 32 * i + lane < parts ? __ldg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
+    v[i] = 32 * i + lane < parts ? __ldcg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
     mx = fmaxf(mx, v[i]);
   }
 #pragma unroll
@@ -1374,7 +1374,7 @@ __device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, i
         if (i0 + i >= parts) f[i] = 0.f;
 #pragma unroll
         for (int y = 0; y < kQ; ++y)
-          a[i][y] = __ldg(reinterpret_cast<const float4*>(part_out + (slot(part) * kRows + row) * kDL + 128 * (q + y)) + lane);
+          a[i][y] = __ldcg(reinterpret_cast<const float4*>(part_out + (slot(part) * kRows + row) * kDL + 128 * (q + y)) + lane);
       }
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
@@ -1395,11 +1395,12 @@ __device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, i
   if (quarter0 == 0 && lane == 0 && lse != nullptr) lse[orow] = z == 0.f ? -INFINITY : mx + logf(z);
 }
 
-__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMeta* __restrict__ meta,
-                                                                    const float* __restrict__ part_lse,
-                                                                    const float* __restrict__ part_out, int n_pairs,
-                                                                    int n_heads, __nv_bfloat16* __restrict__ out,
-                                                                    float* __restrict__ lse) {
+// Starts while the pairs still write what it reads.  So the reads come after its wait for them, are ordinary ones
+// and not of the read-only path, which stands for data that no one writes while the kernel lives, and no pointer
+// is marked as free of aliases, so that none of them moves before the wait.
+__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMeta* meta, const float* part_lse,
+                                                                    const float* part_out, int n_pairs, int n_heads,
+                                                                    __nv_bfloat16* out, float* lse) {
   __shared__ int cum[kMaxPairs + 1];  // rows to join of the pairs before p
   static_assert(kMergeThreads == kMaxPairs, "a thread per pair");
   const int tid = threadIdx.x, warp = tid >> 5;

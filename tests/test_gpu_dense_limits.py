@@ -221,3 +221,24 @@ def test_positions_up_to_the_last_that_is_visited():
     assert smla.smla_get_last_error() == 4
     want = np.log(2.0 ** 31 - 1024)
     assert (out == 0).all() and ((lse - want).abs() <= 1e-5 * (1 + want)).all()
+
+
+def test_steps_in_a_row_share_a_workspace():
+    """Captured steps of other queries and lengths one after another on one workspace, as the layers of a model: each
+    joins its own parts, not those that the step before left at the same place."""
+    cases = [Case([5000 - 700 * i, 300], [1, 2], 64, seed=60 + i) for i in range(6)]
+    want = [c.run()[0] for c in cases]
+    ws = torch.empty(smla.attend_dense_workspace_size(cases[0].lay, cases[0].prm, 3), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for c, o in zip(cases, outs):
+            smla.smla_attend_dense(c.lay, c.prm, c.pool, 0, c.q, c.q_pe, c.table, c.seq_lens, c.qsl, o, workspace=ws)
+    for _ in range(30):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    ok()
