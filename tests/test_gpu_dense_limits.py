@@ -242,3 +242,31 @@ def test_steps_in_a_row_share_a_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     ok()
+
+
+def test_a_cache_of_small_latents():
+    """Relative accuracy where every tile's largest value is about the smallest documented one, 2^-14: the keys'
+    steps of 2^-25 are then 2^-11 of it.  Of smaller caches the sparse call over every position is exact to
+    bf16's roundings: 2^-8 each of the key, its weight, the sum of weights and the result."""
+    for scale, sparse in ((2.0 ** -14 / 0.3, False), (1e-9, True)):
+        c = Case([300], [1], 64, seed=58, key_scale=scale)
+        lat = torch.from_numpy(c.keys[0][0]).cuda()
+        tops = lat.view(300, 4, 128).abs().amax(-1)
+        assert sparse or float(tops.min()) >= 2.0 ** -14
+        if sparse:
+            prm = smla.make_params(64, 1, 512, c.sigma)
+            sel = torch.arange(512, dtype=torch.int32, device="cuda")[None].clone()
+            sel[:, 300:] = -1
+            out, lse = torch.empty(1, 64, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 64, device="cuda")
+            smla.smla_attend(c.lay, prm, c.pool, 0, c.q, c.q_pe, sel, c.table, c.qsl, out, lse)
+        else:
+            out, lse = c.run()
+        ok()
+        s = c.sigma * (c.q[0].double() @ lat.T + c.q_pe[0].double() @ torch.from_numpy(c.keys[0][1]).cuda().T)
+        p = torch.softmax(s, -1)
+        ds = c.sigma * (2.0 ** -8 if sparse else 2.0 ** -10) * (c.q[0].double().abs() @ lat.abs().T).amax(-1)[:, None]
+        ds = ds + (0 if sparse else c.sigma * 2.0 ** -25 * c.q[0].double().abs().sum(-1)[:, None])
+        size = p @ tops.repeat_interleave(128, 1)             # every error is relative to the tiles' largest values
+        want = p @ lat
+        bound = 2.0 ** -8 * want.abs() + size * ((3 * 2.0 ** -8 if sparse else 2.0 ** -10 + 2 * 2.0 ** -11) + 2 * ds) + 1e-5 * tops.max()
+        assert ((out[0].double() - want).abs() <= bound).all()
