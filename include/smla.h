@@ -440,9 +440,11 @@ typedef struct smla_rope {
  *   slot_mapping int64 [n_tokens], as kvpack_store: -1 = skip, a slot beyond the pool is
  *                skipped and latched; a token whose position is outside the table is too
  * Two tokens of one call must not share a slot.  Inputs must be finite, a normed row's
- * squares and their sum too.  The pool is 16-byte aligned, the inputs aligned to their element.  Built for the
- * latents that kvpack_store takes (64, 128, 256 or 512), d_rope <= 64 and d_index
- * of 32, 64, 128 or 256.
+ * squares and their sum too (in fp32; with eps 0 the sum must not vanish).  The pool is 16-byte
+ * aligned, the inputs aligned to their element.  Built for the latents that kvpack_store takes
+ * (64, 128, 256 or 512), d_rope <= 64 and d_index of 32, 64, 128 or 256.  The full shape (512 / 64 /
+ * 128, tiles of 128) with 16-byte aligned rows (strides a multiple of 8 elements), weights and
+ * table has a kernel of its own; other calls take about twice as long (15 us against 8, 8,192 tokens).
  */
 smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, int layer, const void* latent,
                             int64_t latent_stride, const void* rope_key, int64_t rope_stride, const void* idx_k,
@@ -470,7 +472,10 @@ smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, int layer, 
  *   q_idx_out uint8 [n_tokens, n_idx_heads, d_index], w_out fp32 [n_tokens, n_idx_heads]
  *   rope      NULL: nothing rotates (q_pe is copied)
  * A token whose position is outside the table latches SMLA_ERR_BAD_INDEX and its outputs
- * are left as they were.  Built for d_rope <= 64 and d_index of 32, 64, 128 or 256.
+ * are left as they were.  Inputs must be finite, and a normed row as for kvpack_append.  Built for
+ * d_rope <= 64 and d_index of 32, 64, 128 or 256.  64 rope and 128 indexer dims with 16-byte
+ * aligned rows (token and head strides a multiple of 8 elements), outputs, norm and table have a
+ * kernel of their own; other calls take four times as long (243 us against 59, 8,192 tokens of 64 + 64 heads).
  */
 smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* params, const smla_rope_t* rope,
                               const int64_t* positions, const void* q_pe, int64_t q_pe_token_stride,
