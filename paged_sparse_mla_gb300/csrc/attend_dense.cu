@@ -32,7 +32,9 @@ struct DenseArgs {
   const __nv_bfloat16 *q, *q_pe;
   const int32_t *block_table, *seq_lens, *qsl;
   int bt_stride, batch, n_tokens;
-  int most;  // positions of a sequence that are visited at most: those of its block-table row, kMaxContext at most
+  // Positions of a sequence that are visited at most: those of its block-table row, kMaxContext at most.  In 64 bits:
+  // compared in 32, the code around came out 1 % slower on a batch of short units (1,023 us against 1,011).
+  int64_t most;
   __nv_bfloat16* out;
   float* lse;  // or nullptr
   unsigned* err;
@@ -1561,7 +1563,7 @@ extern "C" smla_status_t smla_attend_dense(const smla_layout_t* layout, const sm
   A.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
   A.block_table = block_table;
   A.bt_stride = bt_stride;
-  A.most = static_cast<int>(std::min(static_cast<int64_t>(bt_stride) * L.block_size, static_cast<int64_t>(kMaxContext)));
+  A.most = std::min(static_cast<int64_t>(bt_stride) * L.block_size, static_cast<int64_t>(kMaxContext));
   A.seq_lens = seq_lens;
   A.qsl = query_start_loc;
   A.batch = batch;
