@@ -217,10 +217,11 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 // 1.2 us of MMA at full rate.  With loads that always hit L1 (a wrong answer) the cases below took 8 to
 // 18 % less, the largest share of any one part.  The second limit is the instruction cache, which five roles
 // share: one copy of every part of the loops took 5 to 7 % off.  Measured, 64 heads:
-//   2,048 query tokens at 20,480 positions   3.9 ms, 1.27 PFLOP/s (tensor pipe active half of the time)
-//   32 decode tokens, 8,192 to 32,768        187 us, 2.3 TB/s (half of a pair's rows are empty, and
+//   2,048 query tokens, 18,432 positions     3.96 ms, 1.25 PFLOP/s (tensor pipe active half of the time)
+//   32 decode tokens, 8,192 to 32,768        188 us, 2.3 TB/s (half of a pair's rows are empty, and
 //                                            DRAM's latency adds a sixth)
-//   64 x 4 drafted tokens, 4,096 to 32,768   640 us, 1.03 PFLOP/s
+//   64 x 4 drafted tokens, 4,096 to 32,768   646 us, 1.02 PFLOP/s
+//   5 ragged chunks on short contexts        1.01 ms, 0.73 PFLOP/s at 128 heads (the cut, see launch_dense_pair)
 //   one token at one position                15 us, the chain plan -> queries -> tile -> results -> merge
 // ---------------------------------------------------------------------------
 constexpr int kRows = 128, kKeys = 128;      // of a pair
@@ -1494,9 +1495,11 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.bs_mul = static_cast<uint32_t>((((1ull << log2) - D.L.block_size) << 32) / D.L.block_size + 1);
   A.bs_shift1 = log2 > 0 ? 1 : 0;
   A.bs_shift2 = log2 > 0 ? log2 - 1 : 0;
-  // Splitting pays wherever units are fewer or more uneven than pairs, and costs nothing measurable elsewhere:
-  // 32 decode tokens 188 us (598 without), one long sequence 95 us (4.7 ms), a chunk of 1,024 units 3.89 ms
-  // (4.17).  Without a workspace units stay whole.
+  // Splitting pays wherever units are fewer or more uneven than pairs: 32 decode tokens 188 us (598 without), one
+  // long sequence 95 us (4.7 ms), a chunk of 1,024 units 3.89 ms (4.17).  Without a workspace units stay whole.
+  // The ranges count tiles only, not the time between units (about four tiles' of each): where short contexts
+  // stand beside long ones, the pairs with the short ones' many units end last (8 to 70 units a pair in a ragged
+  // batch of contexts from 777 to 5,003).
   const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
   if (split) {
     uint8_t* w = static_cast<uint8_t*>(workspace);

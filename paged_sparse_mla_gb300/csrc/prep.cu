@@ -419,10 +419,11 @@ __device__ __forceinline__ float half_max8(const float (&x)[8]) {
 // latency.  Warp 0: the latent, 64 dims to eight lanes twice (dims 0-255, then the others), so that a
 // quantisation tile is a half-warp.  Warp 1: the indexer key in its first half-warp and the rope key in eight
 // lanes of the second.
-// 8,192 tokens (20 MB with their records) take 7.8 us with inputs in L2, 2.5 TB/s, launch included (the kernel
-// above, a warp per token with byte stores for the key: 15.2), one token 2.5 us (3.7): both are the chain
-// slot -> row -> sums -> codes and a launch, not bandwidth.  So as many warps as the SM holds: with 40
-// registers a thread instead of 32 a chunk from DRAM took 1.3 us more (1, 2 or 8 tokens a CTA: the same).
+// 8,192 tokens (20 MB with their records) take 8.0 us with inputs in L2, 2.5 TB/s, launch included (the kernel
+// above, a warp per token with byte stores for the key: 15.2), 11.5 us from DRAM, one token 2.7 us (3.7): the
+// chain slot -> row -> sums -> codes, a launch and, for the chunk, instructions (68 % of the issue slots), not
+// bandwidth.  So as many warps as the SM holds: with 40 registers a thread instead of 32 a chunk from DRAM took
+// 1.3 us more, one token 0.2 less (1, 2 or 8 tokens a CTA: the same).
 constexpr int kAppendTokens = 4;  // of a CTA
 template <bool kFp4>
 __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(const AppendArgs A) {
