@@ -19,6 +19,9 @@
  *                      codes and head weights, as smla_index_scores takes them
  *   smla_attend_dense  latent attention over the whole visible context (no
  *                      selection), decode tokens and prefill chunks
+ *   kvpack_load        cached positions back as bf16 rows
+ *   smla_step_tables   block tables, positions and slots of a step from the
+ *                      requests' lengths
  *
  * Sources (cited by page title and section):
  *   [AgentX]  "vLLM、エージェント型ワークロード向け最適化技術「AgentX」を公開"
@@ -81,7 +84,8 @@ typedef enum smla_status {
   SMLA_ERR_BAD_INDEX = 4,    /* device saw a block id / slot outside the pool (read clamped) */
   SMLA_ERR_TIMEOUT = 5,      /* a bounded on-device wait gave up            */
   SMLA_ERR_SCRATCH_LIMIT = 6,/* smla_decode_static: one query token's scratch exceeds the static array */
-  SMLA_ERR_RANGE = 7         /* smla_attend_dense saw a cached value beyond fp16's range */
+  SMLA_ERR_RANGE = 7,        /* smla_attend_dense saw a cached value beyond fp16's range */
+  SMLA_ERR_NO_BLOCKS = 8     /* smla_step_tables found the free list empty (the tokens' slots are -1) */
 } smla_status_t;
 
 /*
@@ -96,6 +100,22 @@ typedef enum smla_key_format {
   SMLA_KEY_E4M3 = 0,
   SMLA_KEY_E2M1 = 1
 } smla_key_format_t;
+
+/*
+ * Format of the cached latents.
+ *   SMLA_LATENT_E4M3: d_latent OCP FP8 E4M3 codes and an fp32 scale per quant_tile values.
+ *   SMLA_LATENT_E2M1: d_latent OCP MX FP4 E2M1 codes, two per byte (value 2i in the low
+ *     nibble of byte i), and one byte of scale per 16 values (quant_tile is 16): an unsigned
+ *     float of 5 exponent bits (bias 15) and 3 mantissa bits, the upper byte of an fp16 value
+ *     without its sign.  416 bytes a token for 512 + 64 dims instead of 656.  A writer rounds
+ *     scale = amax / 6 to nearest even, 10240 at most (0 where amax / 6 <= 2^-18), and
+ *     code = E2M1 round-to-nearest-even, saturating, of fp32(x / scale); code * scale is exact
+ *     in fp16 and bf16.  Scale bytes above 0xE2 (10240) are not written by this library.
+ */
+typedef enum smla_latent_format {
+  SMLA_LATENT_E4M3 = 0,
+  SMLA_LATENT_E2M1 = 1
+} smla_latent_format_t;
 
 /*
  * Packed block-pool layout ([AgentX "Hybrid KV cache management"]: all cache
@@ -122,7 +142,8 @@ typedef struct smla_layout {
   int32_t d_index;        /* indexer key dims (e4m3)                           */
   int64_t num_blocks;     /* pool capacity in blocks                           */
   int32_t n_scales;       /* d_latent / quant_tile                             */
-  int32_t rec_bytes;      /* d_latent + 4*n_scales + 2*d_rope                  */
+  int32_t rec_bytes;      /* d_latent + 4*n_scales + 2*d_rope; with E2M1 latents
+                             d_latent/2 + n_scales + 2*d_rope, by which they are told apart */
   int32_t rec_stride;     /* rec_bytes rounded up to 16                        */
   int32_t idx_key_format; /* smla_key_format_t of the cached indexer keys      */
   int64_t rec_off;        /* byte offset of the record region in a layer slice */
@@ -153,6 +174,16 @@ smla_status_t smla_layout_init(smla_layout_t* layout, int block_size, int n_laye
 smla_status_t smla_layout_init_keys(smla_layout_t* layout, int block_size, int n_layers, int d_latent,
                                     int d_rope, int quant_tile, int d_index, int key_format,
                                     int64_t num_blocks);
+
+/* smla_layout_init_keys with the format of the cached latents (an smla_latent_format_t).
+ * E2M1 latents need quant_tile 16.  Every call below takes either format; with E2M1 latents
+ * the pool is 16-byte aligned in all of them (SMLA_ERR_INVALID_ARG). */
+smla_status_t smla_layout_init_latents(smla_layout_t* layout, int block_size, int n_layers, int d_latent,
+                                       int d_rope, int quant_tile, int d_index, int key_format,
+                                       int latent_format, int64_t num_blocks);
+
+/* The smla_latent_format_t of a layout (told by its record size); -1 if no smla_layout_init made it. */
+int smla_layout_latent_format(const smla_layout_t* layout);
 
 /* Bytes of `workspace` that smla_decode needs for these sizes (scores + top-k
  * scratch, then the split-attention scratch of smla_attend_workspace_size,
@@ -530,6 +561,79 @@ smla_status_t smla_attend_dense(const smla_layout_t* layout, const smla_params_t
 /* Scratch bytes with which smla_attend_dense splits contexts over the SMs (partial outputs of two
  * ranges per pair of SMs); 0 for shapes and sizes that do not split. */
 size_t smla_attend_dense_workspace_size(const smla_layout_t* layout, const smla_params_t* params, int n_tokens);
+
+/*
+ * kvpack_load -- cached positions back as bf16 rows, one after another: the context of a
+ * prefill that multiplies the latents by the up-projections instead of absorbing them.
+ * Row r of sequence b, row_loc[b] <= r < row_loc[b + 1], is position starts[b] + r - row_loc[b]:
+ *   latent_out[r] = the position's dequantised latent, rounded to bf16 (exact for E2M1 latents)
+ *   rope_out[r]   = its rope values
+ *   block_table  int32 [batch, bt_stride] as in the attention calls
+ *   starts       int32 [batch], or NULL: from position 0 on
+ *   row_loc      int32 [batch + 1], increasing from 0 to at most n_rows (trusted); rows from
+ *                row_loc[batch] on are left as they were
+ *   latent_out   bf16 [n_rows, d_latent], rows latent_stride >= d_latent elements apart
+ *   rope_out     bf16 [n_rows, d_rope], rows rope_stride >= d_rope apart, or NULL; both may be
+ *                columns of one wider array
+ * A position outside the block-table row or a block id outside the pool latches
+ * SMLA_ERR_BAD_INDEX and its row is zeros.  The pool is 16-byte aligned.  512 + 64 dims (E4M3 latents in
+ * tiles of 128) with 16-byte aligned rows (strides a multiple of 8 elements) have a kernel of
+ * their own; other calls take a warp per row.
+ */
+smla_status_t kvpack_load(const smla_layout_t* layout, const void* pool, int layer, const int32_t* block_table,
+                          int bt_stride, const int32_t* starts, const int32_t* row_loc, int batch, int n_rows,
+                          void* latent_out, int64_t latent_stride, void* rope_out, int64_t rope_stride, void* stream);
+
+/*
+ * smla_step_tables -- a step's geometry and slots from the requests' lengths, on the device:
+ * what kvpack_append / kvpack_store (positions, slot_mapping) and the indexer and attention
+ * calls (block_table, seq_lens, query_start_loc) take.  [GLM-5.3 "Config and numbers"]: with
+ * drafted tokens (MTP3) the lengths follow from what the last step accepted, which the device
+ * knows first.  The requests live in rows of a persistent table; entry i of the step, 0 <= i <
+ * batch, is the request in row r = rows[i] (rows NULL: r = i) with new_lens[i] new tokens behind
+ * its lens[r] cached ones.
+ *   seq_lens[i]        = lens[r] + new_lens[i]
+ *   query_start_loc[i] = new_lens[0] + .. + new_lens[i - 1], and the total at [batch]
+ *   token k of entry i (arrays' index query_start_loc[i] + k): positions = lens[r] + k,
+ *                        slot_mapping = block * block_size + position % block_size
+ *   blocks             ceil(seq_lens[i] / block_size) of them; table[r][0 .. held[r]) are held
+ *                      already (more than the cached tokens fill where drafts were rejected; held
+ *                      counts at least the cached tokens' blocks), the others are taken from
+ *                      free_blocks[*free_used] on, in the order of entries and positions, and
+ *                      entered into table[r]
+ *   block_table[i][j]  = table[r][j] for the sequence's blocks; what follows is left as it was
+ *   held_out[r]        = the blocks row r then holds; *free_used_out = free blocks used by then
+ *   block_size and num_blocks of the layout are used
+ *   rows        int32 [batch] or NULL, distinct (trusted); below 0: an entry without a request,
+ *               no tokens and seq_lens 0
+ *   lens        int32 [n_rows], new_lens int32 [batch], held / held_out int32 [n_rows]
+ *   table       int32 [n_rows, table_stride]
+ *   free_blocks int32 [n_free]; free_used, free_used_out one int64 each
+ *   positions, slot_mapping  int64 [n_tokens]; behind the step's tokens (a step padded to a
+ *               captured size) position 0 and slot -1, which kvpack_append skips
+ *   block_table int32 [batch, bt_stride], apart from table; NULL without rows: table is the
+ *               batch's block table
+ *   workspace   smla_step_tables_workspace_size(batch) bytes, 16-byte aligned; its contents need
+ *               not be kept; calls that may overlap need one each, captured ones among them
+ * held_out may be held and free_used_out may be free_used (then a repeated call takes further
+ * blocks, as a captured step does); otherwise the call may be repeated.  lens is not changed: the
+ * caller adds what it accepts of a step.
+ * Lengths below 0 count as 0; tokens that pass a row's table_stride or bt_stride blocks, 2^31 - 1024
+ * positions or the arrays' n_tokens are not taken; each latches SMLA_ERR_BAD_INDEX, as do a row from n_rows on (an
+ * entry without a request then) and a block id outside the pool (slot -1).  Without a free block the
+ * table's entry is -1 and so are the slots; SMLA_ERR_NO_BLOCKS is latched, and held_out and
+ * free_used_out count what there was.
+ */
+smla_status_t smla_step_tables(const smla_layout_t* layout, const int32_t* rows, const int32_t* lens,
+                               const int32_t* new_lens, int batch, int32_t* table, int64_t n_rows, int table_stride,
+                               const int32_t* held, int32_t* held_out, const int32_t* free_blocks, int64_t n_free,
+                               const int64_t* free_used, int64_t* free_used_out, int n_tokens, int32_t* seq_lens,
+                               int32_t* query_start_loc, int64_t* positions, int64_t* slot_mapping,
+                               int32_t* block_table, int bt_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Scratch bytes of smla_step_tables (24 per entry). */
+size_t smla_step_tables_workspace_size(int batch);
 
 /* Self-check of the on-device wait bound and of the pipelined kernels' exit
  * protocol.  One CTA of four warps: warp 0 waits on an mbarrier that no thread

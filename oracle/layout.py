@@ -23,6 +23,12 @@ reading (FP4 indexer keys, [AgentX "Hybrid KV cache management"]): with
 byte (key_bytes = d_index / 2 instead of d_index), so the key region and with
 it the block shrink: 656 + 64 + 4 bytes per token instead of 656 + 128 + 4 for
 the DeepSeek shape.
+
+reading (4-bit latents): with ``latent_format="e2m1"`` a latent record is
+
+    [d_latent/2 bytes of E2M1 codes][d_latent/16 scale bytes][d_rope bf16][pad to 16 B]
+
+(416 bytes for d_latent=512, d_rope=64; ``oracle.latent4`` has the codec).
 """
 
 from dataclasses import dataclass
@@ -42,10 +48,13 @@ class PoolLayout:
     d_index: int
     num_blocks: int
     key_format: str = "e4m3"   # "e4m3": one byte per key element; "e2m1": two elements per byte
+    latent_format: str = "e4m3"   # likewise for the latents; "e2m1" has quant_tile 16
 
     def __post_init__(self):
         if self.key_format not in ("e4m3", "e2m1"):
             raise ValueError(f"unknown indexer key format {self.key_format!r}")
+        if self.latent_format not in ("e4m3", "e2m1") or (self.latent_format == "e2m1" and self.quant_tile != 16):
+            raise ValueError("latents are e4m3, or e2m1 in groups of 16")
         if self.key_format == "e2m1" and self.d_index % 2:
             raise ValueError("packed E2M1 keys need an even d_index")
 
@@ -58,8 +67,16 @@ class PoolLayout:
         return self.d_latent // self.quant_tile
 
     @property
+    def code_bytes(self) -> int:
+        return self.d_latent if self.latent_format == "e4m3" else self.d_latent // 2
+
+    @property
+    def scale_bytes(self) -> int:
+        return 4 * self.n_scales if self.latent_format == "e4m3" else self.n_scales
+
+    @property
     def rec_bytes(self) -> int:
-        return self.d_latent + 4 * self.n_scales + 2 * self.d_rope
+        return self.code_bytes + self.scale_bytes + 2 * self.d_rope
 
     @property
     def rec_stride(self) -> int:

@@ -23,6 +23,7 @@ correctly rounded p-bit result (no double-rounding error), and float64 has 53.
 import numpy as np
 
 from .fp4 import e2m1_decode, e2m1_unpack
+from .latent4 import latent4_decode, quantize_latent4
 from .fp8 import e4m3_decode, e4m3_encode, E4M3_MAX
 from .layout import PoolLayout
 
@@ -62,16 +63,19 @@ def kvpack_store(layout: PoolLayout, pool: np.ndarray, layer: int, latent_bits, 
     """Write new tokens' records into ``pool`` (uint8, modified in place)."""
     slots = np.asarray(slot_mapping, dtype=np.int64)
     keep = slots >= 0
-    codes, scales = quantize_latent(np.asarray(latent_bits)[keep], layout.quant_tile)
+    if layout.latent_format == "e2m1":
+        codes, scales = quantize_latent4(bf16_bits_to_f64(np.asarray(latent_bits)[keep]))
+    else:
+        codes, scales = quantize_latent(np.asarray(latent_bits)[keep], layout.quant_tile)
     rope = np.ascontiguousarray(np.asarray(rope_bits, dtype=np.uint16)[keep])
     idx_k = np.asarray(idx_k, dtype=np.uint8)[keep]
     idx_scale = np.ascontiguousarray(np.asarray(idx_scale, dtype=np.float32)[keep])
     slots = slots[keep]
-    d_l, n_s, d_r, d_i = layout.d_latent, layout.n_scales, layout.d_rope, layout.key_bytes
+    d_l, n_s, d_r, d_i = layout.code_bytes, layout.scale_bytes, layout.d_rope, layout.key_bytes
     rec = _offsets(layout, slots, layer, "record")[:, None]
     pool[rec + np.arange(d_l)] = codes
-    pool[rec + d_l + np.arange(4 * n_s)] = np.ascontiguousarray(scales).view(np.uint8).reshape(-1, 4 * n_s)
-    pool[rec + d_l + 4 * n_s + np.arange(2 * d_r)] = rope.view(np.uint8).reshape(slots.size, 2 * d_r)
+    pool[rec + d_l + np.arange(n_s)] = np.ascontiguousarray(scales).view(np.uint8).reshape(-1, n_s)
+    pool[rec + d_l + n_s + np.arange(2 * d_r)] = rope.view(np.uint8).reshape(slots.size, 2 * d_r)
     key = _offsets(layout, slots, layer, "key")[:, None]
     pool[key + np.arange(d_i)] = idx_k
     sc = _offsets(layout, slots, layer, "scale")[:, None]
@@ -82,6 +86,10 @@ def read_record(layout: PoolLayout, pool: np.ndarray, layer: int, slots):
     """Dequantised latent [n, D_L] (fp32 values held in float64) and rope [n, D_R] (float64)."""
     d_l, n_s, d_r = layout.d_latent, layout.n_scales, layout.d_rope
     rec = _offsets(layout, slots, layer, "record")[:, None]
+    if layout.latent_format == "e2m1":
+        lat = latent4_decode(pool[rec + np.arange(d_l // 2)], pool[rec + d_l // 2 + np.arange(n_s)])
+        rope_bits = np.ascontiguousarray(pool[rec + layout.code_bytes + n_s + np.arange(2 * d_r)]).reshape(-1).view(np.uint16)
+        return lat, bf16_bits_to_f64(rope_bits.reshape(-1, d_r) if d_r else np.zeros((lat.shape[0], 0), np.uint16))
     codes = pool[rec + np.arange(d_l)]
     scales = np.ascontiguousarray(pool[rec + d_l + np.arange(4 * n_s)]).view(np.float32)
     vals = e4m3_decode(codes).reshape(-1, n_s, layout.quant_tile) * scales.astype(np.float64)[:, :, None]

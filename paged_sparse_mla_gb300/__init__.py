@@ -22,7 +22,8 @@ __all__ = [
     "status_string", "version", "EXPORTED_SYMBOLS", "smla_decode_static", "smla_prefill_chunk",
     "smla_dcp_topk_merge", "smla_lse_merge", "smla_attend_hisparse", "smla_selftest_wait",
     "attend_workspace_size", "topk_workspace_size", "Rope", "make_rope", "kvpack_append", "smla_query_prep",
-    "smla_attend_dense", "attend_dense_workspace_size",
+    "smla_attend_dense", "attend_dense_workspace_size", "kvpack_load", "smla_step_tables", "step_tables_workspace_size",
+    "latent_format",
 ]
 
 EXPORTED_SYMBOLS = (
@@ -31,13 +32,16 @@ EXPORTED_SYMBOLS = (
     "smla_decode_static", "smla_prefill_chunk", "smla_dcp_topk_merge", "smla_lse_merge", "smla_attend_hisparse",
     "smla_selftest_wait", "smla_attend_workspace_size", "smla_topk_workspace_size", "smla_layout_init_keys",
     "kvpack_append", "smla_query_prep", "smla_attend_dense", "smla_attend_dense_workspace_size",
+    "smla_layout_init_latents", "smla_layout_latent_format", "kvpack_load", "smla_step_tables",
+    "smla_step_tables_workspace_size",
 )
 
 KEY_FORMATS = {"e4m3": 0, "e2m1": 1}  # smla_key_format_t
+LATENT_FORMATS = {"e4m3": 0, "e2m1": 1}  # smla_latent_format_t
 
 STATUS = {0: "SMLA_OK", 1: "SMLA_ERR_INVALID_ARG", 2: "SMLA_ERR_UNSUPPORTED", 3: "SMLA_ERR_CUDA",
           4: "SMLA_ERR_BAD_INDEX", 5: "SMLA_ERR_TIMEOUT", 6: "SMLA_ERR_SCRATCH_LIMIT",
-          7: "SMLA_ERR_RANGE"}
+          7: "SMLA_ERR_RANGE", 8: "SMLA_ERR_NO_BLOCKS"}
 
 
 class SmlaError(RuntimeError):
@@ -119,6 +123,12 @@ def lib() -> ctypes.CDLL:
             "smla_attend_dense": (_I, [LP, PP, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _P, ctypes.c_size_t,
                                        _P]),
             "smla_attend_dense_workspace_size": (ctypes.c_size_t, [LP, PP, _I]),
+            "smla_layout_init_latents": (_I, [LP, _I, _I, _I, _I, _I, _I, _I, _I, _I64]),
+            "smla_layout_latent_format": (_I, [LP]),
+            "kvpack_load": (_I, [LP, _P, _I, _P, _I, _P, _P, _I, _I, _P, _I64, _P, _I64, _P]),
+            "smla_step_tables": (_I, [LP, _P, _P, _P, _I, _P, _I64, _I, _P, _P, _P, _I64, _P, _P, _I, _P, _P, _P, _P, _P,
+                                      _I, _P, ctypes.c_size_t, _P]),
+            "smla_step_tables_workspace_size": (ctypes.c_size_t, [_I]),
             "smla_selftest_wait": (_I, [_I64, _P]),
             "smla_get_last_error": (_I, [_P]),
             "smla_status_string": (ctypes.c_char_p, [_I]),
@@ -211,10 +221,20 @@ def status_string(code: int) -> str:
     return lib().smla_status_string(code).decode()
 
 
-def layout_init(block_size, n_layers, d_latent, d_rope, quant_tile, d_index, num_blocks, key_format="e4m3") -> Layout:
-    """smla_layout_init (E4M3 indexer keys) or, with key_format="e2m1", smla_layout_init_keys (packed FP4 keys)."""
+def layout_init(block_size, n_layers, d_latent, d_rope, quant_tile, d_index, num_blocks, key_format="e4m3",
+                latent_format="e4m3") -> Layout:
+    """smla_layout_init (E4M3 indexer keys), with key_format="e2m1" smla_layout_init_keys (packed FP4 keys), or with
+    latent_format="e2m1" smla_layout_init_latents (latents in 4 bits; quant_tile is 16)."""
     lay = Layout()
-    if key_format == "e4m3":
+    if latent_format not in LATENT_FORMATS:
+        raise ValueError(f"unknown latent format {latent_format!r}")
+    if latent_format != "e4m3":
+        if key_format not in KEY_FORMATS:
+            raise ValueError(f"unknown indexer key format {key_format!r}")
+        _check(lib().smla_layout_init_latents(ctypes.byref(lay), block_size, n_layers, d_latent, d_rope, quant_tile, d_index,
+                                              KEY_FORMATS[key_format], LATENT_FORMATS[latent_format], num_blocks),
+               "smla_layout_init_latents")
+    elif key_format == "e4m3":
         _check(lib().smla_layout_init(ctypes.byref(lay), block_size, n_layers, d_latent, d_rope, quant_tile, d_index,
                                       num_blocks), "smla_layout_init")
     else:
@@ -223,6 +243,14 @@ def layout_init(block_size, n_layers, d_latent, d_rope, quant_tile, d_index, num
         _check(lib().smla_layout_init_keys(ctypes.byref(lay), block_size, n_layers, d_latent, d_rope, quant_tile,
                                            d_index, KEY_FORMATS[key_format], num_blocks), "smla_layout_init_keys")
     return lay
+
+
+def latent_format(layout: Layout) -> str:
+    """"e4m3" or "e2m1": the format of a layout's cached latents."""
+    code = lib().smla_layout_latent_format(ctypes.byref(layout))
+    if code < 0:
+        raise ValueError("not a layout that layout_init made")
+    return "e2m1" if code == LATENT_FORMATS["e2m1"] else "e4m3"
 
 
 def make_params(n_heads, n_idx_heads, top_k, softmax_scale) -> Params:
@@ -566,6 +594,61 @@ def smla_attend_dense(layout, params, pool, layer, q, q_pe, block_table, seq_len
     _check((_LIB or lib()).smla_attend_dense(ctypes.byref(layout), ctypes.byref(params), pl, layer, qa, pe, bt,
                                              block_table.shape[1], sl, qs, batch, T, oa, la, ws,
                                              0 if workspace is None else workspace.numel(), st), "smla_attend_dense")
+
+
+def kvpack_load(layout, pool, layer, block_table, row_loc, latent_out, rope_out=None, starts=None, stream=None):
+    """Positions starts[b] .. of each sequence (starts None: from 0 on) as bf16 rows row_loc[b] .. row_loc[b + 1] - 1 of
+    latent_out [n, d_latent] and rope_out [n, d_rope] (or None), whose rows may be any distance apart."""
+    n = latent_out.shape[0]
+    if row_loc.numel() < 2:
+        raise ValueError(f"row_loc: needs at least 2 elements, got shape {tuple(row_loc.shape)}")
+    batch = row_loc.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
+        raise ValueError(f"block_table: needs a row per sequence ({batch}), got shape {tuple(block_table.shape)}")
+    pl = _take(pool, _U8, "pool", layout.pool_bytes)
+    bt = _take(block_table, _I32, "block_table", 0)
+    rl = _take(row_loc, _I32, "row_loc", 2)
+    sa = _take(starts, _I32, "starts", batch)
+    lo, (ls,) = _take_rows(latent_out, "latent_out", (n, layout.d_latent))
+    if layout.d_rope == 0:
+        rope_out = None
+    ro, (rs,) = _take_rows(rope_out, "rope_out", (n, layout.d_rope))
+    if n == 1:  # the distance of a single row's rows is whatever it was sliced from, or left over
+        ls, rs = max(ls, layout.d_latent), max(rs, layout.d_rope)
+    st = _on_device((latent_out, pool, block_table, row_loc, starts, rope_out), stream)
+    _check((_LIB or lib()).kvpack_load(ctypes.byref(layout), pl, layer, bt, block_table.shape[1], sa, rl, batch, n, lo, ls, ro, rs, st),
+           "kvpack_load")
+
+
+def step_tables_workspace_size(batch) -> int:
+    return int(lib().smla_step_tables_workspace_size(batch))
+
+
+def smla_step_tables(layout, lens, new_lens, table, held, held_out, free_blocks, free_used, free_used_out, seq_lens,
+                     query_start_loc, positions, slot_mapping, rows=None, block_table=None, workspace=None, stream=None):
+    """Block tables, positions and slots of a step whose entry i adds new_lens[i] tokens to row rows[i] (None: row i) of
+    the persistent table [n_rows, blocks].  lens, held and held_out have an element per row, free_used and
+    free_used_out are int64 tensors of one element; workspace: uint8, step_tables_workspace_size(batch) bytes."""
+    batch = new_lens.numel()
+    if table.dim() != 2:
+        raise ValueError(f"table: expected 2 dimensions, got shape {tuple(table.shape)}")
+    n_rows, stride = table.shape
+    if block_table is not None and (block_table.dim() != 2 or block_table.shape[0] < batch):
+        raise ValueError(f"block_table: needs a row per entry ({batch}), got shape {tuple(block_table.shape)}")
+    if workspace is None or workspace.numel() < 24 * batch:
+        raise ValueError("workspace: needs step_tables_workspace_size(batch) bytes")
+    n = positions.numel()
+    args = (_take(rows, _I32, "rows", batch), _take(lens, _I32, "lens", n_rows), _take(new_lens, _I32, "new_lens", batch), batch,
+            _take(table, _I32, "table", 0), n_rows, stride, _take(held, _I32, "held", n_rows),
+            _take(held_out, _I32, "held_out", n_rows), _take(free_blocks, _I32, "free_blocks", 0), free_blocks.numel(),
+            _take(free_used, _I64T, "free_used", 1), _take(free_used_out, _I64T, "free_used_out", 1), n,
+            _take(seq_lens, _I32, "seq_lens", batch), _take(query_start_loc, _I32, "query_start_loc", batch + 1),
+            _take(positions, _I64T, "positions", n), _take(slot_mapping, _I64T, "slot_mapping", n),
+            _take(block_table, _I32, "block_table", 0), 0 if block_table is None else block_table.shape[1],
+            _take(workspace, _U8, "workspace", 0), workspace.numel())
+    st = _on_device((lens, rows, new_lens, table, held, held_out, free_blocks, free_used, free_used_out, seq_lens,
+                     query_start_loc, positions, slot_mapping, block_table, workspace), stream)
+    _check((_LIB or lib()).smla_step_tables(ctypes.byref(layout), *args, st), "smla_step_tables")
 
 
 def smla_selftest_wait(limit_ns, stream=None):

@@ -114,8 +114,8 @@ smla_status_t checked_device(unsigned** err) {
 bool layout_ok(const smla_layout_t* l) {
   if (l == nullptr) return false;
   smla_layout_t ref;
-  if (smla_layout_init_keys(&ref, l->block_size, l->n_layers, l->d_latent, l->d_rope, l->quant_tile, l->d_index,
-                            l->idx_key_format, l->num_blocks) != SMLA_OK)
+  if (smla_layout_init_latents(&ref, l->block_size, l->n_layers, l->d_latent, l->d_rope, l->quant_tile, l->d_index,
+                               l->idx_key_format, record_format(*l), l->num_blocks) != SMLA_OK)
     return false;
   return l->idx_key_format == ref.idx_key_format && l->n_scales == ref.n_scales && l->rec_bytes == ref.rec_bytes && l->rec_stride == ref.rec_stride &&
          l->rec_off == ref.rec_off && l->idx_key_off == ref.idx_key_off && l->idx_scale_off == ref.idx_scale_off &&
@@ -138,6 +138,7 @@ smla_status_t check_step(const StepArgs& a) {
       (!a.new_latent || !a.new_idx_k || !a.new_idx_scale || (layout->d_rope > 0 && !a.new_rope)))
     return SMLA_ERR_INVALID_ARG;
   const KernelLayout L = kernel_layout(*layout);
+  if (!pool_fits(L, a.pool)) return SMLA_ERR_INVALID_ARG;
   if ((a.slot_mapping != nullptr && !store_shape_supported(L)) || !index_shape_supported(L, params->n_idx_heads) ||
       !attend_shape_supported(L, params->n_heads))
     return SMLA_ERR_UNSUPPORTED;
@@ -162,6 +163,7 @@ const char* smla_status_string(smla_status_t s) {
     case SMLA_ERR_TIMEOUT: return "SMLA_ERR_TIMEOUT";
     case SMLA_ERR_SCRATCH_LIMIT: return "SMLA_ERR_SCRATCH_LIMIT";
     case SMLA_ERR_RANGE: return "SMLA_ERR_RANGE";
+    case SMLA_ERR_NO_BLOCKS: return "SMLA_ERR_NO_BLOCKS";
   }
   return "SMLA_ERR_UNKNOWN";
 }
@@ -174,6 +176,17 @@ smla_status_t smla_layout_init(smla_layout_t* l, int block_size, int n_layers, i
 
 smla_status_t smla_layout_init_keys(smla_layout_t* l, int block_size, int n_layers, int d_latent, int d_rope,
                                     int quant_tile, int d_index, int key_format, int64_t num_blocks) {
+  return smla_layout_init_latents(l, block_size, n_layers, d_latent, d_rope, quant_tile, d_index, key_format,
+                                  SMLA_LATENT_E4M3, num_blocks);
+}
+
+int smla_layout_latent_format(const smla_layout_t* layout) {
+  return layout_ok(layout) ? record_format(*layout) : -1;
+}
+
+smla_status_t smla_layout_init_latents(smla_layout_t* l, int block_size, int n_layers, int d_latent, int d_rope,
+                                       int quant_tile, int d_index, int key_format, int latent_format,
+                                       int64_t num_blocks) {
   if (l == nullptr || block_size <= 0 || n_layers <= 0 || d_latent <= 0 || d_rope < 0 || quant_tile <= 0 ||
       d_index <= 0 || num_blocks <= 0)
     return SMLA_ERR_INVALID_ARG;
@@ -181,6 +194,9 @@ smla_status_t smla_layout_init_keys(smla_layout_t* l, int block_size, int n_laye
     return SMLA_ERR_INVALID_ARG;
   if (key_format != SMLA_KEY_E4M3 && (key_format != SMLA_KEY_E2M1 || d_index % 32 != 0))
     return SMLA_ERR_INVALID_ARG;
+  if (latent_format != SMLA_LATENT_E4M3 && (latent_format != SMLA_LATENT_E2M1 || quant_tile != 16))
+    return SMLA_ERR_INVALID_ARG;
+  const bool four = latent_format == SMLA_LATENT_E2M1;
   const int e = d_latent / 32;  // latent elements per lane in the store
   if (quant_tile % e != 0 || (quant_tile / e) > 32 || ((quant_tile / e) & (quant_tile / e - 1)) != 0)
     return SMLA_ERR_INVALID_ARG;
@@ -194,7 +210,7 @@ smla_status_t smla_layout_init_keys(smla_layout_t* l, int block_size, int n_laye
   l->idx_key_format = key_format;
   l->num_blocks = num_blocks;
   l->n_scales = d_latent / quant_tile;
-  l->rec_bytes = d_latent + 4 * l->n_scales + 2 * d_rope;
+  l->rec_bytes = (four ? d_latent / 2 + l->n_scales : d_latent + 4 * l->n_scales) + 2 * d_rope;
   l->rec_stride = static_cast<int32_t>(round_up(l->rec_bytes, 16));
   l->rec_off = 0;
   l->idx_key_off = round_up(static_cast<int64_t>(block_size) * l->rec_stride, 256);
@@ -229,7 +245,8 @@ smla_status_t kvpack_store(const smla_layout_t* layout, void* pool, int layer, c
                            void* stream) {
   if (!layout_ok(layout) || n_tokens < 0 || layer < 0 || layer >= layout->n_layers) return SMLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return SMLA_OK;
-  if (!pool || !latent || !idx_k || !idx_scale || !slot_mapping || (layout->d_rope > 0 && !rope))
+  if (!pool || !latent || !idx_k || !idx_scale || !slot_mapping || (layout->d_rope > 0 && !rope) ||
+      !pool_fits(kernel_layout(*layout), pool))
     return SMLA_ERR_INVALID_ARG;
   DeviceInfo* d;
   smla_status_t st = check_device(&d);
@@ -287,7 +304,7 @@ smla_status_t smla_attend(const smla_layout_t* layout, const smla_params_t* para
     return SMLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return SMLA_OK;
   if (!pool || !q || (layout->d_rope > 0 && !q_pe) || !topk_idx || !block_table || !query_start_loc || !out || !lse ||
-      bt_stride <= 0)
+      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool))
     return SMLA_ERR_INVALID_ARG;
   DeviceInfo* d;
   smla_status_t st = check_device(&d);
@@ -307,7 +324,7 @@ smla_status_t smla_attend_hisparse(const smla_layout_t* layout, const smla_param
     return SMLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return SMLA_OK;
   if (!pool || !q || (layout->d_rope > 0 && !q_pe) || !topk_idx || !block_table || !query_start_loc || !out || !lse ||
-      bt_stride <= 0 || !host_block_map || (n_host_blocks > 0 && !host_records) ||
+      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool) || !host_block_map || (n_host_blocks > 0 && !host_records) ||
       (reinterpret_cast<uintptr_t>(host_records) & 15) != 0)
     return SMLA_ERR_INVALID_ARG;
   DeviceInfo* d;

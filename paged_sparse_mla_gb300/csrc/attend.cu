@@ -37,6 +37,7 @@
 //     lse = ln(sum) from the running max and the reduced row sums.
 #include <cstring>
 
+#include "latent4.cuh"
 #include "smla_internal.h"
 
 namespace smla {
@@ -224,12 +225,16 @@ __device__ __forceinline__ void rope_unit(int ur, int& key, int& v) {
   v = 4 * (w & 1) + (lane >> 3);
 }
 
+// How the producers read records: in 16-code pieces of any shape, or the full shape's records whole; E4M3 or E2M1 codes.
+constexpr int kPieces = 0, kRecords = 1, kPieces4 = 2, kRecords4 = 3;
+
 // Loads for one batch of the producer unit stream (see the key-tile loop):
-// latent units fetch 16 E4M3 codes and their fp32 scale, rope units fetch 8
+// latent units fetch 16 codes and their scale (E4M3: fp32; E2M1: two halves), rope units fetch 8
 // bf16 (zero padded past d_rope).  Masked keys (nullptr record) read as zero.
 constexpr int kBatch = 4;
+template <bool k4>
 __device__ __forceinline__ void load_units(const uint8_t* const* rec, int u0, int n_lat, int n_units, int parts,
-                                           int DL, int DR, int qtile, int n_scales, bool rope16,
+                                           int DL, int DR, int qtile, int rope_off, bool rope16,
                                            uint4 (&val)[kBatch], float (&sc)[kBatch]) {
 #pragma unroll
   for (int b = 0; b < kBatch; ++b) {
@@ -241,15 +246,21 @@ __device__ __forceinline__ void load_units(const uint8_t* const* rec, int u0, in
       latent_unit(u, parts, key, part);
       const uint8_t* r = rec[key];
       if (r != nullptr) {
-        val[b] = __ldg(reinterpret_cast<const uint4*>(r) + part);
-        sc[b] = __ldg(reinterpret_cast<const float*>(r + DL) + (part * 16) / qtile);
+        if constexpr (k4) {
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(r) + part);
+          val[b] = make_uint4(c.x, c.y, 0, 0);
+          sc[b] = __uint_as_float(scale4_half2(__ldg(r + DL / 2 + part)));
+        } else {
+          val[b] = __ldg(reinterpret_cast<const uint4*>(r) + part);
+          sc[b] = __ldg(reinterpret_cast<const float*>(r + DL) + (part * 16) / qtile);
+        }
       }
     } else if (u < n_units) {
       int key, v;
       rope_unit(u - n_lat, key, v);
       const uint8_t* r = rec[key];
       if (r != nullptr && v * 8 < DR) {
-        const uint8_t* src = r + DL + 4 * n_scales + v * 16;
+        const uint8_t* src = r + rope_off + v * 16;
         if (rope16 && v * 8 + 8 <= DR)
           val[b] = __ldg(reinterpret_cast<const uint4*>(src));
         else
@@ -312,7 +323,7 @@ __device__ __forceinline__ int row_tiles(const int32_t* row, int k, int lane) {
   return (last + kTile) / kTile;
 }
 
-template <int NCH, bool WR, int MODE>
+template <int NCH, int kGather, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap qpe_map) {
@@ -327,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const KernelLayout& L = A.L;
   constexpr int DL = (NCH - 1) * 64;  // latent dims (8 chunks of 64 for 512)
   constexpr int kDTiles = (DL + 127) / 128;
+  constexpr bool k4 = kGather >= kPieces4;
   const int DR = L.d_rope;
 
   if (threadIdx.x == 0) {
@@ -362,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, nw = 0, kk = 0;
     uint32_t q_issued = 0;  // query-tile copies issued by this thread (ptid 0 on the copy path)
     constexpr int parts = DL / 16;       // 16-code parts per record
-    const bool rope16 = ((DL + 4 * L.n_scales) % 16) == 0;
-    // WR: 512 latent codes, four per-128 scales and 64 rope values = 41 aligned 16-byte pieces
-    constexpr bool whole_records = WR;
+    const bool rope16 = (L.rope_off % 16) == 0;
+    // 512 latent codes, four per-128 scales and 64 rope values = 41 aligned 16-byte pieces
+    constexpr bool whole_records = kGather == kRecords;
     // A failed wait never makes one warp leave alone: the thread carries on to the next
     // group barrier (what it writes meanwhile is discarded), where the failure is ORed in
     // (bar.red), so that every producer warp leaves the loop together and none is left
@@ -534,14 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // first batch of loads is issued before waiting for the tile buffer
         uint4 cur[kBatch];
         float csc[kBatch];
-        load_units(rec, ptid, n_lat, n_units, parts, DL, DR, L.quant_tile, L.n_scales, rope16, cur, csc);
+        load_units<k4>(rec, ptid, n_lat, n_units, parts, DL, DR, L.quant_tile, L.rope_off, rope16, cur, csc);
         ok = mbar_wait(&sm.kv_empty[kb], ((kk >> 1) & 1) ^ 1, A.err, abort);
         for (int base = 0; base < n_units; base += kBatch * kProducerThreads) {
           uint4 nxt[kBatch];
           float nsc[kBatch];
           const int nbase = base + kBatch * kProducerThreads;
           if (nbase < n_units)
-            load_units(rec, nbase + ptid, n_lat, n_units, parts, DL, DR, L.quant_tile, L.n_scales, rope16, nxt, nsc);
+            load_units<k4>(rec, nbase + ptid, n_lat, n_units, parts, DL, DR, L.quant_tile, L.rope_off, rope16, nxt, nsc);
           if (base == 0) blk_ahead = block_of(j_ahead);
 #pragma unroll
           for (int bb = 0; bb < kBatch; ++bb) {
@@ -551,7 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               int r, part;
               latent_unit(u, parts, r, part);
               uint4 o0, o1;
-              dequant16(cur[bb], csc[bb], o0, o1);
+              if constexpr (k4) {
+                o0 = dequant4x8_bf16(cur[bb].x, __float_as_uint(csc[bb]));
+                o1 = dequant4x8_bf16(cur[bb].y, __float_as_uint(csc[bb]));
+              } else {
+                dequant16(cur[bb], csc[bb], o0, o1);
+              }
               const int d0 = part * 16;
               const int c = d0 / 64, v0 = (d0 % 64) / 8;
               *reinterpret_cast<uint4*>(&sm.kv[kb][c][sw128_off(r, v0)]) = o0;
@@ -821,7 +838,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p0 = fast_exp2(sc[hx] - (m0 == -INFINITY ? 0.f : m0));
             const float p1 = fast_exp2(sc[hx + 1] - (m1 == -INFINITY ? 0.f : m1));
             const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            const float2 pf = __bfloat1622float2(pb);
+            // E4M3: the sum of the rounded weights, as they are multiplied.  E2M1 keys are exact, so that the rounding
+            // of the weights (2^-9 each) would be all that is off in the lse: they are summed before it.
+            const float2 pf = k4 ? make_float2(p0, p1) : __bfloat1622float2(pb);
             l_part[hx] += pf.x;
             l_part[hx + 1] += pf.y;
             pw[hx / 2] = (static_cast<uint32_t>(__bfloat16_as_ushort(pb.y)) << 16) | __bfloat16_as_ushort(pb.x);
@@ -1005,26 +1024,26 @@ __global__ void __launch_bounds__(256) balanced_merge_kernel(const float* __rest
   if (lane == 0) lse[r * n_heads + h] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
-template <int NCH, bool WR>
+template <int NCH, int kGather>
 smla_status_t launch_nch(AttnArgs A, cudaStream_t stream) {
   const size_t smem = sizeof(AttnSmem<NCH>) + 1024;
   static std::atomic<bool> attr_set[kMaxDeviceSlots] = {};
   const int dev = current_device_index();
   if (dev < 0) return SMLA_ERR_CUDA;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(attend_kernel<NCH, WR, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attend_kernel<NCH, kGather, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(attend_kernel<NCH, WR, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(attend_kernel<NCH, kGather, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(attend_kernel<NCH, WR, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(attend_kernel<NCH, kGather, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return SMLA_ERR_CUDA;
     // setmaxnreg.inc can only draw on the registers the CTA was launched with;
     // refuse to launch if the compiled allocation does not cover the split.
     cudaFuncAttributes fa, fs, fb;
-    if (cudaFuncGetAttributes(&fa, attend_kernel<NCH, WR, 0>) != cudaSuccess ||
-        cudaFuncGetAttributes(&fs, attend_kernel<NCH, WR, 1>) != cudaSuccess ||
-        cudaFuncGetAttributes(&fb, attend_kernel<NCH, WR, 2>) != cudaSuccess)
+    if (cudaFuncGetAttributes(&fa, attend_kernel<NCH, kGather, 0>) != cudaSuccess ||
+        cudaFuncGetAttributes(&fs, attend_kernel<NCH, kGather, 1>) != cudaSuccess ||
+        cudaFuncGetAttributes(&fb, attend_kernel<NCH, kGather, 2>) != cudaSuccess)
       return SMLA_ERR_CUDA;
     if (fa.numRegs < kLaunchRegs || fs.numRegs < kLaunchRegs || fb.numRegs < kLaunchRegs) return SMLA_ERR_UNSUPPORTED;
     attr_set[dev].store(true, std::memory_order_release);
@@ -1058,11 +1077,11 @@ smla_status_t launch_nch(AttnArgs A, cudaStream_t stream) {
   const int sms = device_sm_count();
   const int grid = A.mode == 2 ? sms : min(A.n_rows * A.n_splits, sms);
   if (A.mode == 1)
-    attend_kernel<NCH, WR, 1><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
+    attend_kernel<NCH, kGather, 1><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
   else if (A.mode == 2)
-    attend_kernel<NCH, WR, 2><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
+    attend_kernel<NCH, kGather, 2><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
   else
-    attend_kernel<NCH, WR, 0><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
+    attend_kernel<NCH, kGather, 0><<<grid, kThreads, smem, stream>>>(A, q_map, qpe_map);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   if (A.mode == 2) {
     balanced_merge_kernel<(NCH - 1) * 64><<<dim3(grid - 1, (A.n_heads + 7) / 8), 256, 0, stream>>>(
@@ -1149,11 +1168,12 @@ smla_status_t launch_attend(const KernelLayout& L, int n_heads, int top_k, float
                                                     split_out_bytes(n_heads, L.d_latent, parts))
                          : nullptr;
   switch (L.d_latent / 64) {
-    case 1: return launch_nch<2, false>(A, stream);
+    case 1: return latent4(L) ? launch_nch<2, kPieces4>(A, stream) : launch_nch<2, kPieces>(A, stream);
     case 8: {
+      if (latent4(L)) return launch_nch<9, kPieces4>(A, stream);
       // records of 512 codes, four per-128 scales and 64 rope values take the whole-record gather
       const bool wr = L.n_scales == 4 && L.quant_tile == 128 && L.d_rope == 64 && (512 + 4 * L.n_scales) % 16 == 0;
-      return wr ? launch_nch<9, true>(A, stream) : launch_nch<9, false>(A, stream);
+      return wr ? launch_nch<9, kRecords>(A, stream) : launch_nch<9, kPieces>(A, stream);
     }
     default: return SMLA_ERR_UNSUPPORTED;
   }

@@ -14,6 +14,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "latent4.cuh"
 #include "smla_internal.h"
 
 namespace smla {
@@ -100,12 +101,15 @@ __global__ void __launch_bounds__(kSThreads) dense_fp32_kernel(const DenseArgs A
       for (int d = lane; d < D; d += 32) {
         float v = 0.f;
         if (rec != nullptr) {
-          if (d < DL) {
+          if (d < DL && L.latent_format == SMLA_LATENT_E2M1) {
+            v = latent4_value(rec, d, DL);
+            if (rec[DL / 2 + d / kGroup4] > kScale4Top) latch_error(A.err, SMLA_ERR_RANGE);
+          } else if (d < DL) {
             const __half_raw hr = __nv_cvt_fp8_to_halfraw(rec[d], __NV_E4M3);
             v = __half2float(*reinterpret_cast<const __half*>(&hr)) *
                 reinterpret_cast<const float*>(rec + DL)[d / L.quant_tile];
           } else {
-            v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec + DL + 4 * L.n_scales)[d - DL]);
+            v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec + L.rope_off)[d - DL]);
           }
         }
         k[i * DP + d] = v;

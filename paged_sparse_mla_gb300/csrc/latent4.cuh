@@ -1,0 +1,115 @@
+// Latents in 4 bits: E2M1 codes ([OCP-MX]: sign, two exponent bits, one mantissa bit) and a scale for every 16.
+//
+// A scale is an unsigned 8-bit float, 5 bits of exponent (bias 15) and 3 of mantissa: the upper byte of an fp16
+// value without its sign, so that one shift turns it into fp16.  Why this one: a code has two significant bits
+// and a scale four, so that their product is exact in fp16 and in bf16 (six bits), and from 0.5 x 2^-17 to
+// 6 x 10240 it lies inside fp16's range.  The cached values therefore enter the tensor cores unrounded, no
+// per-tensor scale has to be calibrated, and no value of the cache has to be looked at before it is used but the
+// scale bytes that nothing here writes (above kScale4Top: an infinite or NaN scale, or a product past fp16's end).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+
+#include "smla_device.cuh"
+
+namespace smla {
+
+constexpr int kGroup4 = 16;              // latent values that share a scale
+constexpr uint32_t kScale4Top = 0xE2;    // 10240, the largest scale s with 6 s inside fp16's range
+
+__device__ __forceinline__ float scale4_value(uint32_t code) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(code << 7)));
+}
+// The scale twice, as fp16.
+__device__ __forceinline__ uint32_t scale4_half2(uint32_t code) { return code * 0x00800080u; }
+
+// amax / 6 rounded to nearest even: on the float's bits (20 of its 23 mantissa bits go), or as a multiple of the
+// smallest scale below the smallest normal one, 2^-14.
+__device__ __forceinline__ uint32_t scale4_code(float amax) {
+  const float s = __fdiv_rn(amax, 6.0f);
+  const uint32_t u = __float_as_uint(s);
+  const uint32_t normal = ((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
+  const uint32_t sub = static_cast<uint32_t>(__float2int_rn(s * 131072.0f));
+  return min(s < 6.103515625e-5f ? sub : normal, kScale4Top);
+}
+
+// E2M1 codes of N values of a group with scale s, packed, element 2 i in the low half of byte i: round to nearest even
+// of the fp32 quotient, saturating.  The quotient by the reciprocal is corrected once by its exact remainder, so that
+// one that lies between two codes (frequent: bf16 values over scales of four bits) is met exactly.
+template <int N>
+__device__ __forceinline__ void quantise4(const float (&x)[N], float s, uint8_t (&bytes)[N / 2]) {
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  float q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float q0 = x[i] * r;
+    q[i] = fmaf(fmaf(-q0, s, x[i]), r, q0);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    bytes[i] = __nv_cvt_float2_to_fp4x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_E2M1, cudaRoundNearest);
+}
+
+// N values that a lane holds side by side (2, 4, 8 or 16: 16 / N lanes hold a group) into the record at `rec`.
+template <int N>
+__device__ __forceinline__ void store_latent4(const float (&x)[N], uint8_t* rec, int d_latent, int lane) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+  for (int m = 1; m < kGroup4 / N; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  const uint32_t code = scale4_code(amax);
+  uint8_t b[N / 2];
+  quantise4(x, scale4_value(code), b);
+  uint8_t* dst = rec + lane * (N / 2);  // a multiple of N / 2 bytes: records and codes begin on 16
+  if constexpr (N == 16)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | static_cast<uint32_t>(b[3]) << 24,
+                                                b[4] | b[5] << 8 | b[6] << 16 | static_cast<uint32_t>(b[7]) << 24);
+  else if constexpr (N == 8)
+    *reinterpret_cast<uint32_t*>(dst) = b[0] | b[1] << 8 | b[2] << 16 | static_cast<uint32_t>(b[3]) << 24;
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(b[0] | b[1] << 8);
+  else
+    *dst = b[0];
+  if ((lane * N) % kGroup4 == 0) rec[d_latent / 2 + lane * N / kGroup4] = static_cast<uint8_t>(code);
+}
+
+// Two packed codes (the low byte of `byte`) as fp16.
+__device__ __forceinline__ uint32_t e2m1x2_half2(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight codes times a scale (two halves) as fp16: exact.
+__device__ __forceinline__ uint4 dequant4x8(uint32_t codes, uint32_t sc) {
+  uint32_t o[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t h = e2m1x2_half2(codes >> (8 * x));
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&sc));
+    o[x] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// The same as bf16.
+__device__ __forceinline__ uint4 dequant4x8_bf16(uint32_t codes, uint32_t sc) {
+  const uint4 h = dequant4x8(codes, sc);
+  const uint32_t hs[4] = {h.x, h.y, h.z, h.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hs[x]));
+    o[x] = pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Latent value d of a record, in fp32.
+__device__ __forceinline__ float latent4_value(const uint8_t* rec, int d, int d_latent) {
+  const uint32_t h = e2m1x2_half2(rec[d >> 1]);
+  const unsigned short bits = static_cast<unsigned short>((d & 1) ? h >> 16 : h & 0xFFFFu);
+  return __half2float(__ushort_as_half(bits)) * scale4_value(rec[d_latent / 2 + d / kGroup4]);
+}
+
+}  // namespace smla

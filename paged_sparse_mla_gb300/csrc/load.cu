@@ -1,0 +1,175 @@
+// kvpack_load: cached positions back as bf16 rows.
+//
+// A prefill that does not absorb the up-projections multiplies the cached latents by them first, and for that
+// wants the context of its sequences as rows one after another.  [AgentX "Hybrid KV cache management"]: the
+// records lie in pages of one shared pool; [GLM-5.3 "How to try"]: quantised.
+//   latent_out[r] = code scale (rounded to bf16; exact for E2M1 latents),  rope_out[r] = rope
+// with row r = row_loc[b] + i the record of position starts[b] + i.
+#include "latent4.cuh"
+#include "smla_internal.h"
+
+namespace smla {
+namespace {
+
+struct LoadArgs {
+  KernelLayout L;
+  const uint8_t* records;  // the layer's records in block 0
+  const int32_t *block_table, *starts, *row_loc;
+  int bt_stride, batch, n_rows;
+  int64_t max_pos;
+  __nv_bfloat16 *latent, *rope;
+  int64_t latent_stride, rope_stride;
+  unsigned* err;
+};
+
+// Record of output row r; nullptr (zeros) where the block table has none.
+__device__ __forceinline__ const uint8_t* record_of_row(const LoadArgs& A, int r) {
+  const int b = seq_of_token(A.row_loc, A.batch, r);
+  const int64_t j = (A.starts != nullptr ? __ldg(A.starts + b) : 0) + static_cast<int64_t>(r) - __ldg(A.row_loc + b);
+  if (j >= 0 && j < A.max_pos) {
+    const int64_t page = j / A.L.block_size;
+    const int blk = __ldg(A.block_table + static_cast<int64_t>(b) * A.bt_stride + page);
+    if (blk >= 0 && blk < A.L.num_blocks)
+      return A.records + blk * A.L.block_stride + (j - page * A.L.block_size) * A.L.rec_stride;
+  }
+  latch_error(A.err, SMLA_ERR_BAD_INDEX);
+  return nullptr;
+}
+
+constexpr int kWarps = 8;
+
+// Any shape and alignment: a warp per row.
+__global__ void __launch_bounds__(32 * kWarps) load_kernel(const LoadArgs A) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (row >= A.n_rows || row >= __ldg(A.row_loc + A.batch)) return;
+  const KernelLayout& L = A.L;
+  const uint8_t* rec = nullptr;
+  if (lane == 0) rec = record_of_row(A, static_cast<int>(row));
+  rec = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(rec), 0));
+  for (int d = lane; d < L.d_latent; d += 32) {
+    float v = 0.f;
+    if (rec != nullptr) {
+      if (L.latent_format == SMLA_LATENT_E2M1) {
+        v = latent4_value(rec, d, L.d_latent);
+      } else {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(rec[d], __NV_E4M3);
+        v = __half2float(*reinterpret_cast<const __half*>(&h)) * reinterpret_cast<const float*>(rec + L.d_latent)[d / L.quant_tile];
+      }
+    }
+    A.latent[row * A.latent_stride + d] = __float2bfloat16_rn(v);
+  }
+  if (A.rope != nullptr) {
+    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(rec + L.rope_off);
+    for (int d = lane; d < L.d_rope; d += 32) A.rope[row * A.rope_stride + d] = rec != nullptr ? src[d] : __float2bfloat16_rn(0.f);
+  }
+}
+
+// 512 latent dims (E4M3 in tiles of 128) and 64 rope dims, outputs in 16-byte pieces.  A warp takes four rows: a lane
+// converts dims 8 lane .. + 7 and 256 + 8 lane .. + 7 of each, so that codes are read and values written in whole
+// lines, and 16 bytes of one row's rope; all loads of the four rows are in flight at once.
+constexpr int kRowsPerWarp = 4;
+template <bool kLatent4>
+__global__ void __launch_bounds__(32 * kWarps) load_full_kernel(const LoadArgs A) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRowsPerWarp;
+  const int end = min(A.n_rows, __ldg(A.row_loc + A.batch));
+  if (row0 >= end) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kRowsPerWarp), end - row0));
+  const uint8_t* at = nullptr;
+  if (lane < n) at = record_of_row(A, static_cast<int>(row0) + lane);
+  const auto rec = [&](int i) {
+    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), i));
+  };
+  uint2 codes[kRowsPerWarp][2];
+  uint32_t sc[kRowsPerWarp][2];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    const uint8_t* r = rec(i);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      codes[i][h] = make_uint2(0, 0);
+      sc[i][h] = 0;
+      if (r == nullptr) continue;
+      if constexpr (kLatent4) {
+        codes[i][h].x = __ldg(reinterpret_cast<const uint32_t*>(r + 128 * h) + lane);
+        sc[i][h] = __ldg(r + 256 + 16 * h + (lane >> 1));
+      } else {
+        codes[i][h] = __ldg(reinterpret_cast<const uint2*>(r + 256 * h) + lane);
+        sc[i][h] = __ldg(reinterpret_cast<const uint32_t*>(r + 512) + 2 * h + (lane >> 4));
+      }
+    }
+  }
+  const int pi = lane >> 3;  // the row whose rope this lane copies
+  uint4 pe = make_uint4(0, 0, 0, 0);
+  const uint8_t* rp = rec(pi);
+  if (A.rope != nullptr && rp != nullptr) pe = __ldg(reinterpret_cast<const uint4*>(rp + (kLatent4 ? 288 : 528)) + (lane & 7));
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (i >= n) break;
+    uint4* dst = reinterpret_cast<uint4*>(A.latent + (row0 + i) * A.latent_stride) + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 v;
+      if constexpr (kLatent4) {
+        v = dequant4x8_bf16(codes[i][h].x, scale4_half2(sc[i][h]));
+      } else {
+        const float s = __uint_as_float(sc[i][h]);
+        uint32_t o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t w = x < 2 ? codes[i][h].x : codes[i][h].y;
+          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (x & 1))), __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+          o[x] = pack_bf16x2(f.x * s, f.y * s);
+        }
+        v = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      dst[32 * h] = v;
+    }
+  }
+  if (A.rope != nullptr && pi < n) reinterpret_cast<uint4*>(A.rope + (row0 + pi) * A.rope_stride)[lane & 7] = pe;
+}
+
+}  // namespace
+}  // namespace smla
+
+using namespace smla;
+
+extern "C" smla_status_t kvpack_load(const smla_layout_t* layout, const void* pool, int layer, const int32_t* block_table,
+                                     int bt_stride, const int32_t* starts, const int32_t* row_loc, int batch, int n_rows,
+                                     void* latent_out, int64_t latent_stride, void* rope_out, int64_t rope_stride, void* stream) {
+  if (!layout_ok(layout) || layer < 0 || layer >= layout->n_layers || batch <= 0 || n_rows < 0) return SMLA_ERR_INVALID_ARG;
+  if (n_rows == 0) return SMLA_OK;
+  if (!pool || (reinterpret_cast<uintptr_t>(pool) & 15) != 0 || !block_table || bt_stride <= 0 || !row_loc || !latent_out ||
+      latent_stride < layout->d_latent || (rope_out && rope_stride < layout->d_rope))
+    return SMLA_ERR_INVALID_ARG;
+  LoadArgs A{};
+  const smla_status_t st = checked_device(&A.err);
+  if (st != SMLA_OK) return st;
+  A.L = kernel_layout(*layout);
+  A.records = static_cast<const uint8_t*>(pool) + static_cast<int64_t>(layer) * A.L.layer_stride + A.L.rec_off;
+  A.block_table = block_table;
+  A.starts = starts;
+  A.row_loc = row_loc;
+  A.bt_stride = bt_stride;
+  A.batch = batch;
+  A.n_rows = n_rows;
+  A.max_pos = static_cast<int64_t>(bt_stride) * A.L.block_size;
+  A.latent = static_cast<__nv_bfloat16*>(latent_out);
+  A.rope = A.L.d_rope > 0 ? static_cast<__nv_bfloat16*>(rope_out) : nullptr;
+  A.latent_stride = latent_stride;
+  A.rope_stride = rope_stride;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const auto pieces = [](const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
+  if (A.L.d_latent == 512 && (latent4(A.L) || A.L.quant_tile == 128) && A.L.d_rope == 64 && pieces(latent_out, latent_stride) &&
+      (A.rope == nullptr || pieces(rope_out, rope_stride))) {
+    const int per = kWarps * kRowsPerWarp;
+    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n_rows) + per - 1) / per);
+    if (latent4(A.L)) load_full_kernel<true><<<blocks, 32 * kWarps, 0, s>>>(A);
+    else load_full_kernel<false><<<blocks, 32 * kWarps, 0, s>>>(A);
+  } else {
+    load_kernel<<<static_cast<unsigned>((static_cast<int64_t>(n_rows) + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(A);
+  }
+  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}

@@ -10,6 +10,7 @@
 // quantised: that rounding (2^-8) would only add to the code's (2^-4).
 #include <cuda_fp4.h>
 
+#include "latent4.cuh"
 #include "smla_internal.h"
 
 namespace smla {
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
       r1 = r0 * s + r1 * c;
       r0 = y0;
     }
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(rec + L.d_latent + 4 * L.n_scales);
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(rec + L.rope_off);
     dst[ra] = __float2bfloat16_rn(r0);
     dst[rb] = __float2bfloat16_rn(r1);
   }
@@ -190,6 +191,9 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = x[i] * rstd * __ldg(A.latent_norm + lane * E + i);
   }
+  if (L.latent_format == SMLA_LATENT_E2M1) {
+    store_latent4(x, rec, L.d_latent, lane);
+  } else {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendArgs A)
     else reinterpret_cast<uint32_t*>(rec)[lane] = w[0];
   }
   if ((lane * E) % L.quant_tile == 0) reinterpret_cast<float*>(rec + L.d_latent)[(lane * E) / L.quant_tile] = scale;
+  }
 
   // ---- indexer key ----
   if (A.idx_k == nullptr) return;
@@ -425,7 +430,7 @@ __device__ __forceinline__ float half_max8(const float (&x)[8]) {
 // bandwidth.  So as many warps as the SM holds: with 40 registers a thread instead of 32 a chunk from DRAM took
 // 1.3 us more, one token 0.2 less (1, 2 or 8 tokens a CTA: the same).
 constexpr int kAppendTokens = 4;  // of a CTA
-template <bool kFp4>
+template <bool kFp4, bool kLatent4>
 __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(const AppendArgs A) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kAppendTokens + (warp >> 1);
@@ -436,7 +441,12 @@ __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(cons
   const int j = lane & 7, g = lane >> 3;  // the lane's place in its 64 dims, and which 64 dims
   const bool key_part = (warp & 1) != 0, is_key = lane < 16;
   Raw8 v0 = {}, v1 = {};
-  if (!key_part) {
+  if (!key_part && kLatent4) {  // a lane's 16 dims are a group: its scale needs no other lane
+    const uint4* src = reinterpret_cast<const uint4*>(A.latent + t * A.latent_stride + 16 * lane);
+    const uint4 a = __ldg(src), b = __ldg(src + 1);
+    v0 = {make_uint2(a.x, a.y), make_uint2(a.z, a.w)};
+    v1 = {make_uint2(b.x, b.y), make_uint2(b.z, b.w)};
+  } else if (!key_part) {
     const __nv_bfloat16* src = A.latent + t * A.latent_stride + 64 * g;
     v0 = load_raw8(src, j);
     v1 = load_raw8(src + 256, j);
@@ -456,6 +466,29 @@ __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(cons
   uint8_t* rec = base + L.rec_off + static_cast<int64_t>(off) * L.rec_stride;
   float x[8], w[8];
   unpack8(v0, x);
+  if (!key_part && kLatent4) {
+    float y[8];
+    unpack8(v1, y);
+    float z[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = x[i], z[8 + i] = y[i];
+    if (A.latent_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss += z[i] * z[i];
+      const float rstd = rsqrtf(warp_sum(ss) / 512.0f + A.eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 n = __ldg(reinterpret_cast<const float4*>(A.latent_norm + 16 * lane) + i);
+        z[4 * i] = z[4 * i] * rstd * n.x;
+        z[4 * i + 1] = z[4 * i + 1] * rstd * n.y;
+        z[4 * i + 2] = z[4 * i + 2] * rstd * n.z;
+        z[4 * i + 3] = z[4 * i + 3] * rstd * n.w;
+      }
+    }
+    store_latent4(z, rec, 512, lane);
+    return;
+  }
   if (!key_part) {
     float y[8];
     unpack8(v1, y);
@@ -511,7 +544,7 @@ __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(cons
   __syncwarp();
   const float amax = half_max8(x);
   if (!is_key) {
-    if (lane < 24) store_bf16x8(reinterpret_cast<__nv_bfloat16*>(rec + 528), j, x);
+    if (lane < 24) store_bf16x8(reinterpret_cast<__nv_bfloat16*>(rec + (kLatent4 ? 288 : 528)), j, x);
     return;
   }
   if (!A.idx_k) return;
@@ -814,12 +847,14 @@ extern "C" smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The full shape with rows that load as 16-byte pieces takes the kernel built for it (half the time at 8,192
   // tokens, two thirds at one: see there).
-  if (L.d_latent == 512 && L.quant_tile == 128 && L.d_rope == 64 && L.d_index == 128 && A.vec_latent &&
+  const bool four = latent4(L);
+  if (L.d_latent == 512 && (four || L.quant_tile == 128) && L.d_rope == 64 && L.d_index == 128 && A.vec_latent &&
       aligned(rope_key, 16) && rope_stride % 8 == 0 && (!idx || A.vec_idx) && aligned(latent_norm, 16) &&
       aligned(idx_norm, 16) && aligned(idx_bias, 16) && aligned(A.rope.cos_sin, 16)) {
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kAppendTokens - 1) / kAppendTokens);
-    if (L.key_format == SMLA_KEY_E2M1) append_full_kernel<true><<<blocks, 64 * kAppendTokens, 0, s>>>(A);
-    else append_full_kernel<false><<<blocks, 64 * kAppendTokens, 0, s>>>(A);
+    const auto launch = [&](auto kernel) { kernel<<<blocks, 64 * kAppendTokens, 0, s>>>(A); };
+    if (L.key_format == SMLA_KEY_E2M1) four ? launch(append_full_kernel<true, true>) : launch(append_full_kernel<true, false>);
+    else four ? launch(append_full_kernel<false, true>) : launch(append_full_kernel<false, false>);
     return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
   }
   switch (L.d_latent / 32) {

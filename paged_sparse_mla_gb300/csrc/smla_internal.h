@@ -15,12 +15,18 @@ namespace smla {
 struct KernelLayout {
   int32_t block_size, n_layers, d_latent, d_rope, quant_tile, d_index, n_scales, rec_stride;
   int32_t key_format, key_bytes;  // smla_key_format_t; bytes of one cached indexer key
+  int32_t latent_format, rope_off;  // smla_latent_format_t; byte offset of a record's rope values
   int64_t num_blocks, rec_off, idx_key_off, idx_scale_off, layer_stride, block_stride;
 };
 
 // Bytes of one cached indexer key of d_index elements in the given format.
 inline int32_t key_bytes_of(int32_t d_index, int32_t key_format) {
   return key_format == SMLA_KEY_E2M1 ? d_index / 2 : d_index;
+}
+
+// The latents' format shows in the record's size: codes of one byte or of half a byte a value.
+inline int32_t record_format(const smla_layout_t& l) {
+  return l.rec_bytes - 2 * static_cast<int64_t>(l.d_rope) < l.d_latent ? SMLA_LATENT_E2M1 : SMLA_LATENT_E4M3;
 }
 
 inline KernelLayout kernel_layout(const smla_layout_t& l) {
@@ -35,6 +41,8 @@ inline KernelLayout kernel_layout(const smla_layout_t& l) {
   k.rec_stride = l.rec_stride;
   k.key_format = l.idx_key_format;
   k.key_bytes = key_bytes_of(l.d_index, l.idx_key_format);
+  k.latent_format = record_format(l);
+  k.rope_off = l.rec_bytes - 2 * l.d_rope;
   k.num_blocks = l.num_blocks;
   k.rec_off = l.rec_off;
   k.idx_key_off = l.idx_key_off;
@@ -66,6 +74,11 @@ bool layout_ok(const smla_layout_t* l);
 bool store_shape_supported(const KernelLayout& L);
 bool index_shape_supported(const KernelLayout& L, int n_idx_heads);
 bool attend_shape_supported(const KernelLayout& L, int n_heads);
+inline bool latent4(const KernelLayout& L) { return L.latent_format == SMLA_LATENT_E2M1; }
+// Records of 4-bit latents are read and written in pieces of 8 and 16 bytes whatever else is aligned.
+inline bool pool_fits(const KernelLayout& L, const void* pool) {
+  return !latent4(L) || (reinterpret_cast<uintptr_t>(pool) & 15) == 0;
+}
 
 // Arguments of one fused step (smla_decode and smla_decode_static take the same ones apart from
 // the scratch), checked by check_step() in the same order for both.

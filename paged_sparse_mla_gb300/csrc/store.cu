@@ -9,11 +9,12 @@
 // combined with xor-shuffles.  scale = amax / 448 is an IEEE fp32 division
 // (the library is built without fast-math), x / scale likewise, and the E4M3
 // code is the hardware's round-to-nearest-even saturating conversion.
+#include "latent4.cuh"
 #include "smla_internal.h"
 
 namespace smla {
 
-template <int E>
+template <int E, bool kLatent4>
 __global__ void __launch_bounds__(256) kvpack_store_kernel(KernelLayout L, uint8_t* __restrict__ pool, int layer,
                                                            const __nv_bfloat16* __restrict__ latent,
                                                            const __nv_bfloat16* __restrict__ rope,
@@ -74,7 +75,10 @@ __global__ void __launch_bounds__(256) kvpack_store_kernel(KernelLayout L, uint8
   uint8_t* layer_base = pool + blk * L.block_stride + static_cast<int64_t>(layer) * L.layer_stride;
   uint8_t* rec = layer_base + L.rec_off + static_cast<int64_t>(off) * L.rec_stride;
 
-  // ---- latent: per-tile amax, scale, E4M3 codes ----
+  // ---- latent: per-tile amax, scale, codes ----
+  if constexpr (kLatent4) {
+    store_latent4(x, rec, L.d_latent, lane);
+  } else {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -109,8 +113,9 @@ __global__ void __launch_bounds__(256) kvpack_store_kernel(KernelLayout L, uint8
   if ((lane * E) % L.quant_tile == 0) {
     reinterpret_cast<float*>(rec + L.d_latent)[(lane * E) / L.quant_tile] = scale;
   }
+  }
   uint8_t* kdst = layer_base + L.idx_key_off + static_cast<int64_t>(off) * L.key_bytes;
-  uint8_t* rdst8 = rec + L.d_latent + 4 * L.n_scales;
+  uint8_t* rdst8 = rec + L.rope_off;
   if (words) {
     // ---- rope (bf16) and indexer key (e4m3 or packed e2m1 bytes) verbatim, 32-bit words ----
 #pragma unroll
@@ -149,27 +154,18 @@ smla_status_t launch_kvpack_store(const KernelLayout& L, void* pool, int layer, 
   const auto al = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
   const bool vec = al(pool, 16) && al(latent, 16) && al(rope, 4) && al(idx_k, 4) && L.d_latent % 8 == 0 &&
                    L.block_stride % 16 == 0 && L.layer_stride % 16 == 0 && L.rec_off % 16 == 0 &&
-                   L.rec_stride % 16 == 0 && (L.d_latent + 4 * L.n_scales) % 4 == 0 && L.d_rope % 2 == 0 &&
+                   L.rec_stride % 16 == 0 && L.rope_off % 4 == 0 && L.d_rope % 2 == 0 &&
                    L.idx_key_off % 4 == 0 && L.key_bytes % 4 == 0;
+  const auto launch = [&](auto kernel) {
+    kernel<<<blocks, threads, 0, stream>>>(L, pl, layer, lat, rp, idx_k, idx_scale, slot_mapping, n_tokens, vec, err);
+  };
+  const bool four = latent4(L);
   switch (L.d_latent / 32) {
-    case 2:
-      kvpack_store_kernel<2><<<blocks, threads, 0, stream>>>(L, pl, layer, lat, rp, idx_k, idx_scale, slot_mapping,
-                                                             n_tokens, vec, err);
-      break;
-    case 4:
-      kvpack_store_kernel<4><<<blocks, threads, 0, stream>>>(L, pl, layer, lat, rp, idx_k, idx_scale, slot_mapping,
-                                                             n_tokens, vec, err);
-      break;
-    case 8:
-      kvpack_store_kernel<8><<<blocks, threads, 0, stream>>>(L, pl, layer, lat, rp, idx_k, idx_scale, slot_mapping,
-                                                             n_tokens, vec, err);
-      break;
-    case 16:
-      kvpack_store_kernel<16><<<blocks, threads, 0, stream>>>(L, pl, layer, lat, rp, idx_k, idx_scale, slot_mapping,
-                                                              n_tokens, vec, err);
-      break;
-    default:
-      return SMLA_ERR_UNSUPPORTED;
+    case 2: four ? launch(kvpack_store_kernel<2, true>) : launch(kvpack_store_kernel<2, false>); break;
+    case 4: four ? launch(kvpack_store_kernel<4, true>) : launch(kvpack_store_kernel<4, false>); break;
+    case 8: four ? launch(kvpack_store_kernel<8, true>) : launch(kvpack_store_kernel<8, false>); break;
+    case 16: four ? launch(kvpack_store_kernel<16, true>) : launch(kvpack_store_kernel<16, false>); break;
+    default: return SMLA_ERR_UNSUPPORTED;
   }
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
