@@ -254,7 +254,11 @@ constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value th
 // it and not a second form of the loop: the loop's code shares the instruction cache with the other warps'.
 constexpr float kSmallScale = 1.220703125e-4f, kSmallUp = 524288.f;
 constexpr int kMaxPairs = 128;
-constexpr int kRec = kDL + 16 + 2 * kDR;  // bytes of a record: codes, four scales, rope
+// Bytes of a record's codes and scales (its rope values follow), and of the record.
+template <bool k4>
+constexpr int kRopeOff = k4 ? kDL / 2 + kDL / kGroup4 : kDL + 16;
+template <bool k4>
+constexpr int kRec = kRopeOff<k4> + 2 * kDR;
 constexpr int kMinTiles = 2;  // key tiles a pair takes at least (1 to 4: the same)
 // Tiles requested into L2 ahead of the loads (1 to 16: the same; none: decode steps 2 % slower, a chunk 1 %).
 constexpr int kPrefetchAhead = 4;
@@ -558,8 +562,9 @@ __device__ __forceinline__ int page_of(const PairArgs& A, int j) {
 }
 
 // Record of a page's token `off`, in 64 bits: a page may hold more than 2^31 bytes of records.
+template <bool k4>
 __device__ __forceinline__ const uint8_t* record(const PairArgs& A, int blk, int off) {
-  return A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec;
+  return A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec<k4>;
 }
 
 // The records of kN consecutive positions from a multiple of kN on.  kRuns: the block size is a multiple
@@ -569,7 +574,7 @@ __device__ __forceinline__ const uint8_t* record(const PairArgs& A, int blk, int
 // 64 that takes 3 % longer in decode steps (194 us against 188) and 5 % in a chunk (4.11 ms against 3.89).
 // find() asks for the block id, take() turns it into the address: a tile later, so that nothing waits for
 // the block table.
-template <bool kRuns, int kN>
+template <bool kRuns, bool k4, int kN>
 struct Records {
   const uint8_t* at;
   int blk, off, n;  // blk = INT_MIN: past the visible positions; off: token of the page
@@ -591,11 +596,11 @@ struct Records {
       latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
       return kN;
     }
-    at = record(A, blk, off);
+    at = record<k4>(A, blk, off);
     return n;
   }
   __device__ __forceinline__ const uint8_t* get(int i) const {
-    if constexpr (kRuns) return at + i * kRec;
+    if constexpr (kRuns) return at + i * kRec<k4>;
     return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(at), i));
   }
 };
@@ -738,7 +743,7 @@ __device__ __forceinline__ void transpose4(uint32_t (&o)[16], bool hi1, bool hi2
   }
 }
 
-template <bool kRuns>
+template <bool kRuns, bool k4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_pair_kernel(const PairArgs A) {
   extern __shared__ uint8_t smem_raw[];
   PairSmem& sm = *reinterpret_cast<PairSmem*>(
@@ -891,11 +896,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
             const int pg = page_of(A, j);
             const int blk = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg);
             if (blk >= 0 && blk < A.D.L.num_blocks)
-              prefetch_l2_bulk(record(A, blk, j - pg * A.D.L.block_size), kRec);
+              prefetch_l2_bulk(record<k4>(A, blk, j - pg * A.D.L.block_size), kRec<k4>);
           }
         }
       }
-    } else if (warp == kIssuer + 2) {
+    } else if (warp == kIssuer + 2 && !k4) {
       // A NaN (code 0x7F of either sign) at a position that only some of a unit's tokens see reaches the others
       // too: their zeros times it.  So those few positions are looked at.  (In the K warps, which hold
       // the codes anyway, the same check cost 5 % of the whole call.)
@@ -908,7 +913,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
           const int pg = page_of(A, j);
           const int blk = __ldg(A.D.block_table + static_cast<int64_t>(w.b) * A.D.bt_stride + pg);
           if (blk < 0 || blk >= A.D.L.num_blocks) continue;
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(record(A, blk, j - pg * A.D.L.block_size)) + lane);
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(record<false>(A, blk, j - pg * A.D.L.block_size)) + lane);
           const auto is = [](uint32_t x) { return (x & 0x7F7F7F7Fu) + 0x01010101u; };
           bad |= ((is(c.x) | is(c.y) | is(c.z) | is(c.w)) & 0x80808080u) != 0;
         }
@@ -927,21 +932,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     const int vw = warp - kFirstV, other = 1 - static_cast<int>(cta);
     const int key0 = kCtaKeys * other + kN * vw;
     const int sub = lane & 15, odd = (sub >> 2) & 1;
-    const int code_off = 256 * static_cast<int>(cta) + 16 * sub, scale_off = kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
+    // (4-bit codes: eight bytes a lane, and the byte of scale of the same 16 dims, so that no scale is passed around)
+    const int code_off = k4 ? 128 * static_cast<int>(cta) + 8 * sub : 256 * static_cast<int>(cta) + 16 * sub;
+    const int scale_off = k4 ? kDL / 2 + 16 * static_cast<int>(cta) + sub : kDL + 8 * static_cast<int>(cta) + 4 * (lane & 1);
     // row & 7 of key 2 i + (lane >> 4) is that of key lane >> 4 xor 2 i
     const uint32_t dst = (4 * other + (sub >> 2)) * kCtaKeys * 128 + sw128_off(kN * vw + (lane >> 4), 2 * (sub & 3) + odd);
     const uint32_t full[2] = {map_cta(smem_u32(&sm.v_full[0]), 0), map_cta(smem_u32(&sm.v_full[1]), 0)};
     uint4 codes[kN / 2];
-    float sc;
-    Records<kRuns, kN> rec;
-    const auto load = [&](int i) { codes[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(2 * i + (lane >> 4)) + code_off)); };
+    uint32_t sc4[kN / 2];
+    float sc = 0.f;
+    Records<kRuns, k4, kN> rec;
+    const auto load = [&](int i) {
+      const uint8_t* r = rec.get(2 * i + (lane >> 4));
+      if constexpr (k4) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(r + code_off));
+        codes[i] = make_uint4(c.x, c.y, 0, 0);
+        sc4[i] = __ldg(r + scale_off);
+      } else {
+        codes[i] = __ldg(reinterpret_cast<const uint4*>(r + code_off));
+      }
+    };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get((lane >> 1) & (kN - 1)) + scale_off)); };
     const auto store = [&](uint32_t mine, unsigned small, uint8_t* tile) {
 #pragma unroll
       for (int i = 0; i < kN / 2; ++i) {
-        const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * (2 * i + (lane >> 4)) + (sub >> 3));
         const uint4 c = codes[i];
         uint8_t* to = tile + 256 * i;
+        if constexpr (k4) {
+          const uint32_t s = scale4_half2(sc4[i]);
+          *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant4x8(odd ? c.y : c.x, s);
+          *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant4x8(odd ? c.x : c.y, s);
+          continue;
+        }
+        const uint32_t s = __shfl_sync(0xffffffffu, mine, 2 * (2 * i + (lane >> 4)) + (sub >> 3));
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 5))) = dequant8(odd ? make_uint2(c.z, c.w) : make_uint2(c.x, c.y), s);
         *reinterpret_cast<uint4*>(to + (dst ^ (i << 5) ^ 16)) = dequant8(odd ? make_uint2(c.x, c.y) : make_uint2(c.z, c.w), s);
       }
@@ -960,7 +983,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     int n = 0;  // visible records among the loaded ones
     const auto load_tile = [&]() {
       n = rec.take(A);
-      load_scale();
+      if constexpr (!k4) load_scale();
 #pragma unroll
       for (int i = 0; i < kN / 2; ++i) load(i);
       tw.next(A);
@@ -973,10 +996,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       if (n < kN) {  // the end of a context: whatever lies behind it counts as zeros
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i)
-          if (2 * i + (lane >> 4) >= n) codes[i] = make_uint4(0, 0, 0, 0);
+          if (2 * i + (lane >> 4) >= n) {
+            if constexpr (k4) sc4[i] = 0;  // a code has no NaN
+            else codes[i] = make_uint4(0, 0, 0, 0);
+          }
         if (((lane >> 1) & (kN - 1)) >= n) sc = 0.f;
       }
-      const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
+      const unsigned small = k4 ? 0 : __ballot_sync(0xffffffffu, small_scale(sc));
       const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
       const uint32_t mine = pack_half2(scaled, scaled);
       // the tile's scores are formed: the chunks that V does not need are free
@@ -994,22 +1020,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     static_assert(kKRegs == kLaunchRegs, "no change of registers");
     constexpr int kN = kKeysPerK;
     const int kw = warp - kFirstK, key0 = kN * kw + kCtaKeys * static_cast<int>(cta);
-    const uint32_t dst = (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
+    // 4-bit codes: half a warp takes a key's half, 16 codes a lane, as the V warps do.
+    const int sub = lane & 15, odd = (sub >> 2) & 1;
+    const uint32_t dst = k4 ? (sub >> 2) * kCtaKeys * 128 + sw128_off(kN * kw + (lane >> 4), 2 * (sub & 3) + odd)
+                            : (lane >> 3) * kCtaKeys * 128 + sw128_off(kN * kw, lane & 7);
     const uint32_t full = map_cta(smem_u32(&sm.k_full[0][0]), 0);
-    uint2 codes[2][kN];
+    uint2 codes[2][kN];  // 4-bit: [half][pair of keys]
+    uint32_t sc4[2][kN / 2];
     uint4 rope[2];
-    float sc;
-    Records<kRuns, kN> rec;
+    float sc = 0.f;
+    Records<kRuns, k4, kN> rec;
     const auto load = [&](int i) {
+      if constexpr (k4) {
+        if (i >= kN / 2) return;
+        const uint8_t* r = rec.get(2 * i + (lane >> 4));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) codes[h][i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + 256 * h) + lane);
+        for (int h = 0; h < 2; ++h) {
+          codes[h][i] = __ldg(reinterpret_cast<const uint2*>(r + 128 * h) + sub);
+          sc4[h][i] = __ldg(r + kDL / 2 + 16 * h + sub);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) codes[h][i] = __ldg(reinterpret_cast<const uint2*>(rec.get(i) + 256 * h) + lane);
+      }
     };
     const auto load_scale = [&]() { sc = __ldg(reinterpret_cast<const float*>(rec.get(lane >> 2) + kDL + 4 * (lane & 3))); };
     const auto load_rope = [&](int i) {
-      rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kDL + 16) + (lane & 7));
+      rope[i] = __ldg(reinterpret_cast<const uint4*>(rec.get(4 * i + (lane >> 3)) + kRopeOff<k4>) + (lane & 7));
     };
     const auto store = [&](auto h, uint32_t mine, unsigned small, uint8_t* tile) {
       uint8_t* to = tile + 4 * kCtaKeys * 128 * h();
+      if constexpr (k4) {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+          const uint2 c = codes[h()][i];
+          const uint32_t s = scale4_half2(sc4[h()][i]);
+          *reinterpret_cast<uint4*>(to + 256 * i + (dst ^ (i << 5))) = dequant4x8(odd ? c.y : c.x, s);
+          *reinterpret_cast<uint4*>(to + 256 * i + (dst ^ (i << 5) ^ 16)) = dequant4x8(odd ? c.x : c.y, s);
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t s = __shfl_sync(0xffffffffu, mine, 4 * i + 2 * h() + (lane >> 4));
@@ -1028,7 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     int n = 0;  // visible records among the loaded ones
     const auto load_tile = [&]() {
       n = rec.take(A);
-      load_scale();
+      if constexpr (!k4) load_scale();
 #pragma unroll
       for (int i = 0; i < kN; ++i) load(i);
       load_rope(0);
@@ -1043,15 +1093,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
       if (threadIdx.x == 32 * kFirstK) *static_cast<volatile uint32_t*>(&sm.k_loaded) = kk + 1;
       if (n < kN) {  // the end of a context
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-          if (i >= n) codes[0][i] = codes[1][i] = make_uint2(0, 0);
+        for (int i = 0; i < kN; ++i) {
+          if constexpr (k4) {
+            if (i < kN / 2 && 2 * i + (lane >> 4) >= n) sc4[0][i] = sc4[1][i] = 0;
+          } else {
+            if (i >= n) codes[0][i] = codes[1][i] = make_uint2(0, 0);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (4 * i + (lane >> 3) >= n) rope[i] = make_uint4(0, 0, 0, 0);
         if ((lane >> 2) >= n) sc = 0.f;
       }
-      bad |= !(fabsf(sc) < kScaleEnd);
-      const unsigned small = __ballot_sync(0xffffffffu, small_scale(sc));
+      if constexpr (k4) {
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) bad |= max(sc4[0][i], sc4[1][i]) > kScale4Top;
+      } else {
+        bad |= !(fabsf(sc) < kScaleEnd);
+      }
+      const unsigned small = k4 ? 0 : __ballot_sync(0xffffffffu, small_scale(sc));
       const float scaled = small_scale(sc) ? sc * kSmallUp : sc;
       const uint32_t mine = pack_half2(scaled, scaled);
       if (!__all_sync(0xffffffffu, pair_wait(&sm.kv_free[kk & 1][0], ((kk >> 1) & 1) ^ 1, err, &sm.abort))) break;
@@ -1444,20 +1504,20 @@ __global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMe
 }
 
 // Layouts of the full latent shape.
-bool pair_shape(const KernelLayout& L) { return L.d_latent == kDL && L.quant_tile == 128 && L.d_rope == kDR; }
+bool pair_shape(const KernelLayout& L) { return L.d_latent == kDL && (latent4(L) || L.quant_tile == 128) && L.d_rope == kDR; }
 
 constexpr size_t kMetaBytes = (kMaxPairs * sizeof(PairMeta) + 255) / 256 * 256;
 constexpr size_t kPartLseBytes = 2 * kMaxPairs * kRows * sizeof(float);
 constexpr size_t kPartOutBytes = size_t(2) * kMaxPairs * kRows * kDL * sizeof(float);
 
-template <bool kRuns>
+template <bool kRuns, bool k4>
 smla_status_t resident_pairs(int* out) {
   static std::atomic<int> pairs_of[kMaxDeviceSlots] = {};
   const int dev = current_device_index();
   if (dev < 0) return SMLA_ERR_CUDA;
   int pairs = pairs_of[dev].load(std::memory_order_acquire);
   if (pairs == 0) {
-    const auto kernel = dense_pair_kernel<kRuns>;
+    const auto kernel = dense_pair_kernel<kRuns, k4>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPairSmemBytes)) != cudaSuccess)
       return SMLA_ERR_CUDA;
     cudaFuncAttributes fa;
@@ -1485,7 +1545,9 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
                                 cudaStream_t s) {
   const bool runs = D.L.block_size % 16 == 0;
   int pairs = 0;  // resident at once
-  const smla_status_t st = runs ? resident_pairs<true>(&pairs) : resident_pairs<false>(&pairs);
+  const bool four = latent4(D.L);
+  const smla_status_t st = four ? (runs ? resident_pairs<true, true>(&pairs) : resident_pairs<false, true>(&pairs))
+                                : (runs ? resident_pairs<true, false>(&pairs) : resident_pairs<false, false>(&pairs));
   if (st != SMLA_OK) return st;
   PairArgs A{};
   A.D = D;
@@ -1511,8 +1573,9 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
     A.part_lse = reinterpret_cast<float*>(w + kMetaBytes);
     A.part_out = reinterpret_cast<float*>(w + kMetaBytes + kPartLseBytes);
   }
-  if (runs) dense_pair_kernel<true><<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
-  else dense_pair_kernel<false><<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A);
+  const auto launch = [&](auto kernel) { kernel<<<2 * pairs, kThreads, kPairSmemBytes, s>>>(A); };
+  if (four) runs ? launch(dense_pair_kernel<true, true>) : launch(dense_pair_kernel<false, true>);
+  else runs ? launch(dense_pair_kernel<true, false>) : launch(dense_pair_kernel<false, false>);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   if (split) {
     // launched while the pairs still work (its blocks wait for their results before they read)
