@@ -1117,6 +1117,10 @@ smla_status_t launch_attend(const KernelLayout& L, int n_heads, int top_k, float
                             void* split_ws, size_t split_ws_bytes) {
   if (tok_end <= tok_begin) return SMLA_OK;
   if (!attend_shape_supported(L, n_heads)) return SMLA_ERR_UNSUPPORTED;
+  if (latent4(L) && L.d_latent == 512 && L.d_rope == 64)
+    return launch_attend4_select(L, n_heads, top_k, softmax_scale, pool, layer, q, q_pe, topk_idx, block_table, bt_stride,
+                                 query_start_loc, batch, tok_begin, tok_end, out, lse, stream, err, host_records, host_block_map,
+                                 n_host_blocks, split_ws, split_ws_bytes);
   // Fewer rows than SMs: each row's tiles are split over up to sms / rows CTAs (one wave of
   // units), as far as the caller's scratch holds the partials.
   const int n_rows = tok_end - tok_begin;

@@ -1,0 +1,792 @@
+// Latent attention over 4-bit records for units of at most 64 rows: decode steps of smla_attend_dense (a row is one
+// query token's head) and the selected positions of smla_attend.
+//
+//   S^T[128 keys x 64 rows] = K . Q^T          M = 128 keys, N = 64 rows, K = 576 dims
+//   P^T = 2^((S^T - m) f + 7), row sums in registers
+//   O^T[512 dims x 64 rows] += V^T . P^T        4 x M = 128 dims, N = 64 rows, K = 128 keys
+// with K and V the same swizzled fp16 tile (V^T read with the keys as its strided dimension), fp16 operands and
+// fp32 sums; the cached values are exact in fp16 (see latent4.cuh), queries are scaled by a power of two per row.
+//
+// Why keys as M: a decode token has 64 rows (64 heads) or fewer and the products' M is 128.  With rows as M (the two-SM
+// kernel of attend_dense.cu) half of it is empty and every tile still reads the whole operand of 128 rows; here each
+// operand byte is used by 64 rows or 128 keys.  A unit's rows are the heads of one token, whose keys no other unit shares
+// (selected positions), or of as many tokens of a sequence as fit 64.
+//
+// One tile of keys (144 KB) and the queries (72 KB) fill shared memory, so that there is no second tile buffer: the next
+// tile waits in the loaders' registers, 4 bits a value, and is converted into each half of the tile as its last product
+// has read it.  The chain of a tile is softmax -> second products, by halves of the dims -> conversion of the half ->
+// first products; P^T takes the rope values' place, which are converted last.
+//
+// A CTA per SM walks over an equal range of all units' tiles; parts of units that cross ranges are joined by their lse.
+#include "attend_work.cuh"
+
+namespace smla {
+namespace {
+
+constexpr int kUnitRows = 64;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 16;
+constexpr int kFirstLoad = kSoftmaxWarps, kIssuer = kFirstLoad + kLoadWarps;
+constexpr int kThreads = 32 * (kIssuer + 4);  // the last four: issuer, L2 requests, two without work
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 112, kLoadRegs = 64, kOtherRegs = 24;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs,
+              "register split exceeds the launch");
+constexpr int kMaxCtas = 160;
+constexpr int kKeyChunk = kKeys * 128, kRowChunk = kUnitRows * 128;  // bytes of a 64-dim chunk
+constexpr int kRec4 = kDL / 2 + kDL / kGroup4 + 2 * kDR, kScaleOff = kDL / 2, kRopeOff4 = kDL / 2 + kDL / kGroup4;
+constexpr int kPrefetchAhead = 3;   // tiles requested into L2 ahead of the loads
+constexpr float kNoScore = -1e38f;  // running maximum of a row that has seen no score yet
+
+struct __align__(1024) Smem4 {
+  uint8_t k[kChunks][kKeyChunk];  // [128 keys][64 dims] fp16, 128-byte swizzle; the last: rope, then P^T [128 keys][64 rows]
+  uint8_t q[kChunks][kRowChunk];
+  float red[4][kUnitRows];
+  float m[kUnitRows], alpha[kUnitRows], inv[kUnitRows];
+  float f[2][kUnitRows];          // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
+  int vis[2][kUnitRows];          // positions that the row sees
+  uint64_t k_full[2], q_full, s_full, p_full, kv_free[2], final_bar;
+  int64_t x0, total, seq_at;      // the CTA's range of work (plan)
+  int pairs, b, g, rel, len, q0, n_q, seq_len;
+  int abort;
+  uint32_t tmem_slot;
+  uint32_t loaded;                // tiles that the first loader warp has asked for
+};
+constexpr size_t kSmem4Bytes = sizeof(Smem4) + 1024;
+static_assert(kSmem4Bytes <= 232448, "shared memory");
+
+struct Args4 {
+  DenseArgs D;
+  int group;        // query tokens of a unit
+  int unit_cost;    // of a unit beside its tiles, in tiles
+  float abs_scale;  // |softmax_scale| log2(e)
+  float sign;       // of softmax_scale, applied to the queries
+  bool q_vec;       // q and q_pe are 16-byte aligned
+  float *part_out, *part_lse;  // partial results, slots [2 CTAs][slot_rows]; nullptr: units are not split
+  PartMeta* meta;   // [CTAs]
+  int slot_rows;
+  const uint8_t* records;      // the layer's records in block 0
+  PageDiv pages;    // division by block_size
+  // selected positions: rows of top_k, one for each token from tok_begin on
+  const int32_t* topk;
+  int top_k, row_tiles, tok_begin, n_units;
+  const uint8_t* host_records;  // see smla_attend_hisparse
+  const int32_t* host_block_map;
+  int64_t n_host_blocks;
+};
+
+// Tiles of a row of selected positions up to its last one, at least one.
+__device__ __forceinline__ int selected_tiles(const int32_t* row, int k) {
+  const int lane = threadIdx.x & 31;
+  if (__ldg(row + k - 1) >= 0) return (k + kKeys - 1) / kKeys;
+  int last = -1;
+#pragma unroll 8
+  for (int i = lane; i < k; i += 32)
+    if (__ldg(row + i) >= 0) last = i;
+  last = __reduce_max_sync(0xffffffffu, last);
+  return max(1, (last + kKeys) / kKeys);
+}
+
+// The units of a CTA over selected positions: a token each, cut as if every row had all of its positions.
+struct SelectWalk {
+  int u, rel, len, b, nvis, cap;  // cap: tiles of the row that hold positions
+  __device__ __forceinline__ void start(const Args4& A, const Smem4& sm) {
+    u = sm.g;
+    rel = sm.rel + (A.part_out != nullptr ? A.unit_cost : 0);
+    len = sm.len;
+    nvis = 0;
+    if (on()) unit(A);
+  }
+  __device__ __forceinline__ bool on() const { return rel < len; }
+  __device__ __forceinline__ int tok0(const Args4& A) const { return A.tok_begin + u; }
+  __device__ __forceinline__ int ntok(const Args4&) const { return 1; }
+  __device__ __forceinline__ const int32_t* row(const Args4& A) const { return A.topk + static_cast<int64_t>(u) * A.top_k; }
+  __device__ __forceinline__ int ta(const Args4& A) const { return A.part_out != nullptr ? max(-rel, 0) : 0; }
+  __device__ __forceinline__ int end(const Args4& A) const { return A.part_out != nullptr ? min(A.row_tiles, len - rel) : A.row_tiles; }
+  // a part without positions keeps one tile, which leaves zeros and an lse of -inf to the join
+  __device__ __forceinline__ int tb(const Args4& A) const { return min(end(A), max(cap, ta(A) + 1)); }
+  __device__ __forceinline__ bool cut(const Args4& A) const { return end(A) < A.row_tiles; }
+  __device__ __forceinline__ int unit_end(const Args4& A) const { return rel + A.row_tiles; }
+  __device__ __forceinline__ void unit(const Args4& A) {
+    cap = selected_tiles(row(A), A.top_k);
+    b = seq_of_token(A.D.qsl, A.D.batch, tok0(A));
+  }
+  __device__ __forceinline__ void next(const Args4& A) {
+    rel += A.part_out != nullptr ? A.row_tiles + A.unit_cost : 1;
+    ++u;
+    if (on()) unit(A);
+  }
+};
+// The units of a CTA over whole contexts.
+struct ContextWalk : Walk {
+  __device__ __forceinline__ bool cut(const Args4& A) const { return tb(A) < tiles(); }
+  __device__ __forceinline__ int unit_end(const Args4&) const { return rel + tiles(); }
+};
+
+__device__ __forceinline__ void select_plan(const Args4& A, Smem4& sm) {
+  if (threadIdx.x != 0) return;
+  const int64_t per = A.part_out != nullptr ? A.row_tiles + A.unit_cost : 1, total = A.n_units * per;
+  const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), A.part_out != nullptr ? total / kMinTiles : total));
+  const int64_t c = blockIdx.x, x0 = c < P ? c * total / P : total, x1 = c < P ? (c + 1) * total / P : total;
+  sm.x0 = x0;
+  sm.len = static_cast<int>(x1 - x0);
+  sm.total = total;
+  sm.pairs = static_cast<int>(P);
+  sm.g = static_cast<int>(x0 / per);
+  sm.rel = -static_cast<int>(x0 - sm.g * per);
+}
+
+// D (+)= A . B, issued by the lane whose `elected` is set (see mma2_f16 of the two-SM kernel: the whole warp comes here,
+// so that the operands live in uniform registers).
+template <int kAOff, int kBOff>
+__device__ __forceinline__ void mma1_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                         uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+      "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(kAOff >> 4), "n"(kBOff >> 4),
+      "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void commit1(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+
+// Lane l holds, in v[0], the sum (maximum) over the warp's lanes of value l.
+template <bool kMax>
+__device__ __forceinline__ float across32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int st = 0; st < 5; ++st) {
+    const int off = 16 >> st;
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < off; ++i) {
+      const float send = upper ? v[i] : v[i + off], keep = upper ? v[i + off] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, send, off);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
+
+// (a, b) * (c, d) + (e, e) as a packed fp32 operation
+__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float c) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+      "fma.rn.f32x2 %0, x, y, z;\n\t}"
+      : "=l"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
+}
+
+template <bool kSelect>
+__global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
+  using W = std::conditional_t<kSelect, SelectWalk, ContextWalk>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem4& sm = *reinterpret_cast<Smem4*>(smem_raw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u)) & 1023u));
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform to the compiler
+  unsigned* err = A.D.err;
+  volatile int* abort = &sm.abort;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_full[i], kLoadWarps);
+      mbar_init(&sm.kv_free[i], 1);
+    }
+    mbar_init(&sm.q_full, kSoftmaxWarps);
+    mbar_init(&sm.s_full, 1);
+    mbar_init(&sm.p_full, kSoftmaxWarps);
+    mbar_init(&sm.final_bar, 1);
+    sm.abort = 0;
+    sm.loaded = 0;
+    mbar_fence_init();
+  }
+  if (warp == kIssuer) tmem_alloc(&sm.tmem_slot, 512);
+  cudaTriggerProgrammaticLaunchCompletion();  // the join may be launched; it waits for this grid's end
+  if constexpr (kSelect) select_plan(A, sm);
+  else plan<kThreads>(A, sm, blockIdx.x, gridDim.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_slot, 0);
+  const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
+
+  if (warp >= kIssuer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kIssuer) {
+      // ------------------------------ MMA issuer ------------------------------
+      const uint32_t elected = elect_one();
+      const uint32_t idesc1 = make_idesc(kKeys, kUnitRows, 0, 0, 0, 0);  // fp16, both K-major
+      const uint32_t idesc2 = make_idesc(128, kUnitRows, 0, 0, 1, 1);    // fp16, V^T and P^T MN-major
+      const uint64_t dk = sw128_desc(smem_u32(sm.k[0]), 16, 1024), dq = sw128_desc(smem_u32(sm.q[0]), 16, 1024);
+      const uint64_t dv = sw128_desc(smem_u32(sm.k[0]), kKeyChunk, 1024), dp = sw128_desc(smem_u32(sm.k[8]), kKeyChunk, 1024);
+      const uint32_t dk_lo = static_cast<uint32_t>(dk), dq_lo = static_cast<uint32_t>(dq), dv_lo = static_cast<uint32_t>(dv), dp_lo = static_cast<uint32_t>(dp);
+      const uint32_t dk_hi = static_cast<uint32_t>(dk >> 32), dv_hi = static_cast<uint32_t>(dv >> 32);  // K and Q alike; V and P alike
+      const auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort));
+        tc_fence_after();
+        return ok;
+      };
+      uint32_t kk = 0, n = 0;
+      bool ok = true;
+      W w;
+      for (w.start(A, sm); w.on() && ok; w.next(A), ++n) {
+        ok = wait(&sm.q_full, n & 1);
+        const int count = w.tb(A) - w.ta(A);
+#pragma unroll 1
+        for (int i = 0; i < count && ok; ++i, ++kk) {
+          // S^T: dims 0-255, then the others with the rope's
+#pragma unroll 1
+          for (int h = 0; h < 2 && ok; ++h) {
+            ok = wait(&sm.k_full[h], kk & 1);
+            if (!ok) break;
+            const int end = h == 0 ? 4 : kChunks;
+#pragma unroll 1
+            for (int c = 4 * h; c < end; ++c)
+              unrolled<4>([&](auto x) {
+                mma1_f16<x() * 32, x() * 32>(tmem_s, dk_lo + c * (kKeyChunk >> 4), dk_hi, dq_lo + c * (kRowChunk >> 4), dk_hi, idesc1,
+                                             (c | x()) != 0, elected);
+              });
+          }
+          if (!ok) break;
+          commit1(&sm.s_full, elected);
+          ok = wait(&sm.p_full, kk & 1);
+          if (!ok) break;
+          // O^T: dims 0-255, then the others; each half's keys are free when its products are done
+#pragma unroll 1
+          for (int d = 0; d < 4; ++d) {
+            unrolled<8>([&](auto x) {
+              mma1_f16<x() * 2048, x() * 2048>(tmem_o + d * kUnitRows, dv_lo + d * (2 * kKeyChunk >> 4), dv_hi, dp_lo, dv_hi, idesc2,
+                                               !(i == 0 && x() == 0), elected);
+            });
+            if (d & 1) commit1(&sm.kv_free[d >> 1], elected);
+          }
+        }
+      }
+      commit1(&sm.final_bar, elected);  // nothing may still read or write this CTA's memory when it leaves
+      mbar_drain(&sm.final_bar, 0);
+    } else if (warp == kIssuer + 1) {
+      // Requests records into L2 a few tiles before the loaders ask for them.
+      TileWalkOf<W> tw;
+      tw.start(A, sm);
+      uint64_t last = globaltimer_ns();
+      uint32_t seen = 0;
+      for (uint32_t kk = 0; tw.on(); ++kk, tw.next(A)) {
+        if (kk < *static_cast<volatile uint32_t*>(&sm.loaded)) continue;  // too late for this tile
+        for (;;) {
+          const uint32_t done = *static_cast<volatile uint32_t*>(&sm.loaded);
+          if (kk < done + kPrefetchAhead && done > 0) break;
+          const uint64_t now = globaltimer_ns();
+          if (done != seen) last = now;
+          seen = done;
+          if (*abort || now - last > kWaitLimitNs) break;  // requests only: nothing waits for them
+          __nanosleep(100);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int e = tw.tile * kKeys + 32 * i + lane;
+          int j = -1;
+          if constexpr (kSelect) {
+            if (e < A.top_k) j = __ldg(tw.w.row(A) + e);
+            if (j >= A.D.most) j = -1;
+          } else {
+            if (e < tw.w.nvis) j = e;
+          }
+          if (j < 0) continue;
+          const int pg = page_of(A, j);
+          const int blk = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg);
+          if (blk < 0 || blk >= A.D.L.num_blocks || (kSelect && A.host_block_map != nullptr && __ldg(A.host_block_map + blk) >= 0)) continue;
+          prefetch_l2_bulk(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(j - pg * A.D.L.block_size) * kRec4, kRec4);
+        }
+      }
+    }
+  } else if (warp >= kFirstLoad) {
+    // ------------------------------ loaders: 8 keys of a tile each ------------------------------
+    // Eight lanes hold a key: lane j 16 codes (a scale's) of each 128 dims, and 16 bytes of the rope; a lane serves keys
+    // `slot` and slot + 4 of the warp's.  What a quarter-warp stores (a key's 128 dims) goes to eight different 16-byte
+    // slots (lanes of the odd chunk store their second slot first).  All loads of the next tile are asked for behind
+    // the last fence of the one before (a fence waits for loads in flight).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    const int lw = warp - kFirstLoad, j8 = lane & 7, slot = lane >> 3, odd = j8 >> 2;
+    const int key0 = 8 * lw + slot;
+    const uint32_t dst = (j8 >> 2) * kKeyChunk + sw128_off(key0, 2 * (j8 & 3) + odd), rope_dst = 8 * kKeyChunk + sw128_off(key0, j8);
+    uint2 codes[4][2];
+    uint32_t sc[4][2];
+    uint4 rope[2];
+    int pos[2], blk[2], off[2], seq = 0;  // positions of the tile after next; block ids (INT_MIN: no key) of the next
+    bool on_next = false, on = false;
+    TileWalkOf<W> tw;
+    const auto positions = [&]() {
+      on_next = tw.on();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        pos[x] = -1;
+        if (!on_next) continue;
+        const int e = tw.tile * kKeys + key0 + 4 * x;
+        if constexpr (kSelect) {
+          if (e < A.top_k) pos[x] = __ldg(tw.w.row(A) + e);
+        } else {
+          if (e < tw.w.nvis) pos[x] = e;
+        }
+      }
+      seq = tw.w.b;
+      tw.next(A);
+    };
+    const auto lookup = [&]() {
+      on = on_next;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        blk[x] = INT_MIN;
+        if (pos[x] < 0) continue;
+        const int pg = page_of(A, pos[x]);
+        off[x] = pos[x] - pg * A.D.L.block_size;
+        blk[x] = kSelect && pos[x] >= A.D.most ? -1 : max(__ldg(A.D.block_table + static_cast<int64_t>(seq) * A.D.bt_stride + pg), -1);
+      }
+    };
+    const auto record = [&](int x) -> const uint8_t* {
+      if (blk[x] == INT_MIN) return nullptr;
+      if (blk[x] >= 0 && blk[x] < A.D.L.num_blocks) {
+        if (kSelect && A.host_block_map != nullptr) {
+          const int hb = __ldg(A.host_block_map + blk[x]);
+          if (hb >= 0 && hb < A.n_host_blocks)
+            return A.host_records + ((static_cast<int64_t>(hb) * A.D.L.n_layers + A.D.layer) * A.D.L.block_size + off[x]) * kRec4;
+          if (hb < 0) return A.records + static_cast<int64_t>(blk[x]) * A.D.L.block_stride + static_cast<int64_t>(off[x]) * kRec4;
+        } else {
+          return A.records + static_cast<int64_t>(blk[x]) * A.D.L.block_stride + static_cast<int64_t>(off[x]) * kRec4;
+        }
+      }
+      latch_error(err, SMLA_ERR_BAD_INDEX);
+      return nullptr;
+    };
+    const auto load_tile = [&]() {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* r = record(x);
+        if (r != nullptr) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            codes[p][x] = __ldg(reinterpret_cast<const uint2*>(r + 64 * p) + j8);
+            sc[p][x] = __ldg(r + kScaleOff + 8 * p + j8);
+          }
+          rope[x] = __ldg(reinterpret_cast<const uint4*>(r + kRopeOff4) + j8);
+        } else {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            codes[p][x] = make_uint2(0, 0);
+            sc[p][x] = 0;
+          }
+          rope[x] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
+    const auto store = [&](auto h) {
+#pragma unroll
+      for (int p = 2 * h(); p < 2 * h() + 2; ++p) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint2 c = codes[p][x];
+          const uint32_t s = scale4_half2(sc[p][x]);
+          uint8_t* to = sm.k[2 * p] + 512 * x + (dst ^ (x << 6));
+          uint8_t* to2 = sm.k[2 * p] + 512 * x + (dst ^ (x << 6) ^ 16);
+          *reinterpret_cast<uint4*>(to) = dequant4x8(odd ? c.y : c.x, s);
+          *reinterpret_cast<uint4*>(to2) = dequant4x8(odd ? c.x : c.y, s);
+        }
+      }
+    };
+    bool bad = false;
+    tw.start(A, sm);
+    positions();
+    lookup();
+    positions();
+    for (uint32_t kk = 0; on; ++kk) {
+      load_tile();
+      lookup();  // (sets `on` for the next tile)
+      positions();
+      if (threadIdx.x == 32 * kFirstLoad) *static_cast<volatile uint32_t*>(&sm.loaded) = kk + 1;
+      if (kk > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.kv_free[0], (kk - 1) & 1, err, abort))) break;
+      store(std::integral_constant<int, 0>{});
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[0]);
+      if (kk > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.kv_free[1], (kk - 1) & 1, err, abort))) break;
+      store(std::integral_constant<int, 1>{});
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t v[4] = {rope[x].x, rope[x].y, rope[x].z, rope[x].w};
+        uint32_t o[4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
+          o[i] = pack_half2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+        }
+        bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) bad |= sc[p][x] > kScale4Top;
+        *reinterpret_cast<uint4*>(sm.k[0] + 512 * x + (rope_dst ^ (x << 6))) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[1]);
+    }
+    if (bad) latch_error(err, SMLA_ERR_RANGE);
+  } else {
+    // ------------------------------ queries, softmax, epilogue ------------------------------
+    // Thread: key 32 (warp % 4) + lane of a tile (TMEM lane; a dim of O^T), rows 32 (warp / 4) .. + 31.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int tid = threadIdx.x, sp = warp & 3, hh = warp >> 2, key = 32 * sp + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+    const int H = A.D.n_heads;
+    // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is scaled by
+    // a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's eight bits exactly down to
+    // 2^-23 of that element.
+    const auto load_q = [&](const W& w, int buf) {
+      const int rows = w.ntok(A) * H;
+      const int64_t first = static_cast<int64_t>(w.tok0(A)) * H;
+      if constexpr (!kSelect) {
+        if (tid < kUnitRows)
+          sm.vis[buf][tid] = tid < rows ? static_cast<int>(visible(A.D, w.seq_len, w.g * A.group + tid / H, w.n_q)) : INT_MAX;
+      }
+      uint32_t v[4][9];
+      const auto ask = [&](int i, int r) {
+#pragma unroll
+        for (int x = 0; x < 9; ++x) v[i][x] = 0;
+        if (r < rows) load_query(A, first + r, lane, v[i]);
+      };
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ask(i, 8 * warp + i);
+#pragma unroll 1
+      for (int r0 = 8 * warp; r0 < 8 * warp + 8; r0 += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + i;
+          uint32_t top2 = 0;  // the largest magnitude (bf16 bits of non-negative values order as integers)
+#pragma unroll
+          for (int x = 0; x < 9; ++x) top2 = __vmaxu2(top2, v[i][x] & 0x7FFF7FFFu);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+          const int ex = static_cast<int>(top >> 7);  // biased exponent
+          const int up = (ex == 0 || ex == 255) ? 0 : min(126, 127 + 8 - ex);  // zeros, infinities and NaN as they are
+          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23) * A.sign;
+          uint32_t o[9];
+#pragma unroll
+          for (int x = 0; x < 9; ++x)
+            o[x] = pack_half2(__uint_as_float(v[i][x] << 16) * f, __uint_as_float(v[i][x] & 0xFFFF0000u) * f);
+#pragma unroll
+          for (int x = 0; x < 9; ++x) v[i][x] = v[i + 2][x];
+          const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
+          const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]) = odd ? o1 : o0;
+          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + 1 - odd)]) = odd ? o0 : o1;
+          *reinterpret_cast<uint32_t*>(&sm.q[8][sw128_off(r, lane >> 2) + 4 * (lane & 3)]) = o[8];
+          // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
+          if (lane == 0) sm.f[buf][r] = fmaxf(A.abs_scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
+        }
+        if (r0 < 8 * warp + 4) {
+          ask(2, r0 + 4);
+          ask(3, r0 + 5);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+
+    W w;
+    w.start(A, sm);
+    if (A.meta != nullptr && tid == 0) A.meta[blockIdx.x].ntok = 0;
+    W nx = w;  // the unit whose queries come next
+    uint32_t kk = 0, n = 0;
+    float l[32];
+    bool ok = true;
+    // Each turn: the next unit's queries (the last scores are formed, Q is free), the results of the unit before, then
+    // the unit's tiles.  A failed wait skips nothing: it is ORed into the next barrier of the eight warps, which leave
+    // together.
+    for (;; ++n) {
+      if (n > 0) sm.red[sp][32 * hh + lane] = across32<false>(l, lane);
+      if (nx.on()) load_q(nx, n & 1);
+      if (n > 0) {
+        // ---- end of unit ----
+        const int rows = w.ntok(A) * H, ta = w.ta(A);
+        const bool partial = ta > 0 || w.cut(A);
+        const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (ta > 0 ? 0 : 1);
+        const int64_t orow = static_cast<int64_t>(w.tok0(A)) * H;
+        ok = mbar_wait(&sm.kv_free[1], (kk - 1) & 1, err, abort) && ok;
+        __syncwarp();
+        tc_fence_after();
+        if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) break;
+        if (tid < kUnitRows) {
+          const float lt = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+          sm.inv[tid] = lt == 0.f ? 0.f : 1.f / lt;  // no visible key: zeros
+          const float lse = lt == 0.f ? -INFINITY : (sm.m[tid] * sm.f[(n - 1) & 1][tid] - kLift + log2f(lt)) * kLn2;
+          if (tid < rows) {
+            if (partial) A.part_lse[part * A.slot_rows + tid] = lse;
+            else if (A.D.lse != nullptr) A.D.lse[orow + tid] = lse;
+          }
+        }
+        named_bar_sync(1, 32 * kSoftmaxWarps);
+#pragma unroll 1
+        for (int d2 = 0; d2 < 4; ++d2) {
+          if (32 * hh >= rows) break;
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o);
+          tmem_ld_wait(o);
+          const int d = d2 * 128 + key;
+          if (!partial) {
+            // Lane: dim d for 32 rows.  Four rows at a time, a 4x4 transpose within each group of four lanes gives
+            // lane 4 g + i four consecutive dims of row i, which go out as one 8-byte store.
+            const int i4 = lane & 3;
+#pragma unroll
+            for (int x0 = 0; x0 < 32; x0 += 4) {
+              float a[4];
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) a[jj] = __uint_as_float(o[x0 + jj]) * sm.inv[32 * hh + x0 + jj];
+#pragma unroll
+              for (int st = 2; st >= 1; st >>= 1) {
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                  if ((jj & st) == 0) {
+                    const bool hi = (i4 & st) != 0;
+                    const float got = __shfl_xor_sync(0xffffffffu, hi ? a[jj] : a[jj | st], st);
+                    if (hi) a[jj] = got;
+                    else a[jj | st] = got;
+                  }
+                }
+              }
+              const int r = 32 * hh + x0 + i4;
+              if (r < rows)
+                *reinterpret_cast<uint2*>(A.D.out + (orow + r) * kDL + d - i4) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+            }
+          } else {
+            float* to = A.part_out + (part * A.slot_rows + 32 * hh) * kDL + d;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * hh + x < rows) to[x * kDL] = __uint_as_float(o[x]) * sm.inv[32 * hh + x];
+          }
+        }
+        tc_fence_before();
+        // the unit that goes on in the next CTA: what the join has to read
+        if (tid == 0 && ta == 0 && w.cut(A))
+          A.meta[blockIdx.x] = {sm.x0 + w.unit_end(A), sm.total, sm.pairs, w.tok0(A), w.ntok(A)};
+      }
+      named_bar_sync(1, 32 * kSoftmaxWarps);  // red and inv are read, f and vis are written
+      w = nx;
+      if (!w.on()) break;
+      nx.next(A);
+      const int ta = w.ta(A), tb = w.tb(A);
+      const float* f = sm.f[n & 1] + 32 * hh;
+      const float* m = sm.m + 32 * hh;
+      // tiles below `full` are seen whole by every row
+      int full = 0;
+      if constexpr (!kSelect) full = sm.vis[n & 1][0] / kKeys;
+      int entry = -1;
+      const auto selected = [&](int tile) -> int {
+        const int e = tile * kKeys + key;
+        if constexpr (kSelect) return e < A.top_k ? __ldg(w.row(A) + e) : -1;
+        return 0;
+      };
+      entry = selected(ta);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) l[i] = 0.f;
+      bool failed = false;
+#pragma unroll 1
+      for (int tile = ta; tile < tb; ++tile, ++kk) {
+        const bool there = entry >= 0;
+        if (tile + 1 < tb) entry = selected(tile + 1);
+        ok = ok && mbar_wait(&sm.s_full, kk & 1, err, abort);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t r[32];
+        const auto scores = [&]() {  // what the products say, masked
+          tmem_ld32(tmem_s + lane_base + 32 * hh, r);
+          tmem_ld_wait(r);
+          if constexpr (kSelect) {
+            if (!there) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) r[i] = 0xFF800000u;  // -inf
+            }
+          } else if (tile >= full) {
+            const int at = tile * kKeys + key;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const int4 v = *reinterpret_cast<const int4*>(&sm.vis[n & 1][32 * hh + i]);
+              if (at >= v.x) r[i] = 0xFF800000u;
+              if (at >= v.y) r[i + 1] = 0xFF800000u;
+              if (at >= v.z) r[i + 2] = 0xFF800000u;
+              if (at >= v.w) r[i + 3] = 0xFF800000u;
+            }
+          }
+        };
+        // exponents: (score - m) f + 7, the difference first (it is exact near m, however large both are)
+        const auto exponents = [&]() {
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 mv = *reinterpret_cast<const float4*>(m + i), fv = *reinterpret_cast<const float4*>(f + i);
+            const float2 a = fma2v(add2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(-mv.x, -mv.y)), make_float2(fv.x, fv.y), kLift);
+            const float2 b = fma2v(add2(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(-mv.z, -mv.w)), make_float2(fv.z, fv.w), kLift);
+            r[i] = __float_as_uint(a.x), r[i + 1] = __float_as_uint(a.y), r[i + 2] = __float_as_uint(b.x), r[i + 3] = __float_as_uint(b.y);
+            top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+          }
+          return top;
+        };
+        const bool first = tile == ta;
+        scores();
+        float top = INFINITY;
+        if (!first) top = exponents();
+        // A row's maximum moves only when a score passes it by 2^8; only then (and on the first tile) the rows'
+        // maxima over the tile are formed.
+        if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || top > kRescale + kLift)) {
+          if (!first) scores();
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          sm.red[sp][32 * hh + lane] = across32<true>(v, lane);
+          if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) {
+            failed = true;
+            break;
+          }
+          bool moves = false;
+          if (tid < kUnitRows) {
+            const float mt = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
+            const float old = sm.m[tid], fr = sm.f[n & 1][tid];
+            moves = !first && (mt - old) * fr > kRescale;
+            const float mn = first ? fmaxf(mt, kNoScore) : moves ? mt : old;
+            sm.alpha[tid] = moves ? exp2f((old - mn) * fr) : 1.f;
+            sm.m[tid] = mn;
+          }
+          if (bar_red_or(1, 32 * kSoftmaxWarps, moves)) {
+            // O^T holds the tiles before this one once their last product is done; this tile's waits for p_full
+            ok = mbar_wait(&sm.kv_free[1], (kk - 1) & 1, err, abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l[i] *= sm.alpha[32 * hh + i];
+#pragma unroll 1
+            for (int d2 = 0; d2 < 4; ++d2) {
+              uint32_t o[32];
+              tmem_ld32(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.alpha[32 * hh + i]);
+              tmem_st32(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o);
+            }
+            tmem_st_wait();
+          }
+          scores();  // again: the products are still there, and registers for a second copy are not
+          exponents();
+        }
+        uint32_t pw[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 p = make_float2(fast_exp2(__uint_as_float(r[i])), fast_exp2(__uint_as_float(r[i + 1])));
+          const float2 s = add2(make_float2(l[i], l[i + 1]), p);
+          l[i] = s.x, l[i + 1] = s.y;
+          pw[i / 2] = pack_half2(p.x, p.y);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          *reinterpret_cast<uint4*>(sm.k[8] + sw128_off(key, 4 * hh + v)) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full);
+      }
+      if (failed) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+
+template <bool kSelect>
+smla_status_t launch(Args4& A, float softmax_scale, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  static std::atomic<bool> ready[kMaxDeviceSlots] = {};
+  const int dev = current_device_index();
+  if (dev < 0) return SMLA_ERR_CUDA;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(attend4_kernel<kSelect>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem4Bytes)) != cudaSuccess)
+      return SMLA_ERR_CUDA;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attend4_kernel<kSelect>) != cudaSuccess) return SMLA_ERR_CUDA;
+    if (fa.numRegs < kLaunchRegs) return SMLA_ERR_UNSUPPORTED;  // setmaxnreg.inc draws on the launch's registers
+    ready[dev].store(true, std::memory_order_release);
+  }
+  A.abs_scale = fabsf(softmax_scale) * kLog2e;
+  A.sign = softmax_scale < 0.f ? -1.f : 1.f;
+  A.q_vec = (reinterpret_cast<uintptr_t>(A.D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(A.D.q_pe) & 15) == 0;
+  A.records = A.D.pool + static_cast<int64_t>(A.D.layer) * A.D.L.layer_stride + A.D.L.rec_off;
+  A.pages = page_div(A.D.L.block_size);
+  const int ctas = std::min(device_sm_count(), kMaxCtas);
+  // Units are cut where a scratch holds their parts; without one they stay whole.
+  uint8_t* ws = reinterpret_cast<uint8_t*>(up16(reinterpret_cast<uintptr_t>(workspace)));
+  const size_t skipped = workspace != nullptr ? static_cast<size_t>(ws - static_cast<uint8_t*>(workspace)) : 0;
+  const size_t meta = up16(ctas * sizeof(PartMeta)), lse = up16(2 * static_cast<size_t>(ctas) * A.slot_rows * sizeof(float));
+  const size_t out = 2 * static_cast<size_t>(ctas) * A.slot_rows * kDL * sizeof(float);
+  const bool split = workspace != nullptr && workspace_bytes >= skipped + meta + lse + out;
+  if (split) {
+    A.meta = reinterpret_cast<PartMeta*>(ws);
+    A.part_lse = reinterpret_cast<float*>(ws + meta);
+    A.part_out = reinterpret_cast<float*>(ws + meta + lse);
+  }
+  attend4_kernel<kSelect><<<ctas, kThreads, kSmem4Bytes, s>>>(A);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  return split ? launch_part_merge<kMaxCtas>(A.meta, A.part_lse, A.part_out, ctas, A.slot_rows, A.D.n_heads, A.D.out, A.D.lse, s) : SMLA_OK;
+}
+
+}  // namespace
+
+smla_status_t launch_attend4_dense(const DenseArgs& D, float softmax_scale, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  Args4 A{};
+  A.D = D;
+  A.group = kUnitRows / D.n_heads;
+  A.unit_cost = 2;
+  A.slot_rows = A.group * D.n_heads;
+  return launch<false>(A, softmax_scale, workspace, workspace_bytes, s);
+}
+
+smla_status_t launch_attend4_select(const KernelLayout& L, int n_heads, int top_k, float softmax_scale, const void* pool, int layer,
+                                    const void* q, const void* q_pe, const int32_t* topk_idx, const int32_t* block_table, int bt_stride,
+                                    const int32_t* query_start_loc, int batch, int tok_begin, int tok_end, void* out, float* lse,
+                                    cudaStream_t stream, unsigned* err, const void* host_records, const int32_t* host_block_map,
+                                    int64_t n_host_blocks, void* split_ws, size_t split_ws_bytes) {
+  Args4 A{};
+  A.D.L = L;
+  A.D.n_heads = n_heads;
+  A.D.layer = layer;
+  A.D.pool = static_cast<const uint8_t*>(pool);
+  A.D.q = static_cast<const __nv_bfloat16*>(q);
+  A.D.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  A.D.block_table = block_table;
+  A.D.bt_stride = bt_stride;
+  A.D.most = static_cast<int64_t>(bt_stride) * L.block_size;
+  A.D.qsl = query_start_loc;
+  A.D.batch = batch;
+  A.D.out = static_cast<__nv_bfloat16*>(out);
+  A.D.lse = lse;
+  A.D.err = err;
+  A.group = 1;
+  A.unit_cost = 2;
+  A.slot_rows = n_heads;
+  A.topk = topk_idx;
+  A.top_k = top_k;
+  A.row_tiles = (top_k + kKeys - 1) / kKeys;
+  A.tok_begin = tok_begin;
+  A.n_units = tok_end - tok_begin;
+  A.host_records = static_cast<const uint8_t*>(host_records);
+  A.host_block_map = host_block_map;
+  A.n_host_blocks = n_host_blocks;
+  return launch<true>(A, softmax_scale, split_ws, split_ws_bytes, stream);
+}
+
+}  // namespace smla

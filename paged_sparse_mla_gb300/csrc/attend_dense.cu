@@ -8,46 +8,12 @@
 //   out = sum_j e^(s_j - m) K_j / l,  lse = m + ln l            over the positions j that the token sees
 // in one pass over the keys: m and l are running values, and what is summed so far is multiplied by
 // e^(m_old - m_new) when m moves.  Exponentials are powers of two (the scale carries log2 e).
-#include <algorithm>
-#include <atomic>
-#include <climits>
-#include <cmath>
-#include <type_traits>
-
-#include "latent4.cuh"
-#include "smla_internal.h"
+#include "attend_work.cuh"
 
 namespace smla {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxHeads = 128;
-constexpr int kMaxContext = INT_MAX - 1023;  // a tile's rounding up and a range's start stay below 2^31 from there
-
-struct DenseArgs {
-  KernelLayout L;
-  int n_heads, layer;
-  float scale_log2;  // softmax_scale * log2(e)
-  const uint8_t* pool;
-  const __nv_bfloat16 *q, *q_pe;
-  const int32_t *block_table, *seq_lens, *qsl;
-  int bt_stride, batch, n_tokens;
-  // Positions of a sequence that are visited at most: those of its block-table row, kMaxContext at most.  In 64 bits:
-  // compared in 32, the code around came out 1 % slower on a batch of short units (1,023 us against 1,011).
-  int64_t most;
-  __nv_bfloat16* out;
-  float* lse;  // or nullptr
-  unsigned* err;
-};
-
-// Positions that the i-th of n_q query tokens of a sequence of len positions sees: len - n_q + i + 1, at least
-// none and at most A.most.
-__device__ __forceinline__ int64_t visible(const DenseArgs& A, int len, int i, int n_q) {
-  const int64_t n = static_cast<int64_t>(len) - n_q + i + 1;
-  return n < 0 ? 0 : n < A.most ? n : A.most;
-}
-
 // ---------------------------------------------------------------------------
 // Shapes without a tensor-core kernel: fp32 throughout.  One CTA per (query token, 8 heads); keys in
 // tiles of 32, dequantised into shared memory; warp h scores head h (a lane per key), then every
@@ -228,9 +194,8 @@ smla_status_t launch_dense_fp32(const DenseArgs& A, cudaStream_t s) {
 //   5 ragged chunks on short contexts        1.01 ms, 0.73 PFLOP/s at 128 heads (the cut, see launch_dense_pair)
 //   one token at one position                15 us, the chain plan -> queries -> tile -> results -> merge
 // ---------------------------------------------------------------------------
-constexpr int kRows = 128, kKeys = 128;      // of a pair
+constexpr int kRows = 128;                   // of a pair (and kKeys keys)
 constexpr int kCtaRows = 64, kCtaKeys = 64;  // of a CTA
-constexpr int kDL = 512, kDR = 64, kChunks = 9;  // 64-dim chunks: 8 latent, 1 rope
 constexpr int kSoftmaxWarps = 8, kKWarps = 8, kVWarps = 8;
 constexpr int kKeysPerK = kCtaKeys / kKWarps, kKeysPerV = kCtaKeys / kVWarps;  // of a warp, in a tile
 constexpr int kFirstK = kSoftmaxWarps, kFirstV = kFirstK + kKWarps, kIssuer = kFirstV + kVWarps;
@@ -239,15 +204,9 @@ constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kKRegs = 72, kVRegs = 48, kI
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kKWarps * kKRegs + kVWarps * kVRegs + 4 * kIssuerRegs) <=
                   kThreads * kLaunchRegs,
               "register split exceeds the launch");
-// The running maximum moves when a score passes it by 2^8: few tiles rescale O (2^12 was no faster).
-constexpr float kRescale = 8.0f;
-// P is formed 2^7 times as large, 2^15 at most: fp16's last step, 2^-24, is then 2^-31 of a row's largest weight at
-// most.  Without it a long tail 17 nats below one position rounded to zeros in P but not in the sum that divides.
-constexpr float kLift = 7.0f;
 // A scale rounds to fp16 before it multiplies: 146.125 is the last value whose product with code 448 stays finite
 // (65,464; 146.25 gives 65,520, which rounds to infinity), and from half way between them a scale rounds up.
 constexpr float kScaleEnd = 146.1875f;
-constexpr uint32_t kHalfEnd = 0x4780;  // bf16 of 65536, the first bf16 value that fp16 does not reach
 // Below 2^-13 a scale would lose bits in fp16 (from 2^-14 on).  Such a scale is taken times 2^19, which keeps its
 // products (at most 448 x 2^6) in range, and what was stored is multiplied by 2^-19 in a second pass: exact down to
 // fp16's smallest normal value, within half its step (2^-25) below.  A second pass over the few tiles that need
@@ -259,7 +218,6 @@ template <bool k4>
 constexpr int kRopeOff = k4 ? kDL / 2 + kDL / kGroup4 : kDL + 16;
 template <bool k4>
 constexpr int kRec = kRopeOff<k4> + 2 * kDR;
-constexpr int kMinTiles = 2;  // key tiles a pair takes at least (1 to 4: the same)
 // Tiles requested into L2 ahead of the loads (1 to 16: the same; none: decode steps 2 % slower, a chunk 1 %).
 constexpr int kPrefetchAhead = 4;
 
@@ -281,136 +239,17 @@ struct __align__(1024) PairSmem {
 constexpr size_t kPairSmemBytes = sizeof(PairSmem) + 1024;
 static_assert(kPairSmemBytes <= 232448, "shared memory");
 
-// The unit that begins in a pair's range and goes on in the next pairs' (ntok = 0: none): its parts are
-// slot 2 p + 1 of this pair and slot 2 r of every pair r > p whose range begins before `end`.
-struct PairMeta {
-  int64_t end, total;  // one past the unit's last tile; all work, divided evenly over `pairs`
-  int pairs, tok0, ntok;
-};
-
 struct PairArgs {
   DenseArgs D;
   int group;        // query tokens of a unit: as many as fit 128 rows
+  int unit_cost;    // of a unit beside its tiles, in tiles
   float abs_scale;  // |softmax_scale| log2(e)
   float sign;       // of softmax_scale, applied to the queries
   bool q_vec;       // q and q_pe are 16-byte aligned
   float *part_out, *part_lse;  // partial results, slots [2 pairs][128 rows]; nullptr: units are not split
-  PairMeta* meta;   // [pairs]
+  PartMeta* meta;   // [pairs]
   const uint8_t* records;               // the layer's records in block 0
-  uint32_t bs_mul, bs_shift1, bs_shift2;  // division by block_size
-};
-
-// sum_{g < n} floor((a g + b) / m), with a n + b and the sums of the descent below 2^32 (Euclid's algorithm
-// on the lattice points below a line).
-__device__ __noinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  int64_t s = 0;
-  while (n > 0) {
-    s += static_cast<int64_t>(n - 1) * n / 2 * (a / m) + static_cast<int64_t>(n) * (b / m);
-    a %= m;
-    b %= m;
-    const uint32_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
-  }
-  return s;
-}
-
-// A unit is `group` query tokens of a sequence (fewer at its end) with the key tiles its last token sees
-// (at least one, so that tokens which see nothing are written too).
-__device__ __forceinline__ int unit_tiles(const PairArgs& A, int len, int g, int n_q) {
-  const int last = min((g + 1) * A.group, n_q) - 1;
-  return max(1, static_cast<int>((visible(A.D, len, last, n_q) + kKeys - 1) / kKeys));
-}
-
-// Work of the first g units of a sequence of len positions and n_q query tokens: their tiles, or their
-// number where units are not split.
-__device__ int64_t work_before(const PairArgs& A, int len, int g, int n_q) {
-  if (A.part_out == nullptr) return g;
-  const int units = (n_q + A.group - 1) / A.group;
-  if (units == 1) return g == 0 ? 0 : unit_tiles(A, len, 0, n_q);
-  if (len >= n_q && len <= A.D.most) {
-    const int whole = min(g, units - 1);
-    int64_t s = floor_sum(whole, kKeys, A.group, len - n_q + A.group + kKeys - 1);
-    if (g == units) s += (len + kKeys - 1) / kKeys;
-    return s;
-  }
-  int64_t s = 0;
-  for (int i = 0; i < g; ++i) s += unit_tiles(A, len, i, n_q);
-  return s;
-}
-
-// The units of this pair in turn.  Positions count tiles from the start of the pair's range: the unit
-// begins at `rel` (below zero if an earlier pair began it) and the range ends at `len`.
-struct Walk {
-  int b, g, q0, n_q, nvis, rel, len, seq_len;
-  __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
-    b = sm.b;
-    g = sm.g;
-    rel = sm.rel;
-    len = sm.len;
-    q0 = sm.q0;
-    n_q = sm.n_q;
-    seq_len = sm.seq_len;
-    if (on()) unit(A);
-  }
-  __device__ __forceinline__ bool on() const { return rel < len; }
-  __device__ __forceinline__ int tok0(const PairArgs& A) const { return q0 + g * A.group; }
-  __device__ __forceinline__ int ntok(const PairArgs& A) const { return min(A.group, n_q - g * A.group); }
-  // Rows of this CTA: the first half of the unit's rows, or the others.
-  __device__ __forceinline__ int rows_before(const PairArgs& A, int cta) const { return cta * ((ntok(A) * A.D.n_heads + 1) / 2); }
-  __device__ __forceinline__ int rows(const PairArgs& A, int cta) const {
-    const int all = ntok(A) * A.D.n_heads, first = (all + 1) / 2;
-    return cta == 0 ? first : all - first;
-  }
-  __device__ __forceinline__ int tiles() const { return max(1, (nvis + kKeys - 1) / kKeys); }
-  // the pair's tiles [ta, tb) of the unit
-  __device__ __forceinline__ int ta(const PairArgs& A) const { return A.part_out != nullptr ? max(-rel, 0) : 0; }
-  __device__ __forceinline__ int tb(const PairArgs& A) const {
-    return A.part_out != nullptr ? min(tiles(), len - rel) : tiles();
-  }
-  __device__ __forceinline__ void unit(const PairArgs& A) {
-    nvis = static_cast<int>(visible(A.D, seq_len, g * A.group + ntok(A) - 1, n_q));
-  }
-  __device__ __forceinline__ void next(const PairArgs& A) {
-    rel += A.part_out != nullptr ? tiles() : 1;
-    if (!on()) return;
-    if (++g * A.group >= n_q) {
-      g = 0;
-      q0 += n_q;
-      int end;
-      do end = __ldg(A.D.qsl + ++b + 1);
-      while (end == q0);
-      n_q = end - q0;
-      seq_len = __ldg(A.D.seq_lens + b);
-    }
-    unit(A);
-  }
-};
-
-// A walk tile by tile.
-struct TileWalk {
-  Walk w;
-  int tile, tb;
-  __device__ __forceinline__ bool on() const { return w.on(); }
-  __device__ __forceinline__ void enter(const PairArgs& A) {
-    tile = w.on() ? w.ta(A) : 0;
-    tb = w.on() ? w.tb(A) : 0;
-  }
-  __device__ __forceinline__ void start(const PairArgs& A, const PairSmem& sm) {
-    w.start(A, sm);
-    enter(A);
-  }
-  __device__ __forceinline__ void next(const PairArgs& A) {
-    if (!w.on()) return;
-    if (++tile >= tb) {
-      w.next(A);
-      enter(A);
-    }
-  }
+  PageDiv pages;    // division by block_size
 };
 
 // ---- cluster and two-SM instructions ----
@@ -440,17 +279,6 @@ __device__ __forceinline__ void raise_abort(unsigned* err, int* abort, bool time
   if (timeout) latch_error(err, SMLA_ERR_TIMEOUT);
   for (uint32_t r = 0; r < 2; ++r)
     asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(map_cta(smem_u32(abort), r)) : "memory");
-}
-// Non-blocking test of a barrier's phase.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // Bounded wait as mbar_wait; a wait that gives up raises the abort flag of both CTAs.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, unsigned* err, int* abort) {
@@ -495,19 +323,6 @@ __device__ __forceinline__ void mma2_f16(uint32_t d, uint32_t a_lo, uint32_t a_h
       "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
-// f(integral_constant 0) .. f(integral_constant N - 1)
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void unrolled(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    unrolled<N, I + 1>(f);
-  }
-}
 // Arrive on `bar` of both CTAs when every MMA issued so far by the elected lane has completed.
 __device__ __forceinline__ void commit2(uint64_t* bar, uint32_t elected) {
   asm volatile(
@@ -517,16 +332,6 @@ __device__ __forceinline__ void commit2(uint64_t* bar, uint32_t elected) {
       "h"(static_cast<uint16_t>(3)), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Eight E4M3 codes times a scale as fp16.  The codes are exact in fp16; the scale (two halves) rounds to 11
 // bits and the product once more (2 x 2^-11 in all).
 __device__ __forceinline__ uint4 dequant8(const uint2& codes, uint32_t sc) {
@@ -554,12 +359,6 @@ __device__ __forceinline__ bool small_scale(float s) { return fabsf(s) < kSmallS
 
 // What unreadable records read as (bad block ids, and nothing left to read): 16 records of zeros.
 __device__ uint4 g_zero_records[16 * 41];
-
-// Page of position j: j / block_size by multiplication (Granlund and Montgomery's round-up method).
-__device__ __forceinline__ int page_of(const PairArgs& A, int j) {
-  const uint32_t t = __umulhi(static_cast<uint32_t>(j), A.bs_mul);
-  return static_cast<int>((t + ((static_cast<uint32_t>(j) - t) >> A.bs_shift1)) >> A.bs_shift2);
-}
 
 // Record of a page's token `off`, in 64 bits: a page may hold more than 2^31 bytes of records.
 template <bool k4>
@@ -605,144 +404,6 @@ struct Records {
   }
 };
 
-// (a, b) * (c, c) + (d, d) and (a, b) + (c, d) as packed fp32 operations
-__device__ __forceinline__ float2 fma2(float2 a, float c, float d) {
-  uint64_t r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %3};\n\tmov.b64 z, {%4, %4};\n\t"
-      "fma.rn.f32x2 %0, x, y, z;\n\t}"
-      : "=l"(r)
-      : "f"(a.x), "f"(a.y), "f"(c), "f"(d));
-  return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tadd.rn.f32x2 %0, x, y;\n\t}"
-      : "=l"(r)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return make_float2(__uint_as_float(static_cast<uint32_t>(r)), __uint_as_float(static_cast<uint32_t>(r >> 32)));
-}
-
-// The pair's range of work.  Threads take the sequences in turn and a scan over the CTA finds the total and
-// the sequence in which the range begins (again from the start if there are more sequences than
-// threads); the first warp then looks for the unit.
-__device__ __forceinline__ void plan(const PairArgs& A, PairSmem& sm, int pair, int n_pairs) {
-  int64_t* warp_sum = reinterpret_cast<int64_t*>(sm.red);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int batch = A.D.batch;
-  int64_t total = -1, x0 = 0, x1 = 0, carry = 0;
-#pragma unroll 1
-  for (int c0 = 0;;) {
-    const int b = c0 + threadIdx.x;
-    int64_t mine = 0;
-    int q0 = 0, n_q = 0, len = 0;
-    if (b < batch) {
-      q0 = __ldg(A.D.qsl + b);
-      n_q = __ldg(A.D.qsl + b + 1) - q0;
-      len = __ldg(A.D.seq_lens + b);
-      if (n_q > 0) mine = work_before(A, len, (n_q + A.group - 1) / A.group, n_q);
-      if (blockIdx.x == 0 && n_q > 0 && len > A.D.most)
-        latch_error(A.D.err, SMLA_ERR_BAD_INDEX);
-    }
-    int64_t incl = mine;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int64_t lo = carry + incl - mine;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) lo += warp_sum[w];
-      carry += warp_sum[w];
-    }
-    c0 += kThreads;
-    if (total < 0 && c0 >= batch) {  // the total is known: the pair's range, and the first sequences again if need be
-      total = carry;
-      const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / kMinTiles : total));
-      x0 = pair < P ? pair * total / P : total;
-      x1 = pair < P ? (pair + 1) * total / P : total;
-      if (threadIdx.x == 0) {
-        sm.x0 = x0;
-        sm.len = static_cast<int>(x1 - x0);
-        sm.total = total;
-        sm.pairs = static_cast<int>(P);
-        sm.rel = 0;
-      }
-      if (batch > kThreads) {
-        c0 = 0;
-        carry = 0;
-        continue;
-      }
-    }
-    if (total >= 0) {
-      if (x0 < x1 && mine > 0 && lo <= x0 && x0 < lo + mine) {
-        sm.b = b;
-        sm.seq_at = lo;
-        sm.q0 = q0;
-        sm.n_q = n_q;
-        sm.seq_len = len;
-      }
-      if (c0 >= batch) break;
-    }
-  }
-  __syncthreads();
-  if (warp == 0 && x0 < x1) {
-    const int n_q = sm.n_q, len = sm.seq_len;
-    const int64_t at = x0 - sm.seq_at;
-    int ga = 0, gb = (n_q + A.group - 1) / A.group - 1;  // the last unit that begins at or before the range is in [ga, gb]
-#pragma unroll 1
-    while (ga < gb) {
-      const int step = (gb - ga + 31) / 32, g = ga + (lane + 1) * step;
-      const int past = __popc(__ballot_sync(0xffffffffu, g <= gb && work_before(A, len, g, n_q) <= at));
-      ga += past * step;
-      gb = min(gb, ga + step - 1);
-    }
-    if (lane == 0) {
-      sm.g = ga;
-      sm.rel = -static_cast<int>(at - work_before(A, len, ga, n_q));
-    }
-  }
-}
-
-// A lane's part of a query row: 16 latent and 2 rope dims, as nine pairs.
-__device__ __forceinline__ void load_query(const PairArgs& A, int64_t row, int lane, uint32_t (&v)[9]) {
-  const __nv_bfloat16* src = A.D.q + row * kDL + 16 * lane;
-  const __nv_bfloat16* pe = A.D.q_pe + row * kDR + 2 * lane;
-  if (A.q_vec) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    v[8] = __ldg(reinterpret_cast<const uint32_t*>(pe));
-  } else {
-    const uint16_t* u = reinterpret_cast<const uint16_t*>(src);
-    const uint16_t* w = reinterpret_cast<const uint16_t*>(pe);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] = u[2 * x] | (static_cast<uint32_t>(u[2 * x + 1]) << 16);
-    v[8] = w[0] | (static_cast<uint32_t>(w[1]) << 16);
-  }
-}
-
-// Lane i of a group of four holds four items of four words; afterwards item j is what lane j held as item i.
-__device__ __forceinline__ void transpose4(uint32_t (&o)[16], bool hi1, bool hi2) {
-#pragma unroll
-  for (int st = 1; st <= 2; st <<= 1) {
-    const bool hi = st == 1 ? hi1 : hi2;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if ((j & st) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * j + i] : o[4 * (j | st) + i], st);
-          if (hi) o[4 * j + i] = got;
-          else o[4 * (j | st) + i] = got;
-        }
-      }
-    }
-  }
-}
-
 template <bool kRuns, bool k4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_pair_kernel(const PairArgs A) {
   extern __shared__ uint8_t smem_raw[];
@@ -776,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   cudaTriggerProgrammaticLaunchCompletion();  // the merge may be launched; it waits for this grid's end
-  plan(A, sm, pair, n_pairs);
+  plan<kThreads>(A, sm, pair, n_pairs);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before either arrives on the other's
@@ -1394,119 +1055,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) dense_p
   }
 }
 
-// Joins the parts of units that ran on several pairs: lse = ln sum e^lse_i, out = sum e^(lse_i - lse) out_i
-// in fp32.  A warp takes a row (a lane 16 dims) where a few parts are to be joined; where there are many, as
-// for one long sequence, the block's four warps share it (a lane 4 dims, eight parts' loads in flight).
-// With the whole call's time: one sequence of 262,143 positions 95 us (117 with a warp per row), 64 sequences of
-// four tokens 645 us (655 with a block per row).
-constexpr int kMergeThreads = 128, kFewParts = 4;
-template <int kStep>
-__device__ __forceinline__ void merge_row(const PairMeta& M, int p, int parts, int row, int quarter0, int quarters,
-                                          const float* part_lse, const float* part_out, int n_heads, __nv_bfloat16* out, float* lse) {
-  const int lane = threadIdx.x & 31;
-  const auto slot = [&](int i) -> int64_t { return i == 0 ? 2 * p + 1 : 2 * (p + i); };
-  float v[kMaxPairs / 32], mx = -INFINITY, z = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxPairs / 32; ++i) {
-    v[i] = 32 * i + lane < parts ? __ldcg(part_lse + slot(32 * i + lane) * kRows + row) : -INFINITY;
-    mx = fmaxf(mx, v[i]);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-  for (int i = 0; i < kMaxPairs / 32; ++i) {
-    v[i] = expf(v[i] - base);  // NaN stays NaN
-    z += v[i];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int64_t orow = static_cast<int64_t>(M.tok0) * n_heads + row;
-#pragma unroll 1
-  for (int q = quarter0; q < quarter0 + quarters; q += kStep == 2 ? 4 : 1) {
-    constexpr int kQ = kStep == 2 ? 4 : 1;  // quarters at once
-    float4 acc[kQ];
-#pragma unroll
-    for (int y = 0; y < kQ; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += kStep) {
-      float4 a[kStep][kQ];
-      float f[kStep];
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const int part = min(i0 + i, parts - 1);
-        const float w = part < 32 ? v[0] : part < 64 ? v[1] : part < 96 ? v[2] : v[3];
-        f[i] = __shfl_sync(0xffffffffu, w, part & 31) * inv;
-        if (i0 + i >= parts) f[i] = 0.f;
-#pragma unroll
-        for (int y = 0; y < kQ; ++y)
-          a[i][y] = __ldcg(reinterpret_cast<const float4*>(part_out + (slot(part) * kRows + row) * kDL + 128 * (q + y)) + lane);
-      }
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-#pragma unroll
-        for (int y = 0; y < kQ; ++y) {
-          acc[y].x += f[i] * a[i][y].x;
-          acc[y].y += f[i] * a[i][y].y;
-          acc[y].z += f[i] * a[i][y].z;
-          acc[y].w += f[i] * a[i][y].w;
-        }
-      }
-    }
-#pragma unroll
-    for (int y = 0; y < kQ; ++y)
-      reinterpret_cast<uint2*>(out + orow * kDL + 128 * (q + y))[lane] =
-          make_uint2(pack_bf16x2(acc[y].x, acc[y].y), pack_bf16x2(acc[y].z, acc[y].w));
-  }
-  if (quarter0 == 0 && lane == 0 && lse != nullptr) lse[orow] = z == 0.f ? -INFINITY : mx + logf(z);
-}
-
-// Starts while the pairs still write what it reads.  So the reads come after its wait for them, are ordinary ones
-// and not of the read-only path, which stands for data that no one writes while the kernel lives, and no pointer
-// is marked as free of aliases, so that none of them moves before the wait.
-__global__ void __launch_bounds__(kMergeThreads) dense_merge_kernel(const PairMeta* meta, const float* part_lse,
-                                                                    const float* part_out, int n_pairs, int n_heads,
-                                                                    __nv_bfloat16* out, float* lse) {
-  __shared__ int cum[kMaxPairs + 1];  // rows to join of the pairs before p
-  static_assert(kMergeThreads == kMaxPairs, "a thread per pair");
-  const int tid = threadIdx.x, warp = tid >> 5;
-  cudaGridDependencySynchronize();
-  cum[tid + 1] = tid < n_pairs ? meta[tid].ntok * n_heads : 0;
-  if (tid == 0) cum[0] = 0;
-  __syncthreads();
-#pragma unroll 1
-  for (int o = 1; o < kMaxPairs; o <<= 1) {
-    const int v = tid + 1 > o ? cum[tid + 1 - o] : 0;
-    __syncthreads();
-    cum[tid + 1] += v;
-    __syncthreads();
-  }
-  const int total = cum[kMaxPairs];
-  const auto join = [&](int item, bool few) {
-    int p = 0, hi = n_pairs - 1;
-    while (p < hi) {
-      const int mid = (p + hi + 1) / 2;
-      if (cum[mid] <= item) p = mid;
-      else hi = mid - 1;
-    }
-    const PairMeta M = meta[p];
-    // pairs p + 1 .. carry the rest: range r begins at floor(r total / pairs), before the unit's end for
-    // r < end pairs / total
-    const int n = static_cast<int>(min((M.end * M.pairs + M.total - 1) / M.total, static_cast<int64_t>(M.pairs))) - p;
-    if (few && n <= kFewParts) merge_row<2>(M, p, n, item - cum[p], 0, 4, part_lse, part_out, n_heads, out, lse);
-    if (!few && n > kFewParts) merge_row<8>(M, p, n, item - cum[p], warp, 1, part_lse, part_out, n_heads, out, lse);
-  };
-#pragma unroll 1
-  for (int item = 4 * blockIdx.x + warp; item < total; item += 4 * gridDim.x) join(item, true);
-#pragma unroll 1
-  for (int item = blockIdx.x; item < total; item += gridDim.x) join(item, false);
-}
-
 // Layouts of the full latent shape.
 bool pair_shape(const KernelLayout& L) { return L.d_latent == kDL && (latent4(L) || L.quant_tile == 128) && L.d_rope == kDR; }
 
-constexpr size_t kMetaBytes = (kMaxPairs * sizeof(PairMeta) + 255) / 256 * 256;
+constexpr size_t kMetaBytes = (kMaxPairs * sizeof(PartMeta) + 255) / 256 * 256;
 constexpr size_t kPartLseBytes = 2 * kMaxPairs * kRows * sizeof(float);
 constexpr size_t kPartOutBytes = size_t(2) * kMaxPairs * kRows * kDL * sizeof(float);
 
@@ -1556,11 +1108,7 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   A.sign = softmax_scale < 0.f ? -1.f : 1.f;
   A.q_vec = (reinterpret_cast<uintptr_t>(D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(D.q_pe) & 15) == 0;
   A.records = D.pool + static_cast<int64_t>(D.layer) * D.L.layer_stride + D.L.rec_off;
-  uint32_t log2 = 0;
-  while ((1ull << log2) < static_cast<uint64_t>(D.L.block_size)) ++log2;
-  A.bs_mul = static_cast<uint32_t>((((1ull << log2) - D.L.block_size) << 32) / D.L.block_size + 1);
-  A.bs_shift1 = log2 > 0 ? 1 : 0;
-  A.bs_shift2 = log2 > 0 ? log2 - 1 : 0;
+  A.pages = page_div(D.L.block_size);
   // Splitting pays wherever units are fewer or more uneven than pairs: 32 decode tokens 188 us (598 without), one
   // long sequence 95 us (4.7 ms), a chunk of 1,024 units 3.89 ms (4.17).  Without a workspace units stay whole.
   // The ranges count tiles only, not the time between units (about four tiles' of each): where short contexts
@@ -1569,7 +1117,7 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   const bool split = workspace != nullptr && workspace_bytes >= kMetaBytes + kPartLseBytes + kPartOutBytes;
   if (split) {
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    A.meta = reinterpret_cast<PairMeta*>(w);
+    A.meta = reinterpret_cast<PartMeta*>(w);
     A.part_lse = reinterpret_cast<float*>(w + kMetaBytes);
     A.part_out = reinterpret_cast<float*>(w + kMetaBytes + kPartLseBytes);
   }
@@ -1578,19 +1126,7 @@ smla_status_t launch_dense_pair(const DenseArgs& D, float softmax_scale, void* w
   else runs ? launch(dense_pair_kernel<true, false>) : launch(dense_pair_kernel<false, false>);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   if (split) {
-    // launched while the pairs still work (its blocks wait for their results before they read)
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(6 * device_sm_count());
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, dense_merge_kernel, static_cast<const PairMeta*>(A.meta), static_cast<const float*>(A.part_lse),
-                           static_cast<const float*>(A.part_out), pairs, D.n_heads, D.out, D.lse) != cudaSuccess)
-      return SMLA_ERR_CUDA;
+    return launch_part_merge<kMaxPairs>(A.meta, A.part_lse, A.part_out, pairs, kRows, D.n_heads, D.out, D.lse, s);
   }
   return SMLA_OK;
 }
@@ -1641,6 +1177,9 @@ extern "C" smla_status_t smla_attend_dense(const smla_layout_t* layout, const sm
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // Units of up to 64 rows have a kernel whose products are not half empty.
+  if (pair_shape(L) && latent4(L) && A.n_heads <= 64 && static_cast<int64_t>(n_tokens) * A.n_heads <= 64ll * batch)
+    return launch_attend4_dense(A, params->softmax_scale, workspace, workspace_bytes, s);
   if (pair_shape(L)) return launch_dense_pair(A, params->softmax_scale, workspace, workspace_bytes, s);
   return launch_dense_fp32(A, s);
 }

@@ -164,4 +164,11 @@ smla_status_t launch_attend(const KernelLayout& L, int n_heads, int top_k, float
                             const void* host_records = nullptr, const int32_t* host_block_map = nullptr,
                             int64_t n_host_blocks = 0, void* split_ws = nullptr, size_t split_ws_bytes = 0);
 
+// launch_attend for E2M1 records of 512 + 64 dims (attend4.cu).
+smla_status_t launch_attend4_select(const KernelLayout& L, int n_heads, int top_k, float softmax_scale, const void* pool, int layer,
+                                    const void* q, const void* q_pe, const int32_t* topk_idx, const int32_t* block_table, int bt_stride,
+                                    const int32_t* query_start_loc, int batch, int tok_begin, int tok_end, void* out, float* lse,
+                                    cudaStream_t stream, unsigned* err, const void* host_records, const int32_t* host_block_map,
+                                    int64_t n_host_blocks, void* split_ws, size_t split_ws_bytes);
+
 }  // namespace smla
