@@ -156,21 +156,31 @@ __device__ __forceinline__ void commit1(uint64_t* bar, uint32_t elected) {
       : "memory");
 }
 
-// Lane l holds, in v[0], the sum (maximum) over the warp's lanes of value l.
+// 16 TMEM lanes x 32 columns.  Thread t of the warp gets, for each group i of 8 columns, columns 8 i + 2 (t % 4) and the next
+// of lane t / 4 (r[4 i], r[4 i + 1]) and of lane t / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values, held as tmem_ld16x256b_x4 gives them: lane l passes the address of row l % 8 of
+// matrix l / 8.
+__device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The sum (maximum) of a pair over the lanes that share lane % 4, in all of them.
 template <bool kMax>
-__device__ __forceinline__ float across32(float (&v)[32], int lane) {
+__device__ __forceinline__ float2 across8(float2 v) {
 #pragma unroll
-  for (int st = 0; st < 5; ++st) {
-    const int off = 16 >> st;
-    const bool upper = (lane & off) != 0;
-#pragma unroll
-    for (int i = 0; i < off; ++i) {
-      const float send = upper ? v[i] : v[i + off], keep = upper ? v[i + off] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, off);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
-    }
+  for (int o = 16; o >= 4; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, v.x, o), y = __shfl_xor_sync(0xffffffffu, v.y, o);
+    v = kMax ? make_float2(fmaxf(v.x, x), fmaxf(v.y, y)) : make_float2(v.x + x, v.y + y);
   }
-  return v[0];
+  return v;
 }
 
 // (a, b) * (c, d) + (e, e) as a packed fp32 operation
@@ -436,11 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     if (bad) latch_error(err, SMLA_ERR_RANGE);
   } else {
     // ------------------------------ queries, softmax, epilogue ------------------------------
-    // Thread: key 32 (warp % 4) + lane of a tile (TMEM lane; a dim of O^T), rows 32 (warp / 4) .. + 31.
+    // Warp: keys 32 (warp % 4) .. + 31 of a tile (TMEM lanes; dims of O^T) and rows 32 (warp / 4) .. + 31.  Of the scores a
+    // thread holds four keys (lane / 4 and every eighth behind it) times eight rows (pairs 8 i + 2 (lane % 4) of those 32),
+    // so that the rows' maxima, factors and sums fit its registers: with one key and 32 rows a thread, maxima and factors
+    // from shared memory, the exponents alone took 700 to 1,000 cycles.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int tid = threadIdx.x, sp = warp & 3, hh = warp >> 2, key = 32 * sp + lane;
     const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
-    const int H = A.D.n_heads;
+    const int H = A.D.n_heads, row0 = 32 * hh + 2 * (lane & 3);
     // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is scaled by
     // a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's eight bits exactly down to
     // 2^-23 of that element.
@@ -500,13 +513,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     if (A.meta != nullptr && tid == 0) A.meta[blockIdx.x].ntok = 0;
     W nx = w;  // the unit whose queries come next
     uint32_t kk = 0, n = 0;
-    float l[32];
+    float2 l[4], m[4], f[4];  // of rows row0 + 8 i and the next: sum, maximum, factor
     bool ok = true;
     // Each turn: the next unit's queries (the last scores are formed, Q is free), the results of the unit before, then
     // the unit's tiles.  A failed wait skips nothing: it is ORed into the next barrier of the eight warps, which leave
     // together.
     for (;; ++n) {
-      if (n > 0) sm.red[sp][32 * hh + lane] = across32<false>(l, lane);
+      if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          l[i] = across8<false>(l[i]);
+          if (lane < 4) *reinterpret_cast<float2*>(&sm.red[sp][row0 + 8 * i]) = l[i];
+        }
+      }
       if (nx.on()) load_q(nx, n & 1);
       if (n > 0) {
         // ---- end of unit ----
@@ -578,8 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
       if (!w.on()) break;
       nx.next(A);
       const int ta = w.ta(A), tb = w.tb(A);
-      const float* f = sm.f[n & 1] + 32 * hh;
-      const float* m = sm.m + 32 * hh;
       // tiles below `full` are seen whole by every row
       int full = 0;
       if constexpr (!kSelect) full = sm.vis[n & 1][0] / kKeys;
@@ -591,61 +608,87 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
       };
       entry = selected(ta);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) l[i] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        l[i] = make_float2(0.f, 0.f);
+        f[i] = *reinterpret_cast<const float2*>(&sm.f[n & 1][row0 + 8 * i]);
+      }
       bool failed = false;
 #pragma unroll 1
       for (int tile = ta; tile < tb; ++tile, ++kk) {
-        const bool there = entry >= 0;
+        const unsigned there = kSelect ? __ballot_sync(0xffffffffu, entry >= 0) : 0xffffffffu;
         if (tile + 1 < tb) entry = selected(tile + 1);
         ok = ok && mbar_wait(&sm.s_full, kk & 1, err, abort);
         __syncwarp();
         tc_fence_after();
-        uint32_t r[32];
+        uint32_t r[2][16];  // keys lane / 4 and + 8, + 16 and + 24
         const auto scores = [&]() {  // what the products say, masked
-          tmem_ld32(tmem_s + lane_base + 32 * hh, r);
-          tmem_ld_wait(r);
+          tmem_ld16x256b_x4(tmem_s + lane_base + 32 * hh, r[0]);
+          tmem_ld16x256b_x4(tmem_s + lane_base + (16u << 16) + 32 * hh, r[1]);
+          tmem_ld_wait(r[0]);
+          tmem_ld_wait(r[1]);
           if constexpr (kSelect) {
-            if (!there) {
+            if (there != 0xffffffffu) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) r[i] = 0xFF800000u;  // -inf
+              for (int x = 0; x < 4; ++x)
+                if (!(there >> (8 * x + (lane >> 2)) & 1)) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) r[x >> 1][4 * i + 2 * (x & 1)] = r[x >> 1][4 * i + 2 * (x & 1) + 1] = 0xFF800000u;  // -inf
+                }
             }
           } else if (tile >= full) {
-            const int at = tile * kKeys + key;
+            const int at = tile * kKeys + 32 * sp + (lane >> 2);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const int4 v = *reinterpret_cast<const int4*>(&sm.vis[n & 1][32 * hh + i]);
-              if (at >= v.x) r[i] = 0xFF800000u;
-              if (at >= v.y) r[i + 1] = 0xFF800000u;
-              if (at >= v.z) r[i + 2] = 0xFF800000u;
-              if (at >= v.w) r[i + 3] = 0xFF800000u;
+            for (int i = 0; i < 4; ++i) {
+              const int2 v = *reinterpret_cast<const int2*>(&sm.vis[n & 1][row0 + 8 * i]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if (at + 8 * x >= v.x) r[x >> 1][4 * i + 2 * (x & 1)] = 0xFF800000u;
+                if (at + 8 * x >= v.y) r[x >> 1][4 * i + 2 * (x & 1) + 1] = 0xFF800000u;
+              }
             }
           }
+        };
+        const auto pair = [&](int x, int i) -> float2 {
+          return make_float2(__uint_as_float(r[x >> 1][4 * i + 2 * (x & 1)]), __uint_as_float(r[x >> 1][4 * i + 2 * (x & 1) + 1]));
         };
         // exponents: (score - m) f + 7, the difference first (it is exact near m, however large both are)
         const auto exponents = [&]() {
           float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 mv = *reinterpret_cast<const float4*>(m + i), fv = *reinterpret_cast<const float4*>(f + i);
-            const float2 a = fma2v(add2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(-mv.x, -mv.y)), make_float2(fv.x, fv.y), kLift);
-            const float2 b = fma2v(add2(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(-mv.z, -mv.w)), make_float2(fv.z, fv.w), kLift);
-            r[i] = __float_as_uint(a.x), r[i + 1] = __float_as_uint(a.y), r[i + 2] = __float_as_uint(b.x), r[i + 3] = __float_as_uint(b.y);
-            top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 a = fma2v(add2(pair(x, i), make_float2(-m[i].x, -m[i].y)), f[i], kLift);
+              r[x >> 1][4 * i + 2 * (x & 1)] = __float_as_uint(a.x);
+              r[x >> 1][4 * i + 2 * (x & 1) + 1] = __float_as_uint(a.y);
+              top = fmaxf(top, fmaxf(a.x, a.y));
+            }
           }
           return top;
         };
+        // A row's maximum moves only when a score passes it by 2^8; only then (and on the first tile) the rows' maxima over
+        // the tile are formed, and the exponents again.  One copy of each part: the loops of all roles share the
+        // instruction cache.
         const bool first = tile == ta;
-        scores();
-        float top = INFINITY;
-        if (!first) top = exponents();
-        // A row's maximum moves only when a score passes it by 2^8; only then (and on the first tile) the rows'
-        // maxima over the tile are formed.
-        if (bar_red_or(1, 32 * kSoftmaxWarps, first || !ok || top > kRescale + kLift)) {
-          if (!first) scores();
-          float v[32];
+        bool form = first;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          scores();
+          if (!form) {
+            const float top = exponents();
+            if (again || !bar_red_or(1, 32 * kSoftmaxWarps, !ok || top > kRescale + kLift)) break;
+            form = true;
+            continue;
+          }
+          form = false;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          sm.red[sp][32 * hh + lane] = across32<true>(v, lane);
+          for (int i = 0; i < 4; ++i) {
+            float2 v = pair(0, i);
+#pragma unroll
+            for (int x = 1; x < 4; ++x) v = make_float2(fmaxf(v.x, pair(x, i).x), fmaxf(v.y, pair(x, i).y));
+            v = across8<true>(v);
+            if (lane < 4) *reinterpret_cast<float2*>(&sm.red[sp][row0 + 8 * i]) = v;
+          }
           if (bar_red_or(1, 32 * kSoftmaxWarps, !ok)) {
             failed = true;
             break;
@@ -665,7 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
             __syncwarp();
             tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l[i] *= sm.alpha[32 * hh + i];
+            for (int i = 0; i < 4; ++i) {
+              const float2 a = *reinterpret_cast<const float2*>(&sm.alpha[row0 + 8 * i]);
+              l[i] = make_float2(l[i].x * a.x, l[i].y * a.y);
+            }
 #pragma unroll 1
             for (int d2 = 0; d2 < 4; ++d2) {
               uint32_t o[32];
@@ -677,20 +723,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
             }
             tmem_st_wait();
           }
-          scores();  // again: the products are still there, and registers for a second copy are not
-          exponents();
-        }
-        uint32_t pw[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 p = make_float2(fast_exp2(__uint_as_float(r[i])), fast_exp2(__uint_as_float(r[i + 1])));
-          const float2 s = add2(make_float2(l[i], l[i + 1]), p);
-          l[i] = s.x, l[i + 1] = s.y;
-          pw[i / 2] = pack_half2(p.x, p.y);
+          for (int i = 0; i < 4; ++i) m[i] = *reinterpret_cast<const float2*>(&sm.m[row0 + 8 * i]);
         }
+        if (failed) break;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          *reinterpret_cast<uint4*>(sm.k[8] + sw128_off(key, 4 * hh + v)) = make_uint4(pw[4 * v], pw[4 * v + 1], pw[4 * v + 2], pw[4 * v + 3]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pw[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 e = pair(x, i), p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            l[i] = add2(l[i], p);
+            pw[x] = pack_half2(p.x, p.y);
+          }
+          store_matrices(smem_u32(sm.k[8]) + sw128_off(key, 4 * hh + i), pw[0], pw[1], pw[2], pw[3]);
+        }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
