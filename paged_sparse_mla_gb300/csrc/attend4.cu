@@ -316,31 +316,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     }
   } else if (warp >= kFirstLoad) {
     // ------------------------------ loaders: 8 keys of a tile each ------------------------------
-    // Eight lanes hold a key: lane j 16 codes (a scale's) of each 128 dims, and 16 bytes of the rope; a lane serves keys
-    // `slot` and slot + 4 of the warp's.  What a quarter-warp stores (a key's 128 dims) goes to eight different 16-byte
-    // slots (lanes of the odd chunk store their second slot first).  All loads of the next tile are asked for behind
-    // the last fence of the one before (a fence waits for loads in flight).
+    // Four lanes hold a key: lane j 32 codes of each 128 dims (16 bytes), their two scales and 32 bytes of the rope, so
+    // that a tile takes seven requests a warp (with eight lanes a key and a byte load for every scale it took eighteen, and
+    // where records lie anywhere the softmax's own requests waited behind them).  The scales come as eight bytes a
+    // lane and are transposed among the four.  A quarter-warp holds keys k and k + 2 and stores their values to
+    // eight different 16-byte slots (lanes of the odd chunk store the second of two slots first).  All loads of the
+    // next tile are asked for behind the last fence of the one before (a fence waits for loads in flight).
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int lw = warp - kFirstLoad, j8 = lane & 7, slot = lane >> 3, odd = j8 >> 2;
-    const int key0 = 8 * lw + slot;
-    const uint32_t dst = (j8 >> 2) * kKeyChunk + sw128_off(key0, 2 * (j8 & 3) + odd), rope_dst = 8 * kKeyChunk + sw128_off(key0, j8);
-    uint2 codes[4][2];
-    uint32_t sc[4][2];
-    uint4 rope[2];
-    int pos[2], blk[2], off[2], seq = 0;  // positions of the tile after next; block ids (INT_MIN: no key) of the next
+    const int lw = warp - kFirstLoad, j4 = lane & 3, odd = j4 >> 1, second = (lane >> 2) & 1;
+    const int key = 8 * lw + ((lane >> 3) & 1) + 2 * second + 4 * (lane >> 4);
+    const uint32_t dst = odd * kKeyChunk + sw128_off(key, 4 * (j4 & 1) + odd);
+    const uint32_t rope_dst = 8 * kKeyChunk + sw128_off(key, 4 * second + j4);
+    uint4 codes[4], rope[2];
+    uint2 sc;
+    int pos = -1, blk = INT_MIN, off = 0, seq = 0;  // position in the tile after next; block id (INT_MIN: no key) in the next
     bool on_next = false, on = false;
     TileWalkOf<W> tw;
     const auto positions = [&]() {
       on_next = tw.on();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        pos[x] = -1;
-        if (!on_next) continue;
-        const int e = tw.tile * kKeys + key0 + 4 * x;
+      pos = -1;
+      if (on_next) {
+        const int e = tw.tile * kKeys + key;
         if constexpr (kSelect) {
-          if (e < A.top_k) pos[x] = __ldg(tw.w.row(A) + e);
+          if (e < A.top_k) pos = __ldg(tw.w.row(A) + e);
         } else {
-          if (e < tw.w.nvis) pos[x] = e;
+          if (e < tw.w.nvis) pos = e;
         }
       }
       seq = tw.w.b;
@@ -348,63 +348,61 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     };
     const auto lookup = [&]() {
       on = on_next;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        blk[x] = INT_MIN;
-        if (pos[x] < 0) continue;
-        const int pg = page_of(A, pos[x]);
-        off[x] = pos[x] - pg * A.D.L.block_size;
-        blk[x] = kSelect && pos[x] >= A.D.most ? -1 : max(__ldg(A.D.block_table + static_cast<int64_t>(seq) * A.D.bt_stride + pg), -1);
-      }
+      blk = INT_MIN;
+      if (pos < 0) return;
+      const int pg = page_of(A, pos);
+      off = pos - pg * A.D.L.block_size;
+      blk = kSelect && pos >= A.D.most ? -1 : max(__ldg(A.D.block_table + static_cast<int64_t>(seq) * A.D.bt_stride + pg), -1);
     };
-    const auto record = [&](int x) -> const uint8_t* {
-      if (blk[x] == INT_MIN) return nullptr;
-      if (blk[x] >= 0 && blk[x] < A.D.L.num_blocks) {
+    const auto record = [&]() -> const uint8_t* {
+      if (blk == INT_MIN) return nullptr;
+      if (blk >= 0 && blk < A.D.L.num_blocks) {
         if (kSelect && A.host_block_map != nullptr) {
-          const int hb = __ldg(A.host_block_map + blk[x]);
+          const int hb = __ldg(A.host_block_map + blk);
           if (hb >= 0 && hb < A.n_host_blocks)
-            return A.host_records + ((static_cast<int64_t>(hb) * A.D.L.n_layers + A.D.layer) * A.D.L.block_size + off[x]) * kRec4;
-          if (hb < 0) return A.records + static_cast<int64_t>(blk[x]) * A.D.L.block_stride + static_cast<int64_t>(off[x]) * kRec4;
+            return A.host_records + ((static_cast<int64_t>(hb) * A.D.L.n_layers + A.D.layer) * A.D.L.block_size + off) * kRec4;
+          if (hb < 0) return A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec4;
         } else {
-          return A.records + static_cast<int64_t>(blk[x]) * A.D.L.block_stride + static_cast<int64_t>(off[x]) * kRec4;
+          return A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec4;
         }
       }
       latch_error(err, SMLA_ERR_BAD_INDEX);
       return nullptr;
     };
     const auto load_tile = [&]() {
+      const uint8_t* r = record();
+      sc = make_uint2(0, 0);
+      rope[0] = rope[1] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint8_t* r = record(x);
-        if (r != nullptr) {
+      for (int p = 0; p < 4; ++p) codes[p] = make_uint4(0, 0, 0, 0);
+      if (r != nullptr) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            codes[p][x] = __ldg(reinterpret_cast<const uint2*>(r + 64 * p) + j8);
-            sc[p][x] = __ldg(r + kScaleOff + 8 * p + j8);
-          }
-          rope[x] = __ldg(reinterpret_cast<const uint4*>(r + kRopeOff4) + j8);
-        } else {
+        for (int p = 0; p < 4; ++p) codes[p] = __ldg(reinterpret_cast<const uint4*>(r + 64 * p) + j4);
+        sc = __ldg(reinterpret_cast<const uint2*>(r + kScaleOff) + j4);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            codes[p][x] = make_uint2(0, 0);
-            sc[p][x] = 0;
-          }
-          rope[x] = make_uint4(0, 0, 0, 0);
-        }
+        for (int x = 0; x < 2; ++x) rope[x] = __ldg(reinterpret_cast<const uint4*>(r + kRopeOff4 + 64 * (x ^ second)) + j4);
       }
+    };
+    // Lane j's pairs of scale bytes 0 .. 3 are those of 128 dims j's lanes 0 .. 3: afterwards sc.x holds the lane's own pairs
+    // for dims 0-127 and 256-383, sc.y for the others.
+    const auto own_scales = [&]() {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, (j4 & 2) ? sc.x : sc.y, 2), keep = (j4 & 2) ? sc.y : sc.x;
+      const uint32_t low = __byte_perm(keep, got, 0x5410), high = __byte_perm(keep, got, 0x7632);  // of lanes j and j ^ 2
+      const uint32_t own = (j4 & 1) ? high : low, other = __shfl_xor_sync(0xffffffffu, (j4 & 1) ? low : high, 1);
+      sc = (j4 & 1) ? make_uint2(other, own) : make_uint2(own, other);
+      if (j4 & 2) sc = make_uint2(__byte_perm(sc.x, 0, 0x1032), __byte_perm(sc.y, 0, 0x1032));
     };
     const auto store = [&](auto h) {
 #pragma unroll
       for (int p = 2 * h(); p < 2 * h() + 2; ++p) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint2 c = codes[p][x];
-          const uint32_t s = scale4_half2(sc[p][x]);
-          uint8_t* to = sm.k[2 * p] + 512 * x + (dst ^ (x << 6));
-          uint8_t* to2 = sm.k[2 * p] + 512 * x + (dst ^ (x << 6) ^ 16);
-          *reinterpret_cast<uint4*>(to) = dequant4x8(odd ? c.y : c.x, s);
-          *reinterpret_cast<uint4*>(to2) = dequant4x8(odd ? c.x : c.y, s);
-        }
+        const uint4 c = codes[p];
+        const uint32_t w = (p & 1 ? sc.y : sc.x) >> (16 * h());
+        const uint32_t s0 = scale4_half2(w & 0xFFu), s1 = scale4_half2((w >> 8) & 0xFFu);
+        uint8_t* to = sm.k[2 * p];
+        *reinterpret_cast<uint4*>(to + dst) = dequant4x8(odd ? c.y : c.x, s0);
+        *reinterpret_cast<uint4*>(to + (dst ^ 16)) = dequant4x8(odd ? c.x : c.y, s0);
+        *reinterpret_cast<uint4*>(to + (dst ^ 32)) = dequant4x8(odd ? c.w : c.z, s1);
+        *reinterpret_cast<uint4*>(to + (dst ^ 48)) = dequant4x8(odd ? c.z : c.w, s1);
       }
     };
     bool bad = false;
@@ -418,6 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
       positions();
       if (threadIdx.x == 32 * kFirstLoad) *static_cast<volatile uint32_t*>(&sm.loaded) = kk + 1;
       if (kk > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.kv_free[0], (kk - 1) & 1, err, abort))) break;
+      bad |= (__vcmpgtu4(sc.x, kScale4Top * 0x01010101u) | __vcmpgtu4(sc.y, kScale4Top * 0x01010101u)) != 0;
+      own_scales();
       store(std::integral_constant<int, 0>{});
       fence_proxy_async();
       __syncwarp();
@@ -435,9 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
           o[i] = pack_half2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
         }
         bad |= (top & 0xFFFFu) >= kHalfEnd || (top >> 16) >= kHalfEnd;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) bad |= sc[p][x] > kScale4Top;
-        *reinterpret_cast<uint4*>(sm.k[0] + 512 * x + (rope_dst ^ (x << 6))) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(sm.k[0] + (rope_dst ^ (x << 6))) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async();
       __syncwarp();
