@@ -18,6 +18,8 @@
 // first products; P^T takes the rope values' place, which are converted last.
 //
 // A CTA per SM walks over an equal range of all units' tiles; parts of units that cross ranges are joined by their lse.
+#include <cstring>
+
 #include "attend_work.cuh"
 
 namespace smla {
@@ -43,7 +45,7 @@ struct __align__(1024) Smem4 {
   float m[kUnitRows], alpha[kUnitRows], inv[kUnitRows];
   float f[2][kUnitRows];          // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
   int vis[2][kUnitRows];          // positions that the row sees
-  uint64_t k_full[2], q_full, s_full, p_full, kv_free[2], final_bar;
+  uint64_t k_full[2], q_raw, q_full, s_full, p_full, kv_free[2], final_bar;
   int64_t x0, total, seq_at;      // the CTA's range of work (plan)
   int pairs, b, g, rel, len, q0, n_q, seq_len;
   int abort;
@@ -57,9 +59,11 @@ struct Args4 {
   DenseArgs D;
   int group;        // query tokens of a unit
   int unit_cost;    // of a unit beside its tiles, in tiles
+  int min_tiles;    // work of a CTA at least
   float abs_scale;  // |softmax_scale| log2(e)
   float sign;       // of softmax_scale, applied to the queries
   bool q_vec;       // q and q_pe are 16-byte aligned
+  bool q_tma;       // and their rows come by tensor-map copies
   float *part_out, *part_lse;  // partial results, slots [2 CTAs][slot_rows]; nullptr: units are not split
   PartMeta* meta;   // [CTAs]
   int slot_rows;
@@ -72,6 +76,16 @@ struct Args4 {
   const int32_t* host_block_map;
   int64_t n_host_blocks;
 };
+
+// Sequence of query token t (as seq_of_token), by the whole warp: it counts the sequences that begin at or before t, one
+// round of loads where a search takes one after another.
+__device__ __forceinline__ int seq_of_token_warp(const int32_t* qsl, int batch, int t) {
+  if (batch > 1024) return seq_of_token(qsl, batch, t);
+  int n = 0;
+#pragma unroll 2
+  for (int i = threadIdx.x & 31; i < batch; i += 32) n += __ldg(qsl + i) <= t;
+  return __reduce_add_sync(0xffffffffu, n) - 1;
+}
 
 // Tiles of a row of selected positions up to its last one, at least one.
 __device__ __forceinline__ int selected_tiles(const int32_t* row, int k) {
@@ -106,8 +120,8 @@ struct SelectWalk {
   __device__ __forceinline__ bool cut(const Args4& A) const { return end(A) < A.row_tiles; }
   __device__ __forceinline__ int unit_end(const Args4& A) const { return rel + A.row_tiles; }
   __device__ __forceinline__ void unit(const Args4& A) {
+    b = seq_of_token_warp(A.D.qsl, A.D.batch, tok0(A));
     cap = selected_tiles(row(A), A.top_k);
-    b = seq_of_token(A.D.qsl, A.D.batch, tok0(A));
   }
   __device__ __forceinline__ void next(const Args4& A) {
     rel += A.part_out != nullptr ? A.row_tiles + A.unit_cost : 1;
@@ -124,7 +138,7 @@ struct ContextWalk : Walk {
 __device__ __forceinline__ void select_plan(const Args4& A, Smem4& sm) {
   if (threadIdx.x != 0) return;
   const int64_t per = A.part_out != nullptr ? A.row_tiles + A.unit_cost : 1, total = A.n_units * per;
-  const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), A.part_out != nullptr ? total / kMinTiles : total));
+  const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), A.part_out != nullptr ? total / A.min_tiles : total));
   const int64_t c = blockIdx.x, x0 = c < P ? c * total / P : total, x1 = c < P ? (c + 1) * total / P : total;
   sm.x0 = x0;
   sm.len = static_cast<int>(x1 - x0);
@@ -194,7 +208,8 @@ __device__ __forceinline__ float2 fma2v(float2 a, float2 b, float c) {
 }
 
 template <bool kSelect>
-__global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
+__global__ void __launch_bounds__(kThreads, 1)
+    attend4_kernel(const Args4 A, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap qpe_map) {
   using W = std::conditional_t<kSelect, SelectWalk, ContextWalk>;
   extern __shared__ uint8_t smem_raw[];
   Smem4& sm = *reinterpret_cast<Smem4*>(smem_raw + ((1024u - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023u)) & 1023u));
@@ -206,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
       mbar_init(&sm.k_full[i], kLoadWarps);
       mbar_init(&sm.kv_free[i], 1);
     }
+    mbar_init(&sm.q_raw, 1);
     mbar_init(&sm.q_full, kSoftmaxWarps);
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.p_full, kSoftmaxWarps);
@@ -313,6 +329,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
           prefetch_l2_bulk(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(j - pg * A.D.L.block_size) * kRec4, kRec4);
         }
       }
+    } else if (warp == kIssuer + 2 && A.q_tma) {
+      // The queries of each unit as they lie in memory, into their place, once the unit before has formed its last scores
+      // (rows behind the unit's are other tokens', or zeros behind the last: their columns are not used).
+      uint32_t kk = 0, n = 0;
+      bool ok = true;
+      W w;
+      for (w.start(A, sm); w.on(); w.next(A), ++n) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_raw, kChunks * kRowChunk);
+          const int y = w.tok0(A) * A.D.n_heads;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) tma_load_2d(smem_u32(sm.q[c]), &q_map, c * 64, y, &sm.q_raw);
+          tma_load_2d(smem_u32(sm.q[8]), &qpe_map, 0, y, &sm.q_raw);
+        }
+        __syncwarp();
+        for (const uint32_t end = kk + w.tb(A) - w.ta(A); kk < end && ok; ++kk) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full, kk & 1, err, abort));
+        if (!ok) break;
+      }
+      // leave only after the last copies have landed
+      if (n > 0 || !ok) mbar_drain(&sm.q_raw, (n - (ok ? 1 : 0)) & 1);
     }
   } else if (warp >= kFirstLoad) {
     // ------------------------------ loaders: 8 keys of a tile each ------------------------------
@@ -452,54 +488,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     const int tid = threadIdx.x, sp = warp & 3, hh = warp >> 2, key = 32 * sp + lane;
     const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
     const int H = A.D.n_heads, row0 = 32 * hh + 2 * (lane & 3);
-    // Queries of a unit: warp w loads rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each.  A row is scaled by
-    // a power of two that takes its largest element to [2^8, 2^9): fp16 then holds bf16's eight bits exactly down to
-    // 2^-23 of that element.
-    const auto load_q = [&](const W& w, int buf) {
-      const int rows = w.ntok(A) * H;
+    bool ok = true;
+    // Queries of a unit: warp w takes rows 8 w .. + 7, a lane 16 latent and 2 rope dims of each, from where the copies put
+    // them (rows that are not 16-byte aligned: from memory).  A row is scaled by a power of two that takes its largest
+    // element to [2^8, 2^9): fp16 then holds bf16's eight bits exactly down to 2^-23 of that element.
+    const auto load_q = [&](const W& w, uint32_t n) {
+      const int rows = w.ntok(A) * H, buf = n & 1;
       const int64_t first = static_cast<int64_t>(w.tok0(A)) * H;
       if constexpr (!kSelect) {
         if (tid < kUnitRows)
           sm.vis[buf][tid] = tid < rows ? static_cast<int>(visible(A.D, w.seq_len, w.g * A.group + tid / H, w.n_q)) : INT_MAX;
       }
-      uint32_t v[4][9];
-      const auto ask = [&](int i, int r) {
+      if (A.q_tma && !mbar_wait(&sm.q_raw, n & 1, err, abort)) ok = false;
+      __syncwarp();
+      const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
+#pragma unroll 2
+      for (int r = 8 * warp; r < 8 * warp + 8; ++r) {
+        uint4* at0 = reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]);
+        uint4* at1 = reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + 1 - odd)]);
+        uint32_t* at2 = reinterpret_cast<uint32_t*>(&sm.q[8][sw128_off(r, lane >> 2) + 4 * (lane & 3)]);
+        uint32_t v[9] = {};
+        if (A.q_tma) {
+          const uint4 a = *at0, b = *at1;
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w, v[8] = *at2;
+        } else if (r < rows) {
+          load_query(A, first + r, lane, v);
+          if (odd) {  // the slots' order
 #pragma unroll
-        for (int x = 0; x < 9; ++x) v[i][x] = 0;
-        if (r < rows) load_query(A, first + r, lane, v[i]);
-      };
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ask(i, 8 * warp + i);
-#pragma unroll 1
-      for (int r0 = 8 * warp; r0 < 8 * warp + 8; r0 += 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = r0 + i;
-          uint32_t top2 = 0;  // the largest magnitude (bf16 bits of non-negative values order as integers)
-#pragma unroll
-          for (int x = 0; x < 9; ++x) top2 = __vmaxu2(top2, v[i][x] & 0x7FFF7FFFu);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
-          const int ex = static_cast<int>(top >> 7);  // biased exponent
-          const int up = (ex == 0 || ex == 255) ? 0 : min(126, 127 + 8 - ex);  // zeros, infinities and NaN as they are
-          const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23) * A.sign;
-          uint32_t o[9];
-#pragma unroll
-          for (int x = 0; x < 9; ++x)
-            o[x] = pack_half2(__uint_as_float(v[i][x] << 16) * f, __uint_as_float(v[i][x] & 0xFFFF0000u) * f);
-#pragma unroll
-          for (int x = 0; x < 9; ++x) v[i][x] = v[i + 2][x];
-          const int c = lane >> 2, odd = c & 1, s0 = 2 * (lane & 3);
-          const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
-          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + odd)]) = odd ? o1 : o0;
-          *reinterpret_cast<uint4*>(&sm.q[c][sw128_off(r, s0 + 1 - odd)]) = odd ? o0 : o1;
-          *reinterpret_cast<uint32_t*>(&sm.q[8][sw128_off(r, lane >> 2) + 4 * (lane & 3)]) = o[8];
-          // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
-          if (lane == 0) sm.f[buf][r] = fmaxf(A.abs_scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t u = v[x];
+              v[x] = v[4 + x];
+              v[4 + x] = u;
+            }
+          }
         }
-        if (r0 < 8 * warp + 4) {
-          ask(2, r0 + 4);
-          ask(3, r0 + 5);
-        }
+        uint32_t top2 = 0;  // the largest magnitude (bf16 bits of non-negative values order as integers)
+#pragma unroll
+        for (int x = 0; x < 9; ++x) top2 = __vmaxu2(top2, v[x] & 0x7FFF7FFFu);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+        const int ex = static_cast<int>(top >> 7);  // biased exponent
+        const int up = (ex == 0 || ex == 255) ? 0 : min(126, 127 + 8 - ex);  // zeros, infinities and NaN as they are
+        const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23) * A.sign;
+#pragma unroll
+        for (int x = 0; x < 9; ++x)
+          v[x] = pack_half2(__uint_as_float(v[x] << 16) * f, __uint_as_float(v[x] & 0xFFFF0000u) * f);
+        *at0 = make_uint4(v[0], v[1], v[2], v[3]);
+        *at1 = make_uint4(v[4], v[5], v[6], v[7]);
+        *at2 = v[8];
+        // above zero, so that a masked score (-inf) stays one whatever softmax_scale is
+        if (lane == 0) sm.f[buf][r] = fmaxf(A.abs_scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
       }
       fence_proxy_async();
       __syncwarp();
@@ -512,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
     W nx = w;  // the unit whose queries come next
     uint32_t kk = 0, n = 0;
     float2 l[4], m[4], f[4];  // of rows row0 + 8 i and the next: sum, maximum, factor
-    bool ok = true;
     // Each turn: the next unit's queries (the last scores are formed, Q is free), the results of the unit before, then
     // the unit's tiles.  A failed wait skips nothing: it is ORed into the next barrier of the eight warps, which leave
     // together.
@@ -524,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend4_kernel(const Args4 A) {
           if (lane < 4) *reinterpret_cast<float2*>(&sm.red[sp][row0 + 8 * i]) = l[i];
         }
       }
-      if (nx.on()) load_q(nx, n & 1);
+      if (nx.on()) load_q(nx, n);
       if (n > 0) {
         // ---- end of unit ----
         const int rows = w.ntok(A) * H, ta = w.ta(A);
@@ -767,6 +803,7 @@ smla_status_t launch(Args4& A, float softmax_scale, void* workspace, size_t work
     if (fa.numRegs < kLaunchRegs) return SMLA_ERR_UNSUPPORTED;  // setmaxnreg.inc draws on the launch's registers
     ready[dev].store(true, std::memory_order_release);
   }
+  A.min_tiles = 1;  // one row of 2,048 positions 20.5 us, 22.9 with two
   A.abs_scale = fabsf(softmax_scale) * kLog2e;
   A.sign = softmax_scale < 0.f ? -1.f : 1.f;
   A.q_vec = (reinterpret_cast<uintptr_t>(A.D.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(A.D.q_pe) & 15) == 0;
@@ -784,7 +821,21 @@ smla_status_t launch(Args4& A, float softmax_scale, void* workspace, size_t work
     A.part_lse = reinterpret_cast<float*>(ws + meta);
     A.part_out = reinterpret_cast<float*>(ws + meta + lse);
   }
-  attend4_kernel<kSelect><<<ctas, kThreads, kSmem4Bytes, s>>>(A);
+  CUtensorMap q_map, qpe_map;
+  std::memset(&q_map, 0, sizeof(q_map));
+  std::memset(&qpe_map, 0, sizeof(qpe_map));
+  if (A.q_vec) {
+    EncodeTiledFn enc = encode_tiled();
+    const auto encode = [&](CUtensorMap* map, const __nv_bfloat16* p, cuuint64_t dims) {  // boxes of 64 rows x 64 dims
+      const cuuint64_t size[2] = {dims, static_cast<cuuint64_t>(A.D.n_tokens) * A.D.n_heads}, strides[1] = {2 * dims};
+      const cuuint32_t box[2] = {64, kUnitRows}, step[2] = {1, 1};
+      return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(p), size, strides, box, step,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    A.q_tma = enc != nullptr && encode(&q_map, A.D.q, kDL) && encode(&qpe_map, A.D.q_pe, kDR);
+  }
+  attend4_kernel<kSelect><<<ctas, kThreads, kSmem4Bytes, s>>>(A, q_map, qpe_map);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
   return split ? launch_part_merge<kMaxCtas>(A.meta, A.part_lse, A.part_out, ctas, A.slot_rows, A.D.n_heads, A.D.out, A.D.lse, s) : SMLA_OK;
 }
@@ -795,7 +846,7 @@ smla_status_t launch_attend4_dense(const DenseArgs& D, float softmax_scale, void
   Args4 A{};
   A.D = D;
   A.group = kUnitRows / D.n_heads;
-  A.unit_cost = 2;
+  A.unit_cost = 4;
   A.slot_rows = A.group * D.n_heads;
   return launch<false>(A, softmax_scale, workspace, workspace_bytes, s);
 }
@@ -808,6 +859,7 @@ smla_status_t launch_attend4_select(const KernelLayout& L, int n_heads, int top_
   Args4 A{};
   A.D.L = L;
   A.D.n_heads = n_heads;
+  A.D.n_tokens = tok_end;
   A.D.layer = layer;
   A.D.pool = static_cast<const uint8_t*>(pool);
   A.D.q = static_cast<const __nv_bfloat16*>(q);
@@ -821,7 +873,7 @@ smla_status_t launch_attend4_select(const KernelLayout& L, int n_heads, int top_
   A.D.lse = lse;
   A.D.err = err;
   A.group = 1;
-  A.unit_cost = 2;
+  A.unit_cost = 4;
   A.slot_rows = n_heads;
   A.topk = topk_idx;
   A.top_k = top_k;

@@ -43,7 +43,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 128;                        // of a tile
 constexpr int kDL = 512, kDR = 64, kChunks = 9;   // the full latent shape; 64-dim chunks: 8 latent, 1 rope
-constexpr int kMinTiles = 2;  // key tiles a worker takes at least (1 to 4: the same)
 constexpr int kMaxContext = INT_MAX - 1023;  // a tile's rounding up and a range's start stay below 2^31 from there
 
 
@@ -306,7 +305,7 @@ __device__ __forceinline__ void plan(const Args& A, Smem& sm, int pair, int n_pa
     c0 += kThreads;
     if (total < 0 && c0 >= batch) {  // the total is known: the pair's range, and the first sequences again if need be
       total = carry;
-      const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / kMinTiles : total));
+      const int64_t P = max(static_cast<int64_t>(1), min(static_cast<int64_t>(n_pairs), A.part_out != nullptr ? total / A.min_tiles : total));
       x0 = pair < P ? pair * total / P : total;
       x1 = pair < P ? (pair + 1) * total / P : total;
       if (threadIdx.x == 0) {
@@ -394,7 +393,7 @@ __device__ __forceinline__ void transpose4(uint32_t (&o)[16], bool hi1, bool hi2
 // for one long sequence, the block's four warps share it (a lane 4 dims, eight parts' loads in flight).
 // With the whole call's time: one sequence of 262,143 positions 95 us (117 with a warp per row), 64 sequences of
 // four tokens 645 us (655 with a block per row).
-constexpr int kMergeThreads = 128, kFewParts = 4;
+constexpr int kMergeThreads = 128, kFewParts = 8;
 template <int kMax, int kStep>
 __device__ __forceinline__ void merge_row(const PartMeta& M, int p, int parts, int row, int slot_rows, int quarter0, int quarters,
                                           const float* part_lse, const float* part_out, int n_heads, __nv_bfloat16* out, float* lse) {
@@ -466,28 +465,33 @@ template <int kMax>
 __global__ void __launch_bounds__(kMergeThreads) part_merge_kernel(const PartMeta* meta, const float* part_lse,
                                                                    const float* part_out, int n_pairs, int slot_rows, int n_heads,
                                                                    __nv_bfloat16* out, float* lse) {
-  constexpr int kPer = (kMax + kMergeThreads - 1) / kMergeThreads;  // workers of a thread
-  __shared__ int cum[kPer * kMergeThreads + 1];  // rows to join of the workers before p
+  constexpr int kPer = (kMax + 31) / 32;  // workers of a lane of the first warp
+  __shared__ int cum[32 * kPer + 1];  // rows to join of the workers before p
   const int tid = threadIdx.x, warp = tid >> 5;
   cudaGridDependencySynchronize();
+  if (warp == 0) {
+    int v[kPer], sum = 0;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    const int i = tid + x * kMergeThreads;
-    cum[i + 1] = i < n_pairs ? meta[i].ntok * n_heads : 0;
+    for (int x = 0; x < kPer; ++x) {
+      v[x] = kPer * tid + x < n_pairs ? meta[kPer * tid + x].ntok * n_heads : 0;
+      sum += v[x];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += y;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      cum[kPer * tid + x] = at;
+      at += v[x];
+    }
+    if (tid == 31) cum[32 * kPer] = at;
   }
-  if (tid == 0) cum[0] = 0;
   __syncthreads();
-#pragma unroll 1
-  for (int o = 1; o < kPer * kMergeThreads; o <<= 1) {
-    int v[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) v[x] = tid + x * kMergeThreads + 1 > o ? cum[tid + x * kMergeThreads + 1 - o] : 0;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) cum[tid + x * kMergeThreads + 1] += v[x];
-    __syncthreads();
-  }
-  const int total = cum[kPer * kMergeThreads];
+  const int total = cum[32 * kPer];
   const auto join = [&](int item, bool few) {
     int p = 0, hi = n_pairs - 1;
     while (p < hi) {

@@ -414,3 +414,27 @@ def test_fused_step_is_its_parts(static):
     assert torch.equal(topk, top2)
     torch.testing.assert_close(out.float(), out2.float(), rtol=2.0 ** -7, atol=1e-3)   # the fused step splits rows: other sums
     torch.testing.assert_close(lse, lse2, rtol=1e-5, atol=1e-5)
+
+
+# ---------------------------------- calls that other tests do not make ----------------------------------
+
+def off_alignment(t):
+    """A copy of t whose first element lies 2 bytes behind a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)[1:1 + t.numel()].view(t.shape)
+    buf.copy_(t)
+    return buf
+
+
+def test_queries_that_are_not_16_byte_aligned():
+    """Their rows come by ordinary loads instead of tensor-map copies; the results are the same bits."""
+    for lens, counts in (([700, 130, 1], [1, 1, 1]), ([300, 200], [9, 5])):
+        c = Case4(lens, counts, 64, seed=31)
+        want = c.dense()
+        c.check(want)
+        sel = c.select(256)
+        want_sel = c.sparse(sel)
+        c.q, c.q_pe = off_alignment(c.q), off_alignment(c.q_pe)
+        got, got_sel = c.dense(), c.sparse(sel)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert torch.equal(got_sel[0], want_sel[0]) and torch.equal(got_sel[1], want_sel[1])
+    ok()
