@@ -213,6 +213,13 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r;
 }
+// Requests a record into L2, line by line (kBytes from a multiple of 32 on).
+template <int kBytes>
+__device__ __forceinline__ void prefetch_record(const uint8_t* p) {
+#pragma unroll
+  for (int i = 0; i < kBytes - 1; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i) : "memory");
+  if (kBytes % 128 != 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + kBytes - 1) : "memory");
+}
 // f(integral_constant 0) .. f(integral_constant N - 1)
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void unrolled(F&& f) {
