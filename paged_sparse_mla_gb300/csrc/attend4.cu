@@ -313,21 +313,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           __nanosleep(100);
         }
         __syncwarp();
-#pragma unroll 1
+        // all positions, then all block ids, then the records: one round of latency each
+        int pos[4], blk[4];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = tw.tile * kKeys + 32 * i + lane;
-          int j = -1;
+          pos[i] = -1;
           if constexpr (kSelect) {
-            if (e < A.top_k) j = __ldg(tw.w.row(A) + e);
-            if (j >= A.D.most) j = -1;
+            if (e < A.top_k) pos[i] = __ldg(tw.w.row(A) + e);
           } else {
-            if (e < tw.w.nvis) j = e;
+            if (e < tw.w.nvis) pos[i] = e;
           }
-          if (j < 0) continue;
-          const int pg = page_of(A, j);
-          const int blk = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + pg);
-          if (blk < 0 || blk >= A.D.L.num_blocks || (kSelect && A.host_block_map != nullptr && __ldg(A.host_block_map + blk) >= 0)) continue;
-          prefetch_record<kRec4>(A.records + static_cast<int64_t>(blk) * A.D.L.block_stride + static_cast<int64_t>(j - pg * A.D.L.block_size) * kRec4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          blk[i] = -1;
+          if (pos[i] >= 0 && pos[i] < A.D.most)
+            blk[i] = __ldg(A.D.block_table + static_cast<int64_t>(tw.w.b) * A.D.bt_stride + page_of(A, pos[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (blk[i] < 0 || blk[i] >= A.D.L.num_blocks || (kSelect && A.host_block_map != nullptr && __ldg(A.host_block_map + blk[i]) >= 0)) continue;
+          const int off = pos[i] - page_of(A, pos[i]) * A.D.L.block_size;
+          prefetch_record<kRec4>(A.records + static_cast<int64_t>(blk[i]) * A.D.L.block_stride + static_cast<int64_t>(off) * kRec4);
         }
       }
     } else if (warp == kIssuer + 2 && A.q_tma) {
@@ -336,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kk = 0, n = 0;
       bool ok = true;
       W w;
-      for (w.start(A, sm); w.on(); w.next(A), ++n) {
+      w.start(A, sm);
+      for (; w.on(); ++n) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.q_raw, kChunks * kRowChunk);
           const int y = w.tok0(A) * A.D.n_heads;
@@ -345,7 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(smem_u32(sm.q[8]), &qpe_map, 0, y, &sm.q_raw);
         }
         __syncwarp();
-        for (const uint32_t end = kk + w.tb(A) - w.ta(A); kk < end && ok; ++kk) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full, kk & 1, err, abort));
+        const uint32_t end = kk + w.tb(A) - w.ta(A);
+        w.next(A);  // looked up before the wait, not behind it
+        for (; kk < end && ok; ++kk) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full, kk & 1, err, abort));
         if (!ok) break;
       }
       // leave only after the last copies have landed
