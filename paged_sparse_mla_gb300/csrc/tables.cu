@@ -9,8 +9,11 @@
 //   token k of the entry: position len_r + k, slot block * block_size + position % block_size
 // In whole numbers throughout: the same call gives the same tables whatever the order of its threads.
 //
-// Two launches.  One CTA forms both sums and what depends on them alone; the copies are spread over the SMs.  The
-// second is launched with the first and copies the blocks of cached tokens, which need no sum, before it waits.
+// One CTA forms both sums and what depends on them alone, while others copy the blocks of cached tokens, which need
+// no sum; all others wait for it and then take the new blocks and the tokens.  Only that CTA reads and writes
+// held and free_used, which may therefore be updated in place.  Steps of small tables are one launch, a cluster of up to
+// eight CTAs that meet at its barrier; large ones are two, the second launched with the first and over all SMs
+// (an SM writes 32 bytes a cycle).
 #include <algorithm>
 #include <climits>
 
@@ -20,6 +23,8 @@ namespace smla {
 namespace {
 
 constexpr int kPlanThreads = 1024, kFillThreads = 256, kSegment = 1024;  // kSegment: table entries of a warp's unit
+constexpr int kMaxCluster = 8;  // the portable size
+constexpr int64_t kOneLaunchEntries = 1 << 19, kOneLaunchTokens = 1 << 15;
 constexpr int kSearchEntries = 4096;  // batches whose query_start_loc is searched in shared memory
 constexpr int kMaxContext = INT_MAX - 1023;  // as smla_attend_dense
 
@@ -91,10 +96,9 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* sums, int64_t& total
   return (warp > 0 ? before : 0) + incl - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const TableArgs A) {
+// Sums, lengths and offsets of all entries, by one CTA of kPlanThreads.
+__device__ __forceinline__ void plan_entries(const TableArgs& A, int64_t* sums) {
   static_assert(kPlanThreads == 32 * 32, "scan takes 32 warps");
-  __shared__ int64_t sums[32];
-  cudaTriggerProgrammaticLaunchCompletion();
   const int64_t used0 = *A.free_used;  // read before the last barrier, written after it: the two may be one word
   const int64_t used = min(max(used0, static_cast<int64_t>(0)), A.n_free);
   bool bad = used0 != used, out_of_blocks = false;
@@ -148,13 +152,10 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const TableArgs
   }
 }
 
-__global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableArgs A) {
-  extern __shared__ int32_t loc[];
+// The blocks of cached tokens, by warp `warp` of `warps`: nothing else of this call writes what is read here.
+__device__ __forceinline__ void copy_cached(const TableArgs& A, int64_t warp, int64_t warps) {
   const int lane = threadIdx.x & 31;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFillThreads / 32);
   const int64_t units = static_cast<int64_t>(A.batch) * A.segments;
-  // ---- the blocks of cached tokens: no other kernel of this call writes what is read here ----
   if (A.block_table != nullptr) {
     for (int64_t u = warp; u < units; u += warps) {
       const int i = static_cast<int>(u / A.segments), j0 = static_cast<int>(u % A.segments) * kSegment;
@@ -179,8 +180,16 @@ __global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableArgs
       for (int j = at + lane; j < n; j += 32) dst[j] = src[j];
     }
   }
-  cudaGridDependencySynchronize();  // the plan; what it wrote is read by ordinary loads
-  // ---- blocks behind them: held ones, then new ones ----
+}
+
+// What needs the plan (read by ordinary loads: it was written in this launch or the one beside it), by CTA `cta` of `ctas`.
+template <int kThreads>
+__device__ __forceinline__ void fill(const TableArgs& A, int32_t* loc, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(cta) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t warps = static_cast<int64_t>(ctas) * (kThreads / 32);
+  const int64_t units = static_cast<int64_t>(A.batch) * A.segments;
+  // ---- blocks behind the cached ones: held ones, then new ones ----
   for (int64_t u = warp; u < units; u += warps) {
     const int i = static_cast<int>(u / A.segments), j0 = static_cast<int>(u % A.segments) * kSegment;
     const int4 p = A.plan[i];  // row, held, blocks, len
@@ -201,15 +210,15 @@ __global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableArgs
     }
   }
   // ---- tokens ----
-  if (static_cast<int64_t>(blockIdx.x) * kFillThreads >= A.n_tokens) return;
+  if (static_cast<int64_t>(cta) * kThreads >= A.n_tokens) return;
   const bool near = A.batch <= kSearchEntries;
   if (near) {
-    for (int i = threadIdx.x; i <= A.batch; i += kFillThreads) loc[i] = A.qsl[i];
+    for (int i = threadIdx.x; i <= A.batch; i += kThreads) loc[i] = A.qsl[i];
     __syncthreads();
   }
   const int32_t* q = near ? loc : A.qsl;
   const int total = q[A.batch];
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x; t < A.n_tokens; t += static_cast<int64_t>(gridDim.x) * kFillThreads) {
+  for (int64_t t = static_cast<int64_t>(cta) * kThreads + threadIdx.x; t < A.n_tokens; t += static_cast<int64_t>(ctas) * kThreads) {
     int64_t pos = 0, slot = -1;
     if (t < total) {
       int lo = 0, hi = A.batch - 1;  // the last entry that begins at or before t
@@ -231,6 +240,30 @@ __global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableArgs
     A.positions[t] = pos;
     A.slots[t] = slot;
   }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const TableArgs A) {
+  __shared__ int64_t sums[32];
+  cudaTriggerProgrammaticLaunchCompletion();
+  plan_entries(A, sums);
+}
+
+__global__ void __launch_bounds__(kFillThreads) step_fill_kernel(const TableArgs A) {
+  extern __shared__ int32_t loc[];
+  copy_cached(A, static_cast<int64_t>(blockIdx.x) * (kFillThreads / 32) + (threadIdx.x >> 5), static_cast<int64_t>(gridDim.x) * (kFillThreads / 32));
+  cudaGridDependencySynchronize();  // the plan
+  fill<kFillThreads>(A, loc, blockIdx.x, gridDim.x);
+}
+
+// The whole call as one cluster (the grid): its first CTA plans, the others copy meanwhile.
+__global__ void __launch_bounds__(kPlanThreads) step_tables_kernel(const TableArgs A) {
+  extern __shared__ int32_t loc[];
+  __shared__ int64_t sums[32];
+  const int ctas = gridDim.x, copiers = max(ctas - 1, 1), me = ctas > 1 ? static_cast<int>(blockIdx.x) - 1 : 0;
+  if (blockIdx.x == 0) plan_entries(A, sums);
+  if (me >= 0) copy_cached(A, static_cast<int64_t>(me) * (kPlanThreads / 32) + (threadIdx.x >> 5), static_cast<int64_t>(copiers) * (kPlanThreads / 32));
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  fill<kPlanThreads>(A, loc, blockIdx.x, ctas);
 }
 
 // Whether two ranges of bytes share one.
@@ -300,19 +333,33 @@ extern "C" smla_status_t smla_step_tables(const smla_layout_t* layout, const int
   A.plan = static_cast<int4*>(workspace);
   A.first = reinterpret_cast<int64_t*>(A.plan + batch);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  step_plan_kernel<<<1, kPlanThreads, 0, s>>>(A);
-  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
-  const int64_t units = static_cast<int64_t>(batch) * A.segments, per = kFillThreads / 32;
-  const int64_t want = std::max((units + per - 1) / per, (static_cast<int64_t>(n_tokens) + kFillThreads - 1) / kFillThreads);
+  const int64_t units = static_cast<int64_t>(batch) * A.segments;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, 8 * device_sm_count()))));
-  cfg.blockDim = dim3(kFillThreads);
   cfg.dynamicSmemBytes = batch <= kSearchEntries ? 4 * (static_cast<size_t>(batch) + 1) : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  const int64_t entries = block_table != nullptr ? static_cast<int64_t>(batch) * width : 0;
+  if (entries <= kOneLaunchEntries && n_tokens <= kOneLaunchTokens) {
+    // a CTA for every 32 segments (one a warp) or 4,096 tokens
+    const int64_t want = std::max((units + 31) / 32 + (units > 32 ? 1 : 0), (static_cast<int64_t>(n_tokens) + 4095) / 4096);
+    int ctas = 1;
+    while (ctas < want && ctas < kMaxCluster) ctas *= 2;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    return cudaLaunchKernelEx(&cfg, step_tables_kernel, static_cast<const TableArgs>(A)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  }
+  step_plan_kernel<<<1, kPlanThreads, 0, s>>>(A);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_CUDA;
+  const int64_t per = kFillThreads / 32;
+  const int64_t want = std::max((units + per - 1) / per, (static_cast<int64_t>(n_tokens) + kFillThreads - 1) / kFillThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, 8 * device_sm_count()))));
+  cfg.blockDim = dim3(kFillThreads);
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, step_fill_kernel, static_cast<const TableArgs>(A)) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
