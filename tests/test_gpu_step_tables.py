@@ -150,6 +150,15 @@ def test_tables_of_batches(batch, bs, offset):
     Step(lens, new, bs, held=more, pad=int(rng.integers(0, 500)), seed=batch).check(offset=offset)
 
 
+@pytest.mark.parametrize("offset", [0, 1])
+def test_tables_large_enough_for_two_launches(offset):
+    rng = np.random.default_rng(9)
+    lens = rng.integers(10000, 20000, 600)
+    new = np.where(rng.random(600) < 0.05, rng.integers(0, 300, 600), 1)
+    Step(lens, new, 16, pad=33, seed=1).check(offset=offset)
+    Step(lens[:530], new[:530], 16, pad=33, seed=2, n_free=100).check(offset=offset, in_place=True)
+
+
 def test_a_long_row_and_many_new_blocks():
     Step([262143 * 4, 3], [5, 70000], 16).check()
     Step([0, 9], [300000, 1], 16, pad=7).check()
