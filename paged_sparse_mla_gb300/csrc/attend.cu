@@ -226,7 +226,7 @@ __device__ __forceinline__ void rope_unit(int ur, int& key, int& v) {
 }
 
 // How the producers read records: in 16-code pieces of any shape, or the full shape's records whole; E4M3 or E2M1 codes.
-constexpr int kPieces = 0, kRecords = 1, kPieces4 = 2, kRecords4 = 3;
+constexpr int kPieces = 0, kRecords = 1, kPieces4 = 2;
 
 // Loads for one batch of the producer unit stream (see the key-tile loop):
 // latent units fetch 16 codes and their scale (E4M3: fp32; E2M1: two halves), rope units fetch 8

@@ -802,6 +802,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+// Whether rows of selected positions are cut into parts.  Cut, every CTA has the same work; whole, the last round of rows
+// leaves CTAs idle, but no row is switched to twice and nothing is joined.  Rows are cut where that takes at least 7.5
+// tiles off the longest CTA.  Measured (cut against whole rows), 2,048 positions: 1 token 22 us against 62, 76 tokens 59
+// against 66 (10 tiles off), 160 tokens 95 against 127 (19 off), but 256 tokens 135 against 127 (6.3 off) and 400 tokens
+// 191 against 187 (7.4 off); 1,024 positions: 192 tokens 74 against 76 (8.8 off), 368 tokens 115 against 109 (6.9 off);
+// 512 positions: 4 tokens 21 against 25 (7.8 off), 176 tokens 47 against 45 (6.7 off).
+bool cut_selected(const Args4& A, int ctas) {
+  const int64_t row = A.row_tiles + A.unit_cost, rounds = (A.n_units + ctas - 1) / ctas;
+  return 2 * row * (rounds * ctas - A.n_units) >= 15 * static_cast<int64_t>(ctas);
+}
+
 template <bool kSelect>
 smla_status_t launch(Args4& A, float softmax_scale, void* workspace, size_t workspace_bytes, cudaStream_t s) {
   static std::atomic<bool> ready[kMaxDeviceSlots] = {};
@@ -827,7 +838,7 @@ smla_status_t launch(Args4& A, float softmax_scale, void* workspace, size_t work
   const size_t skipped = workspace != nullptr ? static_cast<size_t>(ws - static_cast<uint8_t*>(workspace)) : 0;
   const size_t meta = up16(ctas * sizeof(PartMeta)), lse = up16(2 * static_cast<size_t>(ctas) * A.slot_rows * sizeof(float));
   const size_t out = 2 * static_cast<size_t>(ctas) * A.slot_rows * kDL * sizeof(float);
-  const bool split = workspace != nullptr && workspace_bytes >= skipped + meta + lse + out;
+  const bool split = workspace != nullptr && workspace_bytes >= skipped + meta + lse + out && (!kSelect || cut_selected(A, ctas));
   if (split) {
     A.meta = reinterpret_cast<PartMeta*>(ws);
     A.part_lse = reinterpret_cast<float*>(ws + meta);

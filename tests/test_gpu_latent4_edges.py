@@ -71,6 +71,15 @@ def test_more_query_tokens_than_positions():
     ok()
 
 
+@pytest.mark.parametrize("tokens", [159, 210])
+def test_more_selections_than_sms(tokens):
+    """Rows cut over the SMs (few more than SMs) and left whole (one SM's last round well filled)."""
+    c = Case4([1300, 700], [tokens - 5, 5], 16, seed=tokens)
+    sel = c.select(1024)
+    c.check(c.sparse(sel), sel)
+    assert all(torch.equal(x, y) for x, y in zip(c.sparse(sel), c.sparse(sel)))
+
+
 @pytest.mark.parametrize("top_k", [1, 127, 129, 4096, 5000])
 def test_selections_of_any_length(top_k):
     c = Case4([6000, 90, 1], [2, 1, 1], 64, seed=top_k)
