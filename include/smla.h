@@ -615,6 +615,7 @@ smla_status_t kvpack_load(const smla_layout_t* layout, const void* pool, int lay
  *               batch's block table
  *   workspace   smla_step_tables_workspace_size(batch) bytes, 16-byte aligned; its contents need
  *               not be kept; calls that may overlap need one each, captured ones among them
+ * lens and new_lens share no memory with seq_lens, query_start_loc or held_out (SMLA_ERR_INVALID_ARG).
  * held_out may be held and free_used_out may be free_used (then a repeated call takes further
  * blocks, as a captured step does); otherwise the call may be repeated.  lens is not changed: the
  * caller adds what it accepts of a step.

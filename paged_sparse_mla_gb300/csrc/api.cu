@@ -138,7 +138,7 @@ smla_status_t check_step(const StepArgs& a) {
       (!a.new_latent || !a.new_idx_k || !a.new_idx_scale || (layout->d_rope > 0 && !a.new_rope)))
     return SMLA_ERR_INVALID_ARG;
   const KernelLayout L = kernel_layout(*layout);
-  if (!pool_fits(L, a.pool)) return SMLA_ERR_INVALID_ARG;
+  if (!pool_fits(L, a.pool, a.out)) return SMLA_ERR_INVALID_ARG;
   if ((a.slot_mapping != nullptr && !store_shape_supported(L)) || !index_shape_supported(L, params->n_idx_heads) ||
       !attend_shape_supported(L, params->n_heads))
     return SMLA_ERR_UNSUPPORTED;
@@ -304,7 +304,7 @@ smla_status_t smla_attend(const smla_layout_t* layout, const smla_params_t* para
     return SMLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return SMLA_OK;
   if (!pool || !q || (layout->d_rope > 0 && !q_pe) || !topk_idx || !block_table || !query_start_loc || !out || !lse ||
-      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool))
+      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool, out))
     return SMLA_ERR_INVALID_ARG;
   DeviceInfo* d;
   smla_status_t st = check_device(&d);
@@ -324,7 +324,7 @@ smla_status_t smla_attend_hisparse(const smla_layout_t* layout, const smla_param
     return SMLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return SMLA_OK;
   if (!pool || !q || (layout->d_rope > 0 && !q_pe) || !topk_idx || !block_table || !query_start_loc || !out || !lse ||
-      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool) || !host_block_map || (n_host_blocks > 0 && !host_records) ||
+      bt_stride <= 0 || !pool_fits(kernel_layout(*layout), pool, out) || !host_block_map || (n_host_blocks > 0 && !host_records) ||
       (reinterpret_cast<uintptr_t>(host_records) & 15) != 0)
     return SMLA_ERR_INVALID_ARG;
   DeviceInfo* d;

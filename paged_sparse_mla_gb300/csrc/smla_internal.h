@@ -75,9 +75,10 @@ bool store_shape_supported(const KernelLayout& L);
 bool index_shape_supported(const KernelLayout& L, int n_idx_heads);
 bool attend_shape_supported(const KernelLayout& L, int n_heads);
 inline bool latent4(const KernelLayout& L) { return L.latent_format == SMLA_LATENT_E2M1; }
-// Records of 4-bit latents are read and written in pieces of 8 and 16 bytes whatever else is aligned.
-inline bool pool_fits(const KernelLayout& L, const void* pool) {
-  return !latent4(L) || (reinterpret_cast<uintptr_t>(pool) & 15) == 0;
+// Records of 4-bit latents are read and written in pieces of 8 and 16 bytes whatever else is aligned, and the outputs of
+// attention over them are stored in such pieces.
+inline bool pool_fits(const KernelLayout& L, const void* pool, const void* out = nullptr) {
+  return !latent4(L) || ((reinterpret_cast<uintptr_t>(pool) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
 }
 
 // Arguments of one fused step (smla_decode and smla_decode_static take the same ones apart from

@@ -300,6 +300,11 @@ extern "C" smla_status_t smla_step_tables(const smla_layout_t* layout, const int
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) != 0 ||
       workspace_bytes < smla_step_tables_workspace_size(batch))
     return SMLA_ERR_INVALID_ARG;
+  // lengths are read while their results are written
+  const auto over_lengths = [&](const void* to, int64_t n) {
+    return overlap(lens, 4 * n_rows, to, 4 * n) || overlap(new_lens, 4ll * batch, to, 4 * n);
+  };
+  if (over_lengths(seq_lens, batch) || over_lengths(query_start_loc, batch + 1ll) || over_lengths(held_out, n_rows)) return SMLA_ERR_INVALID_ARG;
   TableArgs A{};
   const smla_status_t st = checked_device(&A.err);
   if (st != SMLA_OK) return st;

@@ -124,6 +124,34 @@ def test_step_tables_refuses(lib, over):
     assert c_tables(lib, layout(), **over) == INVALID
 
 
+LENS, NEW, SEQ, QSL, HELD = 1 << 12, 1 << 13, 1 << 14, 1 << 15, 1 << 16   # apart, as every result is from the lengths
+
+
+@pytest.mark.parametrize("over,refused", [
+    (dict(), False), (dict(seq=LENS), True), (dict(seq=NEW), True), (dict(qsl=LENS), True), (dict(qsl=NEW - 8), True), (dict(seq=NEW - 8), False),
+    (dict(held_out=LENS - 8), True), (dict(held_out=NEW), True), (dict(seq=LENS + 12), False), (dict(seq=LENS + 8), True),
+])
+def test_step_tables_results_over_the_lengths(lib, over, refused):
+    args = dict(lens=LENS, new=NEW, seq=SEQ, qsl=QSL, held=HELD, held_out=HELD, table=1 << 18)
+    args.update(over)
+    if torch.cuda.is_available() and not refused:
+        pytest.skip("a call with made-up addresses")
+    assert (c_tables(lib, layout(), **args) == INVALID) == refused
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_unaligned_outputs_of_attention_over_4_bit_latents(lib, fmt):
+    lay, prm = layout(fmt=fmt), smla.make_params(64, 64, 64, 0.1)
+    if torch.cuda.is_available() and fmt == "e4m3":
+        pytest.skip("a call with made-up addresses")
+    out = P16 + 8
+    step = (P16, 0, P16, P16, P16, P16, P16, P16, P16, P16, P16, P16, 16, P16, P16, 1, 1, 1, 100, out, P16, None)
+    got = [lib.smla_attend(REF(lay), REF(prm), P16, 0, P16, P16, P16, P16, 4, P16, 1, 1, out, P16, None, 0, None),
+           lib.smla_attend_hisparse(REF(lay), REF(prm), P16, 0, P16, P16, 1, P16, P16, P16, P16, 4, P16, 1, 1, out, P16, None),
+           lib.smla_decode(REF(lay), REF(prm), *step, P16, 1 << 30, None)]
+    assert [g == INVALID for g in got] == [fmt == "e2m1"] * 3
+
+
 def test_step_tables_workspace(lib):
     assert smla.step_tables_workspace_size(10) == 240 and smla.step_tables_workspace_size(0) == 0
 
