@@ -2,7 +2,7 @@
  * smla.h -- C ABI of the GB300 paged top-k sparse-MLA library (libsmla.so).
  *
  * The library computes the data-parallel hot path of top-k sparse MLA over a
- * paged FP8 KV cache held in one shared block pool:
+ * paged KV cache in FP8, or with latents in 4 bits, held in one shared block pool:
  *
  *   kvpack_store       new tokens -> packed FP8 records in the pool
  *   smla_index_scores  per-query-token indexer scores over its visible context
@@ -84,7 +84,7 @@ typedef enum smla_status {
   SMLA_ERR_BAD_INDEX = 4,    /* device saw a block id / slot outside the pool (read clamped) */
   SMLA_ERR_TIMEOUT = 5,      /* a bounded on-device wait gave up            */
   SMLA_ERR_SCRATCH_LIMIT = 6,/* smla_decode_static: one query token's scratch exceeds the static array */
-  SMLA_ERR_RANGE = 7,        /* smla_attend_dense saw a cached value beyond fp16's range */
+  SMLA_ERR_RANGE = 7,        /* attention saw a cached value beyond fp16's range     */
   SMLA_ERR_NO_BLOCKS = 8     /* smla_step_tables found the free list empty (the tokens' slots are -1) */
 } smla_status_t;
 
@@ -127,7 +127,9 @@ typedef enum smla_latent_format {
  *   [block_size indexer key scales, fp32]
  *
  * every region on a 256-byte boundary; a record is
- *   [d_latent e4m3 codes][d_latent/quant_tile fp32 scales][d_rope bf16] (padded to 16 B).
+ *   [d_latent e4m3 codes][d_latent/quant_tile fp32 scales][d_rope bf16] (padded to 16 B),
+ * with E2M1 latents
+ *   [d_latent/2 bytes of codes][d_latent/16 scale bytes][d_rope bf16] (padded to 16 B).
  * Filled in by smla_layout_init(); read-only afterwards.  Every entry point
  * accepts a layout only as smla_layout_init filled it in: it recomputes the
  * derived fields from the shape fields and refuses any difference with
@@ -136,9 +138,9 @@ typedef enum smla_latent_format {
 typedef struct smla_layout {
   int32_t block_size;     /* tokens per block                                  */
   int32_t n_layers;       /* layers packed in one block                        */
-  int32_t d_latent;       /* latent (no-rope) dims, FP8 in the cache           */
+  int32_t d_latent;       /* latent (no-rope) dims, E4M3 or E2M1 in the cache  */
   int32_t d_rope;         /* rope dims, bf16 in the cache                      */
-  int32_t quant_tile;     /* latent elements per fp32 scale                    */
+  int32_t quant_tile;     /* latent elements per scale                         */
   int32_t d_index;        /* indexer key dims (e4m3)                           */
   int64_t num_blocks;     /* pool capacity in blocks                           */
   int32_t n_scales;       /* d_latent / quant_tile                             */
@@ -177,7 +179,8 @@ smla_status_t smla_layout_init_keys(smla_layout_t* layout, int block_size, int n
 
 /* smla_layout_init_keys with the format of the cached latents (an smla_latent_format_t).
  * E2M1 latents need quant_tile 16.  Every call below takes either format; with E2M1 latents
- * the pool is 16-byte aligned in all of them (SMLA_ERR_INVALID_ARG). */
+ * each call that reads or writes records wants a 16-byte aligned pool and the attention calls a
+ * 16-byte aligned `out` (SMLA_ERR_INVALID_ARG). */
 smla_status_t smla_layout_init_latents(smla_layout_t* layout, int block_size, int n_layers, int d_latent,
                                        int d_rope, int quant_tile, int d_index, int key_format,
                                        int latent_format, int64_t num_blocks);
@@ -201,7 +204,8 @@ size_t smla_workspace_size(const smla_layout_t* layout, const smla_params_t* par
  *   idx_scale   fp32 [n_tokens]            copied verbatim
  *   slot_mapping int64 [n_tokens]          physical slot (block*block_size+off); -1 = skip
  * Per quant_tile of the latent: scale = amax/448 (IEEE fp32 division; 1.0 if
- * that is 0), code = E4M3 round-to-nearest-even, saturating, of x/scale.
+ * that is 0), code = E4M3 round-to-nearest-even, saturating, of x/scale.  E2M1 latents:
+ * see smla_latent_format_t.
  * Latent values must be finite.  Slots >= num_blocks*block_size are skipped
  * and latch SMLA_ERR_BAD_INDEX.
  */
@@ -254,7 +258,10 @@ size_t smla_topk_workspace_size(const smla_params_t* params, int n_tokens);
  * all query heads; [AgentX "DeepSeek V4"]: attention runs over the top-k only.
  *   s[h, j] = softmax_scale * (q[t, h] . K[j] + q_pe[t, h] . kpe[j]),
  *   out[t, h] = sum_j softmax_j(s)[h, j] * K[j],  lse[t, h] = ln sum_j exp(s[h, j])
- * with K[j] the dequantised latent and kpe[j] the cached rope.
+ * with K[j] the dequantised latent and kpe[j] the cached rope.  E4M3 latents are rounded to the
+ * bf16 operands of the tensor cores; E2M1 latents are exact there.  E2M1 latents of 512 dims with 64
+ * rope dims run with fp16 operands: a scale byte above 0xE2 or a rope value beyond fp16's range
+ * latches SMLA_ERR_RANGE, and the outputs that read it are not valid.
  *   q        bf16 [n_tokens, n_heads, d_latent]
  *   q_pe     bf16 [n_tokens, n_heads, d_rope]
  *   topk_idx int32 [n_tokens, top_k]; entries < 0 are ignored.  An entry at or
@@ -273,6 +280,8 @@ size_t smla_topk_workspace_size(const smla_params_t* params, int n_tokens);
  *     an equal share of all tokens' position tiles instead; a token whose tiles straddle two
  *     CTAs is merged the same way from two partials.  Without a scratch, each token runs on
  *     one CTA.  The result agrees with the one-CTA path within rounding.
+ *     (E2M1 latents of 512 + 64 dims: with a scratch every CTA takes an equal share of all tokens'
+ *     tiles wherever that takes 7.5 tiles of 128 positions off the longest; else whole tokens.)
  */
 smla_status_t smla_attend(const smla_layout_t* layout, const smla_params_t* params, const void* pool,
                           int layer, const void* q, const void* q_pe, const int32_t* topk_idx,
@@ -290,7 +299,7 @@ size_t smla_attend_workspace_size(const smla_layout_t* layout, const smla_params
  * records ([GLM-5.3 "What is new"]: Hybrid HiSparse decode keeps part of the
  * KV in host memory and fetches the selected entries from there, so decode
  * concurrency is no longer bounded by HBM).  The indexer keys stay in the HBM
- * pool; the 656-byte records of evicted blocks live in a host buffer that the
+ * pool; the records of evicted blocks (656 bytes, 416 with E2M1 latents) live in a host buffer that the
  * GPU reads directly (pinned, mapped host memory: on GB300 the reads go over
  * NVLink-C2C).
  *   host_block_map: int32 [layout.num_blocks] device array; -1 = the block's
@@ -459,7 +468,8 @@ typedef struct smla_rope {
  *       (idx_norm NULL: z = idx_k), then its first d_rope dims rotated if rope->idx_rope
  * all in fp32, y and z not rounded before they are quantised: scale = amax / F,
  * code = round-to-nearest-even, saturating, of y * (F / amax), F = 448 (E4M3) or
- * 6 (E2M1); amax below 2^-100 takes scale 1 and codes 0.
+ * 6 (E2M1 keys); amax below 2^-100 takes scale 1 and codes 0.  E2M1 latents are quantised as
+ * smla_latent_format_t says.
  *   latent       bf16 [n_tokens, d_latent], rows latent_stride elements apart
  *   rope_key     bf16 [n_tokens, d_rope], rows rope_stride elements apart
  *   idx_k        bf16 [n_tokens, d_index], rows idx_k_stride elements apart; NULL
@@ -474,7 +484,7 @@ typedef struct smla_rope {
  * squares and their sum too (in fp32; with eps 0 the sum must not vanish).  The pool is 16-byte
  * aligned, the inputs aligned to their element.  Built for the latents that kvpack_store takes
  * (64, 128, 256 or 512), d_rope <= 64 and d_index of 32, 64, 128 or 256.  The full shape (512 / 64 /
- * 128, tiles of 128) with 16-byte aligned rows (strides a multiple of 8 elements), weights and
+ * 128; E4M3 latents in tiles of 128) with 16-byte aligned rows (strides a multiple of 8 elements), weights and
  * table has a kernel of its own; other calls take about twice as long (15 us against 8, 8,192 tokens).
  */
 smla_status_t kvpack_append(const smla_layout_t* layout, void* pool, int layer, const void* latent,
@@ -549,6 +559,10 @@ smla_status_t smla_query_prep(const smla_layout_t* layout, const smla_params_t* 
  * 2^-14 are held to 2^-25 absolutely and without a status: a quant tile keeps 2^-11 of its largest
  * value where that is at least 2^-14 (6e-5), fewer bits the smaller it is, and none below 2^-25.  A
  * cache of smaller latents is for smla_attend, whose bf16 operands reach down to 2^-126.
+ * E2M1 latents of 512 dims with 64 rope dims run there too and enter the products unrounded; a scale
+ * byte above 0xE2 or a rope value beyond fp16's range latches SMLA_ERR_RANGE (in every shape a scale
+ * byte does).  Of steps of at most 64 rows a sequence on the average (n_tokens * n_heads against
+ * batch, 64 heads or fewer) one CTA takes 64 rows, and the split is over single SMs.
  * Other shapes kvpack_store takes (d_rope <= 64) run in fp32 on the CUDA cores, where a call takes
  * over a hundred times as long (33.6 ms against 0.19, measured on the full shape).
  * The pool is 16-byte aligned.  The same call gives the same bits every time.
@@ -576,9 +590,10 @@ size_t smla_attend_dense_workspace_size(const smla_layout_t* layout, const smla_
  *   rope_out     bf16 [n_rows, d_rope], rows rope_stride >= d_rope apart, or NULL; both may be
  *                columns of one wider array
  * A position outside the block-table row or a block id outside the pool latches
- * SMLA_ERR_BAD_INDEX and its row is zeros.  The pool is 16-byte aligned.  512 + 64 dims (E4M3 latents in
+ * SMLA_ERR_BAD_INDEX and its row is zeros.  The pool is 16-byte aligned, the outputs to their
+ * element, and they do not overlap the pool.  512 + 64 dims (E4M3 latents in
  * tiles of 128) with 16-byte aligned rows (strides a multiple of 8 elements) have a kernel of
- * their own; other calls take a warp per row.
+ * their own (131,072 rows of E2M1 latents: 37 us); other calls take a warp per row.
  */
 smla_status_t kvpack_load(const smla_layout_t* layout, const void* pool, int layer, const int32_t* block_table,
                           int bt_stride, const int32_t* starts, const int32_t* row_loc, int batch, int n_rows,
