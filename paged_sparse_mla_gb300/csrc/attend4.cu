@@ -41,6 +41,7 @@ constexpr float kNoScore = -1e38f;  // running maximum of a row that has seen no
 struct __align__(1024) Smem4 {
   uint8_t k[kChunks][kKeyChunk];  // [128 keys][64 dims] fp16, 128-byte swizzle; the last: rope, then P^T [128 keys][64 rows]
   uint8_t q[kChunks][kRowChunk];
+  uint8_t stage[kSoftmaxWarps][8 * 64];  // results on their way out: 8 rows x 32 dims bf16 of a warp
   float red[4][kUnitRows];
   float m[kUnitRows], alpha[kUnitRows], inv[kUnitRows];
   float f[2][kUnitRows];          // per unit (alternating): |softmax_scale| log2(e) / the row's query factor
@@ -184,6 +185,11 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t (&r)[
 // matrix l / 8.
 __device__ __forceinline__ void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// The same matrices transposed: lane l passes the address of column l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_columns(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // The sum (maximum) of a pair over the lanes that share lane % 4, in all of them.
@@ -593,41 +599,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         named_bar_sync(1, 32 * kSoftmaxWarps);
+        if (!partial) {
+          // A warp's 32 dims x 8 rows at a time: packed as the products' fragments, transposed by the store to shared memory
+          // (slots of 16 bytes XORed by row / 2), and out as 64 bytes a row.
+          uint8_t* stage = sm.stage[warp];
+          float2 inv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) inv[i] = *reinterpret_cast<const float2*>(&sm.inv[row0 + 8 * i]);
+          const uint32_t to = smem_u32(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
+          const uint4* from = reinterpret_cast<const uint4*>(stage + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4));
+          __nv_bfloat16* out = A.D.out + (orow + 32 * hh + (lane >> 2)) * kDL + 32 * sp + 8 * (lane & 3);
 #pragma unroll 1
-        for (int d2 = 0; d2 < 4; ++d2) {
-          if (32 * hh >= rows) break;
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o);
-          tmem_ld_wait(o);
-          const int d = d2 * 128 + key;
-          if (!partial) {
-            // Lane: dim d for 32 rows.  Four rows at a time, a 4x4 transpose within each group of four lanes gives
-            // lane 4 g + i four consecutive dims of row i, which go out as one 8-byte store.
-            const int i4 = lane & 3;
+          for (int d2 = 0; d2 < 4; ++d2) {
+            if (32 * hh >= rows) break;
+            uint32_t o[2][16];
+            __syncwarp();
+            tmem_ld16x256b_x4(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o[0]);
+            tmem_ld16x256b_x4(tmem_o + lane_base + (16u << 16) + d2 * kUnitRows + 32 * hh, o[1]);
+            tmem_ld_wait(o[0]);
+            tmem_ld_wait(o[1]);
 #pragma unroll
-            for (int x0 = 0; x0 < 32; x0 += 4) {
-              float a[4];
+            for (int i = 0; i < 4; ++i) {
+              uint32_t v[4];
 #pragma unroll
-              for (int jj = 0; jj < 4; ++jj) a[jj] = __uint_as_float(o[x0 + jj]) * sm.inv[32 * hh + x0 + jj];
-#pragma unroll
-              for (int st = 2; st >= 1; st >>= 1) {
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                  if ((jj & st) == 0) {
-                    const bool hi = (i4 & st) != 0;
-                    const float got = __shfl_xor_sync(0xffffffffu, hi ? a[jj] : a[jj | st], st);
-                    if (hi) a[jj] = got;
-                    else a[jj | st] = got;
-                  }
-                }
-              }
-              const int r = 32 * hh + x0 + i4;
-              if (r < rows)
-                *reinterpret_cast<uint2*>(A.D.out + (orow + r) * kDL + d - i4) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+              for (int x = 0; x < 4; ++x)
+                v[x] = pack_bf16x2(__uint_as_float(o[x >> 1][4 * i + 2 * (x & 1)]) * inv[i].x, __uint_as_float(o[x >> 1][4 * i + 2 * (x & 1) + 1]) * inv[i].y);
+              store_columns(to, v[0], v[1], v[2], v[3]);
+              __syncwarp();
+              const uint4 w4 = *from;
+              __syncwarp();
+              if (32 * hh + 8 * i + (lane >> 2) < rows) *reinterpret_cast<uint4*>(out + 8 * i * kDL + 128 * d2) = w4;
             }
-          } else {
-            float* to = A.part_out + (part * A.slot_rows + 32 * hh) * kDL + d;
+          }
+        } else {
+#pragma unroll 1
+          for (int d2 = 0; d2 < 4; ++d2) {
+            if (32 * hh >= rows) break;
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(tmem_o + lane_base + d2 * kUnitRows + 32 * hh, o);
+            tmem_ld_wait(o);
+            float* to = A.part_out + (part * A.slot_rows + 32 * hh) * kDL + d2 * 128 + key;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (32 * hh + x < rows) to[x * kDL] = __uint_as_float(o[x]) * sm.inv[32 * hh + x];
