@@ -328,3 +328,23 @@ def test_layers_and_key_formats_share_a_pool():
     a, b = pool.view(4, 2, -1), before.view(4, 2, -1)
     assert torch.equal(a[:, 0], b[:, 0]) and not torch.equal(a[:, 1], b[:, 1])
     ok()
+
+
+@pytest.mark.parametrize("selected", [False, True])
+def test_queries_that_are_not_numbers_stay_by_themselves(selected):
+    """Units of 64 and of 16 rows in turn: rows of NaN and infinite queries change no other row to the bit."""
+    c = Case4([700, 300, 900, 40, 513], [4, 1, 4, 1, 2], 16, seed=77)
+    sel = c.select(256) if selected else None
+    run = (lambda: c.sparse(sel)) if selected else c.dense
+    clean = run()
+    c.check(clean, sel)
+    bad = [(0, 3), (1, 15), (5, 0), (6, 9), (10, 2)]
+    for i, (t, h) in enumerate(bad):
+        c.q[t, h, 7 * i] = float("nan") if i % 2 else float("inf")
+    got = run()
+    torch.cuda.synchronize()
+    keep = torch.ones(c.T, 16, dtype=torch.bool, device="cuda")
+    for t, h in bad:
+        keep[t, h] = False
+    assert all(torch.equal(x[keep], y[keep]) for x, y in zip(clean, got))
+    ok()
