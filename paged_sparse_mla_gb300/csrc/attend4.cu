@@ -18,6 +18,17 @@
 // first products; P^T takes the rope values' place, which are converted last.
 //
 // A CTA per SM walks over an equal range of all units' tiles; parts of units that cross ranges are joined by their lse.
+//
+// Bound by shared memory and the chain.  A tile moves 633 KB through it: 221 of the first products' operands (an MMA of
+// 128 x 64 x 16 reads 6 KB, 48 cycles, where its multiplications take 16), 196 of the second's, 147 stores of converted
+// keys, 53 record loads, 16 of P: 4,950 cycles.  The softmax in between, 1,200 cycles, finds no other work for it, since
+// there is no room for another tile's keys: 6,200 cycles a tile in decode steps, 6,700 over selected positions.  Measured,
+// 64 heads:
+//   32 decode tokens, 8,192 to 32,768 positions    135 us, 2.1 TB/s (the two-SM kernel on the same records 165)
+//   256 tokens, 2,048 selected positions each      126 us, 1.9 TB/s (gathered by the kernel of attend.cu 265)
+//   one token, 2,048 selected positions            21 us: start-up 10, a tile, results, the join
+// Of that, a CTA's start is 10 us (plan, positions, blocks, records and queries one after another, cold code), a switch
+// of units 6 us beside its tiles, the join of parts up to 7 us.
 #include <cstring>
 
 #include "attend_work.cuh"
@@ -28,14 +39,14 @@ namespace {
 constexpr int kUnitRows = 64;
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 16;
 constexpr int kFirstLoad = kSoftmaxWarps, kIssuer = kFirstLoad + kLoadWarps;
-constexpr int kThreads = 32 * (kIssuer + 4);  // the last four: issuer, L2 requests, two without work
+constexpr int kThreads = 32 * (kIssuer + 4);  // the last four: issuer, L2 requests, queries, one without work
 constexpr int kLaunchRegs = 72, kSoftmaxRegs = 112, kLoadRegs = 64, kOtherRegs = 24;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs,
               "register split exceeds the launch");
 constexpr int kMaxCtas = 160;
 constexpr int kKeyChunk = kKeys * 128, kRowChunk = kUnitRows * 128;  // bytes of a 64-dim chunk
 constexpr int kRec4 = kDL / 2 + kDL / kGroup4 + 2 * kDR, kScaleOff = kDL / 2, kRopeOff4 = kDL / 2 + kDL / kGroup4;
-constexpr int kPrefetchAhead = 3;   // tiles requested into L2 ahead of the loads
+constexpr int kPrefetchAhead = 3;   // tiles requested into L2 ahead of the loads (8: the same)
 constexpr float kNoScore = -1e38f;  // running maximum of a row that has seen no score yet
 
 struct __align__(1024) Smem4 {

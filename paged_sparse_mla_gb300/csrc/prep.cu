@@ -429,6 +429,8 @@ __device__ __forceinline__ float half_max8(const float (&x)[8]) {
 // chain slot -> row -> sums -> codes, a launch and, for the chunk, instructions (68 % of the issue slots), not
 // bandwidth.  So as many warps as the SM holds: with 40 registers a thread instead of 32 a chunk from DRAM took
 // 1.3 us more, one token 0.2 less (1, 2 or 8 tokens a CTA: the same).
+// kLatent4: a lane takes 16 dims, a scale's group, so that only the norm needs the other lanes: 12.7 us from DRAM (the
+// quotients are corrected once each, see latent4.cuh).
 constexpr int kAppendTokens = 4;  // of a CTA
 template <bool kFp4, bool kLatent4>
 __global__ void __launch_bounds__(64 * kAppendTokens, 8) append_full_kernel(const AppendArgs A) {

@@ -14,6 +14,10 @@
 // held and free_used, which may therefore be updated in place.  Steps of small tables are one launch, a cluster of up to
 // eight CTAs that meet at its barrier; large ones are two, the second launched with the first and over all SMs
 // (an SM writes 32 bytes a cycle).
+// Bound by latency: the chain rows -> lengths -> two sums over 1,024 threads -> plan -> table -> slots, each a round of
+// loads, and a launch.  A request 8.3 us replayed as a graph (12 a call), 64 requests of up to 262,144 positions with four
+// tokens each 10.3 (13), 1,024 requests of up to 32,768 positions on pages of 16, 512 new tokens at most, 10.3 in two
+// launches (15).
 #include <algorithm>
 #include <climits>
 
@@ -24,6 +28,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kFillThreads = 256, kSegment = 1024;  // kSegment: table entries of a warp's unit
 constexpr int kMaxCluster = 8;  // the portable size
+// One launch up to here: a call for one request 12.3 us (two launches 14.3), 64 rows of 4,096 blocks, half of these entries,
+// 12.9 (15.4).  Beyond, eight CTAs would write the tables at 256 bytes a cycle at most: 8 MB of 1,024 rows take 16 us.
 constexpr int64_t kOneLaunchEntries = 1 << 19, kOneLaunchTokens = 1 << 15;
 constexpr int kSearchEntries = 4096;  // batches whose query_start_loc is searched in shared memory
 constexpr int kMaxContext = INT_MAX - 1023;  // as smla_attend_dense
